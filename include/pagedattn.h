@@ -520,6 +520,145 @@ pa_status_t pa_prefill_attention(const pa_shape_t* shape, const pa_prefill_plan_
                                  void* out, void* workspace, size_t workspace_bytes,
                                  int32_t* dev_status, void* stream);
 
+/* ---- Latent attention: one shared latent vector a token ----------------
+ *
+ * A layer with latent attention caches one row a token, shared by all its
+ * query heads: the latent c_t (512 values) followed by the rotary key r_t
+ * (64 values).  Each head's keys and values are linear maps of the latent,
+ *     k_th = [W_h c_t ; r_t],   v_th = U_h c_t,
+ * and two forms of the same attention follow.
+ *  - Absorbed (decode, drafts, short chunks).  The key map is moved to the
+ *    query, q' = [W_h^T q_nope ; q_rope], and the value map to the output:
+ *        out[r][h] = sum_t softmax_t(scale * q'[r][h] . [c_t ; r_t]) c_t,
+ *    over the cached rows themselves.  All heads read the same rows.
+ *  - Expanded (prompts).  pa_latent_gather reads the rows back, the caller
+ *    multiplies them into k = W_h c and v = U_h c, and
+ *        out[r][h] = sum_t softmax_t(scale * (q_nope . k_th + q_rope . r_t)) v_th.
+ * The projections are the caller's; scale is that of the expanded form in
+ * both, normally 1/sqrt(head_dim + 64).
+ *
+ * As in the multi-token calls, sequence b has seq_lens[b] tokens, the newest
+ * q_lens[b] of which are this step's queries, packed by sequence: query i
+ * sits at position seq_lens[b] - q_lens[b] + i and sees positions 0 .. that
+ * one.  A decode token is q_lens[b] = 1.
+ *
+ * Layouts (device, 16-bit elements of the shape's dtype):
+ *   pages       [num_pages][page_size][576], dense
+ *   block_table [batch][max_pages_per_seq], int32, dense
+ *   packed rows T = sum of q_lens, Tk = sum of seq_lens, in sequence order
+ * The lengths are those of the plan, which every call reads from the
+ * workspace the plan was uploaded to.  The calls on one plan and workspace
+ * may share it in stream order; absorbed calls in flight at once each need
+ * their own (their split partials live there).
+ */
+typedef struct {
+  int32_t batch;             /* B, >= 0 */
+  int32_t num_heads;         /* H: 1 to 128 query heads */
+  int32_t head_dim;          /* D: 64 or 128, the head's keys (without the rotary part) and
+                                values in the expanded form */
+  int32_t latent_dim;        /* 512 */
+  int32_t rope_dim;          /* 64 */
+  int32_t page_size;         /* 16, 32, 64 or 128 tokens */
+  int32_t max_pages_per_seq; /* row length of block_table */
+  int32_t num_pages;         /* pages in the pool */
+  int32_t dtype;             /* PA_DTYPE_F16 or PA_DTYPE_BF16 */
+} pa_latent_shape_t;
+
+#define PA_LATENT_ABSORBED 0 /* the plan serves pa_latent_attention */
+#define PA_LATENT_EXPANDED 1 /* the plan serves pa_latent_prefill */
+
+/* A plan: the packed row offsets, which every latent call reads, and the
+ * work list of one form.  host_blob is released by pa_latent_plan_free. */
+typedef struct {
+  pa_latent_shape_t shape;  /* the shape the plan was made for */
+  int32_t form;             /* PA_LATENT_ABSORBED or PA_LATENT_EXPANDED */
+  int32_t rows_per_tile;    /* query rows of one tile: which kernel the work was cut for */
+  int32_t num_ranges;       /* absorbed: work ranges (one CTA, or one CTA pair, each);
+                               expanded: tiles */
+  int32_t num_segments;     /* absorbed: (tile, token range) pieces over all ranges */
+  int32_t num_merges;       /* absorbed: tiles cut into several pieces */
+  int32_t num_slots;        /* absorbed: pieces that write partial results */
+  int32_t total_q;          /* T */
+  int32_t total_k;          /* Tk */
+  int32_t owns_blob;        /* 1: host_blob was allocated by the planner */
+  uint64_t plan_id;
+  size_t blob_bytes;        /* bytes pa_latent_plan_upload copies */
+  size_t workspace_bytes;   /* minimum workspace of every call with this plan */
+  void* host_blob;
+  uint64_t wait_limit_ns;   /* see pa_latent_options_t */
+} pa_latent_plan_t;
+
+/* Options of a latent plan; a zeroed struct or NULL gives the defaults. */
+typedef struct {
+  int32_t rows_per_tile;    /* absorbed: 16 or 128 (0: the planner's choice by the rows of a
+                               sequence); expanded: 0 */
+  int32_t forced_splits;    /* absorbed: cut every tile's tokens into this many pieces, as far
+                               as it has stages of 64 tokens (0: the planner's choice) */
+  uint64_t wait_limit_ns;   /* how long a warp waits on one barrier before it gives up, sets
+                               PA_DEV_TIMEOUT and leaves its rows unwritten (0: 1 s) */
+} pa_latent_options_t;
+
+/* Host: make a plan.  seq_lens_host, q_lens_host: int32[batch] with
+ * 0 <= q_lens[b] <= seq_lens[b] <= max_pages_per_seq * page_size; num_sms:
+ * SM count of the target GPU.  PA_ERR_UNSUPPORTED for dimensions not built,
+ * PA_ERR_INVALID_ARG for bad lengths or options. */
+pa_status_t pa_latent_plan(const pa_latent_shape_t* shape, const int32_t* seq_lens_host,
+                           const int32_t* q_lens_host, int32_t num_sms, int32_t form,
+                           const pa_latent_options_t* options, pa_latent_plan_t* plan_out);
+void pa_latent_plan_free(pa_latent_plan_t* plan);
+
+/* Copy the plan into the head of a device workspace of at least
+ * plan->workspace_bytes (16-byte aligned), asynchronously on stream. */
+pa_status_t pa_latent_plan_upload(const pa_latent_plan_t* plan, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Write the step's T new rows into their pages, bit for bit: row cu_q[b] + i
+ * goes to position seq_lens[b] - q_lens[b] + i of sequence b.
+ * c_new: T rows of 512 values, c_stride elements apart; r_new: T rows of 64
+ * values, r_stride elements apart (both may be slices of one projection's
+ * output).  Pointers 16-byte aligned, strides multiples of 8 elements and at
+ * least the row's width.  A row whose page index is out of range is skipped
+ * and sets PA_DEV_BAD_PAGE.  A plan of either form serves. */
+pa_status_t pa_latent_append(const pa_latent_shape_t* shape, const pa_latent_plan_t* plan,
+                             const void* c_new, int64_t c_stride, const void* r_new,
+                             int64_t r_stride, void* pages, const int32_t* block_table,
+                             const void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                             void* stream);
+
+/* Read whole sequences back: row cu_k[b] + t of rows ([Tk][576], dense)
+ * becomes the cached row of token t of sequence b, bit for bit.  A row whose
+ * page index is out of range becomes zeros and sets PA_DEV_BAD_PAGE.  A plan
+ * of either form serves. */
+pa_status_t pa_latent_gather(const pa_latent_shape_t* shape, const pa_latent_plan_t* plan,
+                             const void* pages, const int32_t* block_table, void* rows,
+                             const void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                             void* stream);
+
+/* Absorbed attention.  q: [T][H][576] dense; out: [T][H][512] dense.  fp32
+ * accumulation and softmax.  Tokens of a page whose index is out of range
+ * are left out and set PA_DEV_BAD_PAGE; a row left without any token gets
+ * zeros.  Long sequences are cut into pieces over their tokens, whose
+ * partial results a second kernel merges (one launch when nothing was cut).
+ * The same bits on every call.  The plan's form must be PA_LATENT_ABSORBED. */
+pa_status_t pa_latent_attention(const pa_latent_shape_t* shape, const pa_latent_plan_t* plan,
+                                const void* q, const void* pages, const int32_t* block_table,
+                                float scale, void* out, void* workspace, size_t workspace_bytes,
+                                int32_t* dev_status, void* stream);
+
+/* Expanded attention of prompts.  q: [T][H][D + 64] dense (the rotary part
+ * last); out: [T][H][D] dense.  k, v: Tk tokens of H heads of D values, each
+ * with its token and head stride in elements (k and v may be halves of one
+ * projection's output); k_rope: Tk rows of 64 values, kr_stride elements
+ * apart (the tail of pa_latent_gather's rows, kr_stride = 576).  Values
+ * dense within a head; pointers 16-byte aligned, strides positive multiples of 8
+ * elements.  The plan's form must be PA_LATENT_EXPANDED. */
+pa_status_t pa_latent_prefill(const pa_latent_shape_t* shape, const pa_latent_plan_t* plan,
+                              const void* q, const void* k, int64_t k_token_stride,
+                              int64_t k_head_stride, const void* k_rope, int64_t kr_stride,
+                              const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                              float scale, void* out, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, void* stream);
+
 /* ---- KV blocks: how many, which are free, and moving them ------------
  *
  * swiftLLM's engine (architecture section) profiles the number of GPU

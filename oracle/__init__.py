@@ -5,6 +5,8 @@ from .attention import (attend_one, decode_attention, decode_attention_split, ga
 from .blocks import BlockAllocatorModel, copy_blocks, profile_num_blocks
 from .fp8 import (decode_attention_fp8, dequantize_rows_e4m3, e4m3_encode, e4m3_round, e4m3_value,
                   kv_append_fp8, quantize_rows_e4m3)
+from .latent import (latent_append, latent_attention, latent_gather, latent_prefill,
+                     latent_rows)
 from .prefill import cu_lens, kv_append_tokens, prefill_attention
 from .quant import (decode_attention_q8, dequantize_rows, gather_sequence_q8, kv_append_q8,
                     quantize_rows_int8)
@@ -15,4 +17,5 @@ __all__ = ["attend_one", "decode_attention", "decode_attention_split", "gather_s
            "quantize_rows_int8", "BlockAllocatorModel", "copy_blocks", "profile_num_blocks",
            "cu_lens", "kv_append_tokens", "prefill_attention", "decode_attention_fp8",
            "dequantize_rows_e4m3", "e4m3_encode", "e4m3_round", "e4m3_value", "kv_append_fp8",
-           "quantize_rows_e4m3"]
+           "quantize_rows_e4m3", "latent_append", "latent_attention", "latent_gather",
+           "latent_prefill", "latent_rows"]

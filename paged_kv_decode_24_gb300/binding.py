@@ -80,6 +80,38 @@ class PaPrefillOptions(ctypes.Structure):
                 ("wait_limit_ns", ctypes.c_uint64)]
 
 
+class PaLatentShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages_per_seq", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class PaLatentPlan(ctypes.Structure):
+    _fields_ = [("shape", PaLatentShape), ("form", ctypes.c_int32),
+                ("rows_per_tile", ctypes.c_int32), ("num_ranges", ctypes.c_int32),
+                ("num_segments", ctypes.c_int32), ("num_merges", ctypes.c_int32),
+                ("num_slots", ctypes.c_int32), ("total_q", ctypes.c_int32),
+                ("total_k", ctypes.c_int32), ("owns_blob", ctypes.c_int32),
+                ("plan_id", ctypes.c_uint64), ("blob_bytes", ctypes.c_size_t),
+                ("workspace_bytes", ctypes.c_size_t), ("host_blob", ctypes.c_void_p),
+                ("wait_limit_ns", ctypes.c_uint64)]
+
+
+class PaLatentOptions(ctypes.Structure):
+    _fields_ = [("rows_per_tile", ctypes.c_int32), ("forced_splits", ctypes.c_int32),
+                ("wait_limit_ns", ctypes.c_uint64)]
+
+
+LATENT_DIM = 512
+LATENT_ROPE_DIM = 64
+LATENT_ROW = LATENT_DIM + LATENT_ROPE_DIM
+PA_LATENT_ABSORBED = 0
+PA_LATENT_EXPANDED = 1
+LATENT_FORMS = {"absorbed": PA_LATENT_ABSORBED, "expanded": PA_LATENT_EXPANDED}
+
+
 def plan_options(**kw) -> PaPlanOptions:
     """pa_plan_options_t from keyword fields (merge may be "split" or "combine");
     unnamed fields stay 0, their default."""
@@ -164,6 +196,26 @@ _SIGS = {
     "pa_prefill_attention": (ctypes.c_int, [ctypes.POINTER(PaShape),
                                             ctypes.POINTER(PaPrefillPlan), _P, _P, _P, _P, _P,
                                             ctypes.c_float, _P, _P, ctypes.c_size_t, _P, _P]),
+    "pa_latent_plan": (ctypes.c_int, [ctypes.POINTER(PaLatentShape), _P, _P, ctypes.c_int32,
+                                      ctypes.c_int32, ctypes.POINTER(PaLatentOptions),
+                                      ctypes.POINTER(PaLatentPlan)]),
+    "pa_latent_plan_free": (None, [ctypes.POINTER(PaLatentPlan)]),
+    "pa_latent_plan_upload": (ctypes.c_int, [ctypes.POINTER(PaLatentPlan), _P, ctypes.c_size_t,
+                                             _P]),
+    "pa_latent_append": (ctypes.c_int, [ctypes.POINTER(PaLatentShape),
+                                        ctypes.POINTER(PaLatentPlan), _P, ctypes.c_int64, _P,
+                                        ctypes.c_int64, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "pa_latent_gather": (ctypes.c_int, [ctypes.POINTER(PaLatentShape),
+                                        ctypes.POINTER(PaLatentPlan), _P, _P, _P, _P,
+                                        ctypes.c_size_t, _P, _P]),
+    "pa_latent_attention": (ctypes.c_int, [ctypes.POINTER(PaLatentShape),
+                                           ctypes.POINTER(PaLatentPlan), _P, _P, _P,
+                                           ctypes.c_float, _P, _P, ctypes.c_size_t, _P, _P]),
+    "pa_latent_prefill": (ctypes.c_int, [ctypes.POINTER(PaLatentShape),
+                                         ctypes.POINTER(PaLatentPlan), _P, _P, ctypes.c_int64,
+                                         ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64,
+                                         ctypes.c_int64, ctypes.c_float, _P, _P, ctypes.c_size_t,
+                                         _P, _P]),
     "pa_debug_gather_indices": (ctypes.c_int, [ctypes.POINTER(PaShape), _P, _P, _P, _P, _P]),
     "pa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "pa_version": (ctypes.c_char_p, []),
@@ -485,6 +537,26 @@ def gather_indices(shape, block_table, seq_lens, out_slots, status, stream=None)
         _dev_ptr(status, torch.int32, "status"), _stream(stream)))
 
 
+class Prepared:
+    """A library call with its ctypes arguments converted once.
+
+    Calling it re-issues the same call (same buffers, same stream) with no
+    per-call Python marshalling; used where host overhead would otherwise
+    dominate a short kernel.  The tensors are kept alive by the object.
+    """
+
+    def __init__(self, name, args, keep):
+        self._fn = getattr(load(), name)
+        self._name = name
+        self._args = tuple(args)
+        self._keep = keep
+
+    def __call__(self):
+        code = self._fn(*self._args)
+        if code != 0:
+            raise PagedAttnError(self._name, code, _lib)
+
+
 # --------------------------------------------------------------------------
 # several query tokens per sequence
 
@@ -559,6 +631,205 @@ def prefill(shape, plan: PrefillPlan, q, k_pages, v_pages, block_table, seq_lens
         _dev_ptr(block_table, torch.int32, "block_table"), _dev_ptr(seq_lens, torch.int32, "seq_lens"),
         ctypes.c_float(scale), _dev_ptr(out, et, "out"), _dev_ptr(workspace, torch.uint8, "workspace"),
         workspace.numel(), _dev_ptr(status, torch.int32, "status"), _stream(stream)))
+
+
+# --------------------------------------------------------------------------
+# latent attention: one shared latent vector a token
+
+def make_latent_shape(batch, num_heads, head_dim, page_size, max_pages_per_seq, num_pages,
+                      dtype="fp16") -> PaLatentShape:
+    """pa_latent_shape_t; dtype "fp16" or "bf16" (or the PA_DTYPE_* code)."""
+    code = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
+    return PaLatentShape(int(batch), int(num_heads), int(head_dim), LATENT_DIM, LATENT_ROPE_DIM,
+                         int(page_size), int(max_pages_per_seq), int(num_pages), code)
+
+
+class LatentPlan:
+    """Owner of a pa_latent_plan_t (packed row offsets and one form's work
+    list, host side).  form: "absorbed" or "expanded"."""
+
+    def __init__(self, shape: PaLatentShape, seq_lens_host, q_lens_host, num_sms: int,
+                 form: str = "absorbed", rows_per_tile: int = 0, forced_splits: int = 0,
+                 wait_limit_ns: int = 0):
+        lib = load()
+        self.shape = shape
+        self.c = PaLatentPlan()
+        lens = np.ascontiguousarray(np.asarray(seq_lens_host, dtype=np.int32))
+        qs = np.ascontiguousarray(np.asarray(q_lens_host, dtype=np.int32))
+        if lens.shape != (shape.batch,) or qs.shape != (shape.batch,):
+            raise ValueError("seq_lens and q_lens must hold one length per sequence")
+        self.options = PaLatentOptions(int(rows_per_tile), int(forced_splits), int(wait_limit_ns))
+        _check("pa_latent_plan", lib.pa_latent_plan(
+            ctypes.byref(shape), lens.ctypes.data if lens.size else None,
+            qs.ctypes.data if qs.size else None, int(num_sms), LATENT_FORMS[form],
+            ctypes.byref(self.options), ctypes.byref(self.c)))
+
+    @property
+    def workspace_bytes(self) -> int:
+        return int(self.c.workspace_bytes)
+
+    def blob(self) -> np.ndarray:
+        """The plan as int32 (host copy, for inspection and tests)."""
+        n = int(self.c.blob_bytes) // 4
+        buf = (ctypes.c_int32 * n).from_address(self.c.host_blob)
+        return np.frombuffer(buf, dtype=np.int32, count=n).copy()
+
+    def free(self):
+        if _lib is not None and getattr(self, "c", None) is not None and self.c.host_blob:
+            _lib.pa_latent_plan_free(ctypes.byref(self.c))
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+def _latent_elem(shape):
+    torch = _torch()
+    return torch.bfloat16 if shape.dtype == PA_DTYPE_BF16 else torch.float16
+
+
+def _latent_ptr(t, dtype, size, name):
+    """Address of a dense tensor of exactly this size on the current device."""
+    ptr = _dev_ptr(t, dtype, name)
+    if tuple(t.shape) != tuple(size):
+        raise ValueError(f"{name} must have shape {tuple(size)}, got {tuple(t.shape)}")
+    _on_current_device(t, name)
+    return ptr
+
+
+def _latent_rows(t, dtype, size, name):
+    """Address of a tensor of this size whose last dimension is dense, and the
+    strides of the others (in elements)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+    if tuple(t.shape) != tuple(size):
+        raise ValueError(f"{name} must have shape {tuple(size)}, got {tuple(t.shape)}")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    _on_current_device(t, name)
+    # a dimension of one entry has no stride of its own: any valid one will do
+    strides = [t.stride(i) if t.shape[i] > 1 else -(-max(t.stride(i), size[-1]) // 8) * 8
+               for i in range(t.dim() - 1)]
+    return ctypes.c_void_p(t.data_ptr()), strides
+
+
+def _on_current_device(t, name):
+    torch = _torch()
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _latent_head(shape, plan, workspace):
+    torch = _torch()
+    if workspace.dim() != 1:
+        raise ValueError("workspace must be one-dimensional")
+    ws = _latent_ptr(workspace, torch.uint8, workspace.shape, "workspace")
+    return [ctypes.byref(shape), ctypes.byref(plan.c)], [ws, ctypes.c_size_t(workspace.numel())]
+
+
+def _latent_pool(shape, pages, block_table):
+    torch = _torch()
+    return (_latent_ptr(pages, _latent_elem(shape), (shape.num_pages, shape.page_size, LATENT_ROW),
+                        "pages"),
+            _latent_ptr(block_table, torch.int32, (shape.batch, shape.max_pages_per_seq),
+                        "block_table"))
+
+
+def _latent_status(status, stream):
+    torch = _torch()
+    _on_current_device(status, "status")
+    return [_dev_ptr(status, torch.int32, "status"), _stream(stream)]
+
+
+def latent_upload(plan: LatentPlan, workspace, stream=None):
+    """pa_latent_plan_upload."""
+    torch = _torch()
+    _check("pa_latent_plan_upload", load().pa_latent_plan_upload(
+        ctypes.byref(plan.c), _latent_ptr(workspace, torch.uint8, workspace.shape, "workspace"),
+        workspace.numel(), _stream(stream)))
+
+
+def prepare_latent_append(shape, plan: LatentPlan, c_new, r_new, pages, block_table, workspace,
+                          status, stream=None) -> Prepared:
+    """latent_append as a call with its arguments converted once."""
+    et, n = _latent_elem(shape), plan.c.total_q
+    head, ws = _latent_head(shape, plan, workspace)
+    c, cs = _latent_rows(c_new, et, (n, LATENT_DIM), "c_new")
+    r, rs = _latent_rows(r_new, et, (n, LATENT_ROPE_DIM), "r_new")
+    args = [*head, c, *cs, r, *rs, *_latent_pool(shape, pages, block_table), *ws,
+            *_latent_status(status, stream)]
+    return Prepared("pa_latent_append", args, (shape, plan, c_new, r_new, pages, block_table,
+                                               workspace, status))
+
+
+def prepare_latent_gather(shape, plan: LatentPlan, pages, block_table, rows, workspace, status,
+                          stream=None) -> Prepared:
+    """latent_gather as a call with its arguments converted once."""
+    head, ws = _latent_head(shape, plan, workspace)
+    args = [*head, *_latent_pool(shape, pages, block_table),
+            _latent_ptr(rows, _latent_elem(shape), (plan.c.total_k, LATENT_ROW), "rows"), *ws,
+            *_latent_status(status, stream)]
+    return Prepared("pa_latent_gather", args, (shape, plan, pages, block_table, rows, workspace,
+                                               status))
+
+
+def prepare_latent_attention(shape, plan: LatentPlan, q, pages, block_table, scale, out, workspace,
+                             status, stream=None) -> Prepared:
+    """latent_attention as a call with its arguments converted once."""
+    et, n, h = _latent_elem(shape), plan.c.total_q, shape.num_heads
+    head, ws = _latent_head(shape, plan, workspace)
+    args = [*head, _latent_ptr(q, et, (n, h, LATENT_ROW), "q"),
+            *_latent_pool(shape, pages, block_table), ctypes.c_float(scale),
+            _latent_ptr(out, et, (n, h, LATENT_DIM), "out"), *ws, *_latent_status(status, stream)]
+    return Prepared("pa_latent_attention", args, (shape, plan, q, pages, block_table, out,
+                                                  workspace, status))
+
+
+def prepare_latent_prefill(shape, plan: LatentPlan, q, k, k_rope, v, scale, out, workspace, status,
+                           stream=None) -> Prepared:
+    """latent_prefill as a call with its arguments converted once."""
+    et, n, nk = _latent_elem(shape), plan.c.total_q, plan.c.total_k
+    h, d = shape.num_heads, shape.head_dim
+    head, ws = _latent_head(shape, plan, workspace)
+    kp, ks = _latent_rows(k, et, (nk, h, d), "k")
+    rp, rs = _latent_rows(k_rope, et, (nk, LATENT_ROPE_DIM), "k_rope")
+    vp, vs = _latent_rows(v, et, (nk, h, d), "v")
+    args = [*head, _latent_ptr(q, et, (n, h, d + LATENT_ROPE_DIM), "q"), kp, *ks, rp, *rs, vp, *vs,
+            ctypes.c_float(scale), _latent_ptr(out, et, (n, h, d), "out"), *ws,
+            *_latent_status(status, stream)]
+    return Prepared("pa_latent_prefill", args, (shape, plan, q, k, k_rope, v, out, workspace,
+                                                status))
+
+
+def latent_append(shape, plan, c_new, r_new, pages, block_table, workspace, status, stream=None):
+    """pa_latent_append: the step's new rows into their pages.  c_new [T, 512]
+    and r_new [T, 64] may be slices of wider rows."""
+    prepare_latent_append(shape, plan, c_new, r_new, pages, block_table, workspace, status,
+                          stream)()
+
+
+def latent_gather(shape, plan, pages, block_table, rows, workspace, status, stream=None):
+    """pa_latent_gather: whole sequences read back into rows [Tk, 576]."""
+    prepare_latent_gather(shape, plan, pages, block_table, rows, workspace, status, stream)()
+
+
+def latent_attention(shape, plan, q, pages, block_table, scale, out, workspace, status,
+                     stream=None):
+    """pa_latent_attention: absorbed queries [T, H, 576] over the cached rows,
+    out [T, H, 512]."""
+    prepare_latent_attention(shape, plan, q, pages, block_table, scale, out, workspace, status,
+                             stream)()
+
+
+def latent_prefill(shape, plan, q, k, k_rope, v, scale, out, workspace, status, stream=None):
+    """pa_latent_prefill: causal attention over expanded keys k [Tk, H, D] and
+    k_rope [Tk, 64] and values v [Tk, H, D] (each may be a slice of wider
+    rows); q [T, H, D + 64], out [T, H, D]."""
+    prepare_latent_prefill(shape, plan, q, k, k_rope, v, scale, out, workspace, status, stream)()
 
 
 # --------------------------------------------------------------------------
@@ -649,26 +920,6 @@ def alloc_workspace(plan: Plan, device="cuda"):
     """A uint8 device buffer of the plan's workspace size (256-byte aligned by torch)."""
     torch = _torch()
     return torch.empty(max(plan.workspace_bytes, 256), dtype=torch.uint8, device=device)
-
-
-class Prepared:
-    """A library call with its ctypes arguments converted once.
-
-    Calling it re-issues the same call (same buffers, same stream) with no
-    per-call Python marshalling; used where host overhead would otherwise
-    dominate a short kernel.  The tensors are kept alive by the object.
-    """
-
-    def __init__(self, name, args, keep):
-        self._fn = getattr(load(), name)
-        self._name = name
-        self._args = tuple(args)
-        self._keep = keep
-
-    def __call__(self):
-        code = self._fn(*self._args)
-        if code != 0:
-            raise PagedAttnError(self._name, code, _lib)
 
 
 def prepare_append(shape, k_new, v_new, k_pages, v_pages, block_table, seq_lens, status,

@@ -1,0 +1,325 @@
+// Latent attention: the entry points, and the kernels that move rows.
+#include <math.h>
+
+#include "device_common.cuh"
+#include "latent_params.h"
+#include "split_launch.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kRowChunks = kLatentRow / 8;    // 16-byte chunks of a row
+constexpr int kCChunks = kLatent / 8;         // of its latent
+
+// The sequence of packed row r: the largest b with cu[b] <= r (the last of
+// equal ones, so sequences without rows are passed over).  The warp's lanes
+// probe 32 places at once.
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int batch, int r, int lane) {
+  int lo = 0, n = batch;  // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lo + lane * step;
+    const unsigned below = __ballot_sync(kFull, lane * step < n && cu[at] <= r);
+    const int k = 31 - __clz(below | 1u);
+    n = min(step, n - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
+
+// One warp per row: a row is 72 chunks of 16 bytes, two or three per lane.
+// Both directions only move bytes, so they run at the copy bandwidth once
+// enough rows are in flight.
+template <bool APPEND>
+__global__ void __launch_bounds__(256) latent_rows_kernel(const LatentRowsParams p) {
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  const int lane = threadIdx.x & 31;
+  const int32_t* cu = p.ws + 16 + (APPEND ? 0 : p.batch + 1);
+  const int32_t* cu_q = p.ws + 16;
+  const int32_t* cu_k = cu_q + p.batch + 1;
+  if (p.ws[0] != (int)kLatentMagic || p.ws[1] != p.batch || p.ws[APPEND ? 2 : 3] != p.total) {
+    if (threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
+    return;
+  }
+  const int warps = (int)(gridDim.x * (blockDim.x >> 5));
+  for (int64_t r64 = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r64 < p.total;
+       r64 += warps) {
+    const int r = (int)r64;
+    const int b = sequence_of(cu, p.batch, r, lane);
+    int t = r - cu[b];
+    if (APPEND) t += cu_k[b + 1] - cu_k[b] - (cu_q[b + 1] - cu_q[b]);
+    const int j = t / p.page_size;
+    const int page = j < p.max_pages ? p.block_table[(int64_t)b * p.max_pages + j] : -1;
+    const bool bad = page < 0 || page >= p.num_pages;
+    if (bad && lane == 0) set_status(p.status, PA_DEV_BAD_PAGE);
+    uint4* cached = static_cast<uint4*>(p.pages) +
+                    ((int64_t)(bad ? 0 : page) * p.page_size + t % p.page_size) * kRowChunks;
+    if (APPEND) {
+      if (bad) continue;
+      const uint4* c = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.c) + r * p.c_stride);
+      const uint4* rr = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.r) + r * p.r_stride);
+      const uint4 v0 = c[lane], v1 = c[lane + 32];
+      if (lane < kRowChunks - kCChunks) cached[kCChunks + lane] = rr[lane];
+      cached[lane] = v0;
+      cached[lane + 32] = v1;
+    } else {
+      uint4* row = static_cast<uint4*>(p.rows) + (int64_t)r * kRowChunks;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int ch = lane + 32 * i;
+        if (ch < kRowChunks) row[ch] = bad ? make_uint4(0u, 0u, 0u, 0u) : cached[ch];
+      }
+    }
+  }
+}
+
+template <bool APPEND>
+cudaError_t launch_rows(const LatentRowsParams& p, cudaStream_t stream) {
+  static std::atomic<unsigned long long> configured{0};
+  const int64_t blocks = ((int64_t)p.total + 7) / 8;
+  const int grid = (int)(blocks < 152 * 8 ? blocks : 152 * 8);
+  return launch_pdl(latent_rows_kernel<APPEND>, 0, configured, p, grid, 256, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_append(const LatentRowsParams& p, cudaStream_t stream) {
+  return launch_rows<true>(p, stream);
+}
+cudaError_t launch_latent_gather(const LatentRowsParams& p, cudaStream_t stream) {
+  return launch_rows<false>(p, stream);
+}
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return p && ((uintptr_t)p % a) == 0; }
+
+pa_status_t cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return PA_OK;
+  (void)cudaGetLastError();  // clear a launch error so that later calls report their own
+  return PA_ERR_CUDA;
+}
+
+// What every call checks first: the shape, the plan against it, and the workspace.
+// form < 0: a plan of either form serves.
+pa_status_t check_latent_call(const pa_latent_shape_t* s, const pa_latent_plan_t* plan, int form,
+                              const void* workspace, size_t workspace_bytes) {
+  const pa_status_t st = check_latent_shape(s);
+  if (st != PA_OK) return st;
+  if (!plan) return PA_ERR_INVALID_ARG;
+  const pa_latent_shape_t& a = plan->shape;
+  if (a.batch != s->batch || a.num_heads != s->num_heads || a.head_dim != s->head_dim ||
+      a.latent_dim != s->latent_dim || a.rope_dim != s->rope_dim || a.page_size != s->page_size ||
+      a.max_pages_per_seq != s->max_pages_per_seq)
+    return PA_ERR_PLAN;
+  if ((plan->form != PA_LATENT_ABSORBED && plan->form != PA_LATENT_EXPANDED) ||
+      (form >= 0 && plan->form != form))
+    return PA_ERR_PLAN;
+  if (plan->form == PA_LATENT_ABSORBED ? plan->rows_per_tile != kLatentRowsMma
+                                       : plan->rows_per_tile != kLatentRowsExpanded)
+    return PA_ERR_PLAN;
+  if (plan->num_ranges < 0 || plan->num_segments < 0 || plan->num_merges < 0 ||
+      plan->num_slots < 0 || plan->total_q < 0 || plan->total_k < 0)
+    return PA_ERR_PLAN;
+  const LatentLayout l = latent_layout(s->batch, plan->form, plan->rows_per_tile, plan->num_ranges,
+                                       plan->num_segments, plan->num_merges, plan->num_slots);
+  if (plan->workspace_bytes != l.total) return PA_ERR_PLAN;
+  if (s->batch == 0) return PA_OK;
+  if (!aligned(workspace, 16)) return PA_ERR_INVALID_ARG;
+  if (workspace_bytes < plan->workspace_bytes) return PA_ERR_WORKSPACE;
+  return PA_OK;
+}
+
+bool stride_ok(int64_t stride, int width) {
+  return stride >= width && stride % 8 == 0 && stride < (int64_t)1 << 38;
+}
+
+LatentRowsParams rows_params(const pa_latent_shape_t* s, const int32_t* block_table,
+                             const void* pages, const void* workspace, int32_t* dev_status,
+                             int32_t total) {
+  LatentRowsParams p{};
+  p.pages = const_cast<void*>(pages);
+  p.block_table = block_table;
+  p.ws = static_cast<const int32_t*>(workspace);
+  p.status = dev_status;
+  p.batch = s->batch;
+  p.total = total;
+  p.max_pages = s->max_pages_per_seq;
+  p.num_pages = s->num_pages;
+  p.page_size = s->page_size;
+  return p;
+}
+
+// The pool [P][S][576] with boxes of `cols` column blocks (64 elements each)
+// by 16 tokens, 128-byte swizzle.
+bool encode_latent_map(CUtensorMap* map, const void* pages, const pa_latent_shape_t& s, int cols) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t row = kLatentRow * 2;
+  cuuint64_t dims[4] = {64, kLatentRow / 64, (cuuint64_t)s.page_size, (cuuint64_t)s.num_pages};
+  cuuint64_t strides[3] = {128, row, row * s.page_size};
+  cuuint32_t box[4] = {64, (cuuint32_t)cols, kLatentBlock, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUtensorMapDataType ty = s.dtype == PA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(map, ty, 4, const_cast<void*>(pages), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" pa_status_t pa_latent_plan_upload(const pa_latent_plan_t* plan, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+  using namespace pa;
+  if (!plan || !plan->host_blob || !aligned(workspace, 16)) return PA_ERR_INVALID_ARG;
+  if (workspace_bytes < plan->workspace_bytes || workspace_bytes < plan->blob_bytes)
+    return PA_ERR_WORKSPACE;
+  return cuda_status(cudaMemcpyAsync(workspace, plan->host_blob, plan->blob_bytes,
+                                     cudaMemcpyHostToDevice, (cudaStream_t)stream));
+}
+
+extern "C" pa_status_t pa_latent_append(const pa_latent_shape_t* shape,
+                                        const pa_latent_plan_t* plan, const void* c_new,
+                                        int64_t c_stride, const void* r_new, int64_t r_stride,
+                                        void* pages, const int32_t* block_table,
+                                        const void* workspace, size_t workspace_bytes,
+                                        int32_t* dev_status, void* stream) {
+  using namespace pa;
+  const pa_status_t st = check_latent_call(shape, plan, -1, workspace, workspace_bytes);
+  if (st != PA_OK) return st;
+  if (shape->batch == 0 || plan->total_q == 0) return PA_OK;
+  if (!aligned(c_new, 16) || !aligned(r_new, 16) || !aligned(pages, 16) ||
+      !aligned(block_table, 4) || !aligned(dev_status, 4))
+    return PA_ERR_INVALID_ARG;
+  if (!stride_ok(c_stride, kLatent) || !stride_ok(r_stride, kRope)) return PA_ERR_INVALID_ARG;
+  LatentRowsParams p = rows_params(shape, block_table, pages, workspace, dev_status, plan->total_q);
+  p.c = c_new;
+  p.r = r_new;
+  p.c_stride = c_stride;
+  p.r_stride = r_stride;
+  return cuda_status(launch_latent_append(p, (cudaStream_t)stream));
+}
+
+extern "C" pa_status_t pa_latent_gather(const pa_latent_shape_t* shape,
+                                        const pa_latent_plan_t* plan, const void* pages,
+                                        const int32_t* block_table, void* rows,
+                                        const void* workspace, size_t workspace_bytes,
+                                        int32_t* dev_status, void* stream) {
+  using namespace pa;
+  const pa_status_t st = check_latent_call(shape, plan, -1, workspace, workspace_bytes);
+  if (st != PA_OK) return st;
+  if (shape->batch == 0 || plan->total_k == 0) return PA_OK;
+  if (!aligned(rows, 16) || !aligned(pages, 16) || !aligned(block_table, 4) ||
+      !aligned(dev_status, 4))
+    return PA_ERR_INVALID_ARG;
+  LatentRowsParams p = rows_params(shape, block_table, pages, workspace, dev_status, plan->total_k);
+  p.rows = rows;
+  return cuda_status(launch_latent_gather(p, (cudaStream_t)stream));
+}
+
+extern "C" pa_status_t pa_latent_attention(const pa_latent_shape_t* shape,
+                                           const pa_latent_plan_t* plan, const void* q,
+                                           const void* pages, const int32_t* block_table,
+                                           float scale, void* out, void* workspace,
+                                           size_t workspace_bytes, int32_t* dev_status,
+                                           void* stream) {
+  using namespace pa;
+  const pa_status_t st =
+      check_latent_call(shape, plan, PA_LATENT_ABSORBED, workspace, workspace_bytes);
+  if (st != PA_OK) return st;
+  if (shape->batch == 0 || plan->total_q == 0) return PA_OK;
+  if (!aligned(q, 16) || !aligned(pages, 16) || !aligned(out, 16) || !aligned(block_table, 4) ||
+      !aligned(dev_status, 4))
+    return PA_ERR_INVALID_ARG;
+  if (!isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
+  if (plan->num_ranges < 1 || plan->num_segments < plan->num_ranges) return PA_ERR_PLAN;
+  LatentParams p{};
+  const LatentLayout l = latent_layout(shape->batch, plan->form, plan->rows_per_tile,
+                                       plan->num_ranges, plan->num_segments, plan->num_merges,
+                                       plan->num_slots);
+  char* ws = static_cast<char*>(workspace);
+  p.q = q;
+  p.out = out;
+  p.block_table = block_table;
+  p.ws = reinterpret_cast<const int32_t*>(ws);
+  p.cu_q = reinterpret_cast<const int32_t*>(ws + l.cu_q);
+  p.cu_k = reinterpret_cast<const int32_t*>(ws + l.cu_k);
+  p.ranges = reinterpret_cast<const int32_t*>(ws + l.ranges);
+  p.segments = reinterpret_cast<const LatentSegment*>(ws + l.work);
+  p.merges = reinterpret_cast<const LatentMerge*>(ws + l.merges);
+  p.part_lse = reinterpret_cast<float*>(ws + l.lse);
+  p.part_o = reinterpret_cast<float*>(ws + l.o);
+  p.status = dev_status;
+  p.wait_ns = wait_limit_or_default(plan->wait_limit_ns);
+  p.qscale = (float)((double)scale * 1.4426950408889634);  // log2(e)
+  p.batch = shape->batch;
+  p.heads = shape->num_heads;
+  p.max_pages = shape->max_pages_per_seq;
+  p.num_pages = shape->num_pages;
+  p.page_size = shape->page_size;
+  p.num_ranges = plan->num_ranges;
+  p.num_segments = plan->num_segments;
+  p.num_merges = plan->num_merges;
+  p.num_slots = plan->num_slots;
+  p.total_q = plan->total_q;
+  p.rows = plan->rows_per_tile;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (!encode_latent_map(&p.pages_map, pages, *shape, kLatentRow / 64)) return PA_ERR_CUDA;
+  cudaError_t e = launch_latent_mma(p, shape->dtype, s);
+  if (e == cudaSuccess && p.num_merges > 0) e = launch_latent_merge(p, shape->dtype, s);
+  return cuda_status(e);
+}
+
+extern "C" pa_status_t pa_latent_prefill(const pa_latent_shape_t* shape,
+                                         const pa_latent_plan_t* plan, const void* q,
+                                         const void* k, int64_t k_token_stride,
+                                         int64_t k_head_stride, const void* k_rope,
+                                         int64_t kr_stride, const void* v, int64_t v_token_stride,
+                                         int64_t v_head_stride, float scale, void* out,
+                                         void* workspace, size_t workspace_bytes,
+                                         int32_t* dev_status, void* stream) {
+  using namespace pa;
+  const pa_status_t st =
+      check_latent_call(shape, plan, PA_LATENT_EXPANDED, workspace, workspace_bytes);
+  if (st != PA_OK) return st;
+  if (shape->batch == 0 || plan->total_q == 0) return PA_OK;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(k_rope, 16) || !aligned(v, 16) ||
+      !aligned(out, 16) || !aligned(dev_status, 4))
+    return PA_ERR_INVALID_ARG;
+  if (!isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
+  if (!stride_ok(k_token_stride, 8) || !stride_ok(k_head_stride, 8) ||
+      !stride_ok(kr_stride, 8) || !stride_ok(v_token_stride, 8) || !stride_ok(v_head_stride, 8))
+    return PA_ERR_INVALID_ARG;
+  LatentPrefillParams p{};
+  const LatentLayout l = latent_layout(shape->batch, plan->form, plan->rows_per_tile,
+                                       plan->num_ranges, 0, 0, 0);
+  char* ws = static_cast<char*>(workspace);
+  p.q = q;
+  p.k = k;
+  p.k_rope = k_rope;
+  p.v = v;
+  p.out = out;
+  p.ws = reinterpret_cast<const int32_t*>(ws);
+  p.cu_q = reinterpret_cast<const int32_t*>(ws + l.cu_q);
+  p.cu_k = reinterpret_cast<const int32_t*>(ws + l.cu_k);
+  p.tiles = reinterpret_cast<const LatentTile*>(ws + l.work);
+  p.status = dev_status;
+  p.k_token = k_token_stride;
+  p.k_head = k_head_stride;
+  p.kr_token = kr_stride;
+  p.v_token = v_token_stride;
+  p.v_head = v_head_stride;
+  p.wait_ns = wait_limit_or_default(plan->wait_limit_ns);
+  p.qscale = (float)((double)scale * 1.4426950408889634);  // log2(e)
+  p.batch = shape->batch;
+  p.heads = shape->num_heads;
+  p.num_tiles = plan->num_ranges;
+  p.total_q = plan->total_q;
+  p.total_k = plan->total_k;
+  return cuda_status(
+      launch_latent_prefill(p, shape->head_dim, shape->dtype, (cudaStream_t)stream));
+}

@@ -1,0 +1,246 @@
+// Host-side planner of the latent attention calls.
+//
+// Absorbed form.  A tile is up to `rows` consecutive query rows of one
+// sequence (its tokens x heads, which lie next to each other in q and out);
+// its work is the stages of 64 tokens its last row sees.  The GPU runs one
+// CTA (or CTA pair) per SM (pair of SMs), each of which takes one range of
+// the list of all tiles' stages: the list is cut into ranges of equal work,
+// wherever that falls, so that the CTAs end together whatever the lengths.
+// A tile that a cut falls into becomes several pieces, whose partial results
+// are merged.  A piece costs its stages and a fixed part (queries in, output
+// out), kPieceStages; a cut that would leave a piece of less than
+// kMinPiece stages is moved to the tile's edge.
+//
+// Expanded form.  A tile is up to kLatentRowsExpanded query tokens of one
+// head, longest first, so that the short ones fill the tail of the grid.
+#include <stdlib.h>
+#include <string.h>
+
+#include <algorithm>
+#include <atomic>
+#include <new>
+#include <vector>
+
+#include "latent.h"
+
+namespace pa {
+
+pa_status_t check_latent_shape(const pa_latent_shape_t* s) {
+  if (!s) return PA_ERR_INVALID_ARG;
+  if (s->batch < 0 || s->num_heads <= 0 || s->head_dim <= 0 || s->latent_dim <= 0 ||
+      s->rope_dim <= 0 || s->page_size <= 0 || s->max_pages_per_seq <= 0 || s->num_pages <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (s->num_heads > 128 || (s->head_dim != 64 && s->head_dim != 128) ||
+      s->latent_dim != kLatent || s->rope_dim != kRope)
+    return PA_ERR_UNSUPPORTED;
+  if (s->page_size != 16 && s->page_size != 32 && s->page_size != 64 && s->page_size != 128)
+    return PA_ERR_UNSUPPORTED;
+  if (s->dtype != PA_DTYPE_F16 && s->dtype != PA_DTYPE_BF16) return PA_ERR_UNSUPPORTED;
+  if ((int64_t)s->max_pages_per_seq * s->page_size > INT32_MAX) return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
+namespace {
+
+std::atomic<uint64_t> g_latent_ids{1};
+
+constexpr int kPieceStages = 2;  // fixed cost of a piece, in stages
+constexpr int kMinPiece = 2;     // stages of the shortest piece a cut leaves
+constexpr int kMinRange = 4;     // stages a range is worth launching a CTA for
+
+struct Work {
+  std::vector<int32_t> ranges;
+  std::vector<LatentSegment> segments;
+  std::vector<LatentMerge> merges;
+  std::vector<LatentTile> tiles;
+  int64_t slots = 0;
+};
+
+int64_t stages_of(int64_t tokens) { return (tokens + kLatentStage - 1) / kLatentStage; }
+
+// One tile's pieces: cuts (in stages, ascending, first 0 and last the tile's
+// stages) become segments; several of them a merge.
+struct AbsorbedTile {
+  int32_t b, row0, nrows, span;  // span: tokens its last row sees
+};
+
+void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_t* qs,
+                   const std::vector<int32_t>& cu_q, int rows, int workers, int forced, Work* w) {
+  std::vector<AbsorbedTile> tiles;
+  int64_t total = 0;
+  for (int b = 0; b < s.batch; ++b) {
+    const int64_t all = (int64_t)qs[b] * s.num_heads;
+    for (int64_t r = 0; r < all; r += rows) {
+      const int n = (int)std::min<int64_t>(rows, all - r);
+      const int32_t last = (int32_t)((r + n - 1) / s.num_heads);  // query token of its last row
+      const int32_t span = lens[b] - qs[b] + last + 1;
+      tiles.push_back({b, (int32_t)r, n, span});
+      total += stages_of(span) + kPieceStages;
+    }
+  }
+  if (tiles.empty()) {
+    w->ranges.push_back(0);
+    return;
+  }
+  const int64_t by_work = std::max<int64_t>(1, total / (kMinRange + kPieceStages));
+  const int64_t ranges = std::min<int64_t>(workers, by_work);
+  // each range gets an equal share of what is left when it is opened, the
+  // last one all of it
+  int64_t quota = (total + ranges - 1) / ranges;
+  int64_t left = quota;  // of the range that is being filled
+  w->ranges.push_back(0);
+  auto close = [&] {
+    if (w->ranges.back() != (int32_t)w->segments.size())
+      w->ranges.push_back((int32_t)w->segments.size());
+    const int64_t open = std::max<int64_t>(1, ranges - ((int64_t)w->ranges.size() - 1));
+    left = quota = (total + open - 1) / open;
+  };
+  for (const AbsorbedTile& t : tiles) {
+    const int64_t n = stages_of(t.span);
+    const size_t first = w->segments.size();
+    int64_t at = 0, piece = 0;
+    while (at < n) {
+      int64_t take = n - at;
+      if (forced > 0) {
+        const int64_t parts = std::min<int64_t>(forced, n);
+        ++piece;
+        take = n * piece / parts - at;
+        close();
+      } else if (take + kPieceStages > left) {
+        if (left < kMinPiece + kPieceStages && left < quota) {  // nothing worth starting
+          close();
+          continue;
+        }
+        take = std::min<int64_t>(take, std::max<int64_t>(left - kPieceStages, kMinPiece));
+        if (n - at - take < kMinPiece) take = n - at;
+      }
+      const int32_t tok1 = (int32_t)std::min<int64_t>((at + take) * kLatentStage, t.span);
+      w->segments.push_back({t.b, t.row0, t.nrows, (int32_t)(at * kLatentStage), tok1, -1, 0, 0});
+      at += take;
+      left -= take + kPieceStages;
+      total -= take + (at == n ? kPieceStages : 0);
+      if (forced == 0 && left <= 0) close();
+    }
+    const size_t pieces = w->segments.size() - first;
+    if (pieces > 1) {
+      w->merges.push_back({(int32_t)w->slots, (int32_t)pieces,
+                           (int32_t)((int64_t)cu_q[(size_t)t.b] * s.num_heads + t.row0), t.nrows});
+      for (size_t i = first; i < w->segments.size(); ++i)
+        w->segments[i].slot = (int32_t)w->slots++;
+    }
+  }
+  if (w->ranges.back() != (int32_t)w->segments.size())
+    w->ranges.push_back((int32_t)w->segments.size());
+}
+
+void expanded_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_t* qs, int rows,
+                   Work* w) {
+  struct Sized {
+    LatentTile t;
+    int32_t span;
+  };
+  std::vector<Sized> all;
+  for (int b = 0; b < s.batch; ++b)
+    for (int32_t t0 = 0; t0 < qs[b]; t0 += rows) {
+      const int32_t n = std::min(rows, qs[b] - t0);
+      const int32_t span = lens[b] - qs[b] + t0 + n;
+      for (int h = 0; h < s.num_heads; ++h) all.push_back({{b, h, t0, n}, span});
+    }
+  std::stable_sort(all.begin(), all.end(), [](const Sized& x, const Sized& y) {
+    return x.span != y.span ? x.span > y.span : x.t.ntok > y.t.ntok;
+  });
+  for (const Sized& x : all) w->tiles.push_back(x.t);
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" pa_status_t pa_latent_plan(const pa_latent_shape_t* shape, const int32_t* seq_lens_host,
+                                      const int32_t* q_lens_host, int32_t num_sms, int32_t form,
+                                      const pa_latent_options_t* options,
+                                      pa_latent_plan_t* plan_out) try {
+  using namespace pa;
+  if (!plan_out) return PA_ERR_INVALID_ARG;
+  memset(plan_out, 0, sizeof(*plan_out));
+  const pa_status_t st = check_latent_shape(shape);
+  if (st != PA_OK) return st;
+  const pa_latent_options_t o = options ? *options : pa_latent_options_t{};
+  const bool absorbed = form == PA_LATENT_ABSORBED;
+  if ((!absorbed && form != PA_LATENT_EXPANDED) || num_sms <= 0 || o.forced_splits < 0 ||
+      o.rows_per_tile < 0)
+    return PA_ERR_INVALID_ARG;
+  if (absorbed ? (o.rows_per_tile != 0 && o.rows_per_tile != kLatentRowsMma)
+               : (o.rows_per_tile != 0 || o.forced_splits != 0))
+    return PA_ERR_INVALID_ARG;
+  const int B = shape->batch;
+  if (B > 0 && (!seq_lens_host || !q_lens_host)) return PA_ERR_INVALID_ARG;
+
+  std::vector<int32_t> cu_q((size_t)B + 1, 0), cu_k((size_t)B + 1, 0);
+  for (int b = 0; b < B; ++b) {
+    const int32_t len = seq_lens_host[b], q = q_lens_host[b];
+    if (q < 0 || q > len || (int64_t)len > (int64_t)shape->max_pages_per_seq * shape->page_size)
+      return PA_ERR_INVALID_ARG;
+    // the packed rows are indexed with 32 bits, heads included
+    if (((int64_t)cu_q[(size_t)b] + q) * shape->num_heads > INT32_MAX ||
+        (int64_t)cu_k[(size_t)b] + len > INT32_MAX)
+      return PA_ERR_INVALID_ARG;
+    cu_q[(size_t)b + 1] = cu_q[(size_t)b] + q;
+    cu_k[(size_t)b + 1] = cu_k[(size_t)b] + len;
+  }
+  Work w;
+  const int rows = absorbed ? kLatentRowsMma : kLatentRowsExpanded;
+  if (absorbed)
+    absorbed_work(*shape, seq_lens_host, q_lens_host, cu_q, rows, num_sms, o.forced_splits, &w);
+  else
+    expanded_work(*shape, seq_lens_host, q_lens_host, rows, &w);
+  const size_t ranges = absorbed ? w.ranges.size() - 1 : w.tiles.size();
+  if (ranges > (size_t)INT32_MAX || w.segments.size() > (size_t)INT32_MAX ||
+      w.slots > INT32_MAX / rows)
+    return PA_ERR_INVALID_ARG;
+  const LatentLayout lay = latent_layout(B, form, rows, (int)ranges, (int)w.segments.size(),
+                                         (int)w.merges.size(), (int)w.slots);
+  char* blob = (char*)calloc(1, lay.blob_bytes);
+  if (!blob) return PA_ERR_NO_MEMORY;
+  const uint64_t id = g_latent_ids.fetch_add(1);
+  const int32_t header[16] = {(int32_t)kLatentMagic, B, cu_q[(size_t)B], cu_k[(size_t)B],
+                              (int32_t)(id & 0xffffffffu), (int32_t)(id >> 32), form, rows,
+                              (int32_t)ranges, (int32_t)w.segments.size(),
+                              (int32_t)w.merges.size(), (int32_t)w.slots};
+  memcpy(blob, header, sizeof(header));
+  memcpy(blob + lay.cu_q, cu_q.data(), 4 * cu_q.size());
+  memcpy(blob + lay.cu_k, cu_k.data(), 4 * cu_k.size());
+  if (absorbed) {
+    memcpy(blob + lay.ranges, w.ranges.data(), 4 * w.ranges.size());
+    if (!w.segments.empty())
+      memcpy(blob + lay.work, w.segments.data(), sizeof(LatentSegment) * w.segments.size());
+    if (!w.merges.empty())
+      memcpy(blob + lay.merges, w.merges.data(), sizeof(LatentMerge) * w.merges.size());
+  } else if (!w.tiles.empty()) {
+    memcpy(blob + lay.work, w.tiles.data(), sizeof(LatentTile) * w.tiles.size());
+  }
+  plan_out->shape = *shape;
+  plan_out->form = form;
+  plan_out->rows_per_tile = rows;
+  plan_out->num_ranges = (int32_t)ranges;
+  plan_out->num_segments = (int32_t)w.segments.size();
+  plan_out->num_merges = (int32_t)w.merges.size();
+  plan_out->num_slots = (int32_t)w.slots;
+  plan_out->total_q = cu_q[(size_t)B];
+  plan_out->total_k = cu_k[(size_t)B];
+  plan_out->owns_blob = 1;
+  plan_out->plan_id = id;
+  plan_out->blob_bytes = lay.blob_bytes;
+  plan_out->workspace_bytes = lay.total;
+  plan_out->host_blob = blob;
+  plan_out->wait_limit_ns = o.wait_limit_ns;
+  return PA_OK;
+} catch (const std::bad_alloc&) {
+  return PA_ERR_NO_MEMORY;
+}
+
+extern "C" void pa_latent_plan_free(pa_latent_plan_t* plan) {
+  if (!plan) return;
+  if (plan->owns_blob && plan->host_blob) free(plan->host_blob);
+  plan->host_blob = nullptr;
+  plan->blob_bytes = 0;
+}

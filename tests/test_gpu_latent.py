@@ -1,0 +1,379 @@
+"""Latent attention on the GPU against the float64 oracle: append and gather
+bit for bit, the absorbed and the expanded attention within the tolerance
+derived in tests/latent.py, and the four as one run."""
+
+from __future__ import annotations
+
+import zlib
+
+import numpy as np
+import pytest
+
+import oracle
+from paged_kv_decode_24_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from tests.latent import DT, LATENT, ROW, Case, Device, assert_latent_close, f64  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(lib):
+    return lib
+
+
+def seed_of(*x):
+    return zlib.crc32(str(x).encode())
+
+
+def bits(t):
+    return t.cpu().view(torch.int16)
+
+
+# ---- append and gather
+
+ROWS_CASES = [([1], [1]), ([16, 17, 1, 300], [16, 3, 1, 0]), ([0, 5, 0, 129, 64], [0, 5, 0, 64, 1]),
+              ([33] * 70, [1] * 70), ([1000, 2049], [1000, 1025])]
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("case", ROWS_CASES, ids=lambda c: f"B{len(c[0])}_T{sum(c[1])}")
+def test_append_and_gather_are_bit_exact(case, page):
+    c = Case(*case, heads=1, page=page, dtype="bf16", seed=seed_of(case, page))
+    d = Device(c)
+    d.append()
+    rows = d.gather()
+    assert d.done() == 0
+    table = c.table.numpy()
+    want = oracle.latent_append(c.pages.view(torch.int16).numpy(), c.c_new.view(torch.int16).numpy(),
+                                c.r_new.view(torch.int16).numpy(), table, c.lens, c.qs)
+    assert np.array_equal(bits(d.pages).numpy(), want)     # every other row as it was
+    assert np.array_equal(bits(rows).numpy(), oracle.latent_gather(want, table, c.lens))
+
+
+def test_append_takes_slices_of_a_wider_projection():
+    c = Case([40, 9], [7, 9], heads=1, seed=3)
+    d = Device(c)
+    wide = torch.randn(c.T, 1000, device="cuda").half()
+    d.c_new, d.r_new = wide[:, 8:8 + LATENT], wide[:, 904:904 + 64]
+    d.append()
+    assert d.done() == 0
+    want = oracle.latent_append(f64(c.pages), f64(d.c_new.cpu()), f64(d.r_new.cpu()),
+                                c.table.numpy(), c.lens, c.qs)
+    assert np.array_equal(f64(d.pages.cpu()), want)
+
+
+def test_rows_of_a_bad_page_are_skipped_and_flagged():
+    c = Case([50, 20], [50, 4], heads=1, seed=4)
+    c.table[0, 1] = c.num_pages
+    d = Device(c)
+    d.append()
+    assert d.done() == binding.PA_DEV_BAD_PAGE
+    d.status.zero_()
+    rows = d.gather().cpu()
+    assert d.done() == binding.PA_DEV_BAD_PAGE
+    assert torch.all(rows[16:32] == 0) and torch.equal(rows[:16, :LATENT], c.c_new[:16])
+    assert torch.equal(rows[32:50, :LATENT], c.c_new[32:50])
+
+
+# ---- absorbed attention
+
+ABSORBED = [
+    # lens, q_lens, heads, page
+    ([1], [1], 1, 16),
+    ([1, 2, 15, 16, 17, 63, 64, 65], [1] * 8, 16, 16),
+    ([300, 0, 129, 1000], [1, 0, 1, 1], 16, 32),
+    ([100, 64], [5, 3], 3, 64),                   # rows of several tokens in a tile, 9 and 15 rows
+    ([70, 513], [7, 2], 20, 128),                 # tiles that begin inside a token
+    ([257, 31], [1, 31], 128, 64),
+    ([2000, 333], [1, 4], 40, 16),
+]
+
+
+@pytest.mark.parametrize("splits", [0, 3])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("case", ABSORBED, ids=lambda c: f"L{c[0][:3]}_q{c[1][:2]}_H{c[2]}_S{c[3]}")
+def test_absorbed_parity(case, dtype, splits):
+    lens, qs, heads, page = case
+    c = Case(lens, qs, heads=heads, page=page, dtype=dtype, seed=seed_of(case), poison=True)
+    d = Device(c, forced_splits=splits)
+    out = d.attention()
+    assert d.done() == 0
+    want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), lens, qs, c.scale)
+    assert_latent_close(out.double().cpu().numpy(), want, max(lens), dtype, str(case))
+
+
+def test_absorbed_planner_splits_and_reruns_give_the_same_bits():
+    c = Case([20000, 777], [1, 1], heads=16, page=64, dtype="bf16", seed=8)
+    d = Device(c)
+    assert d.plan.c.num_merges >= 1
+    a, b = d.attention(), d.attention()
+    assert d.done() == 0
+    assert torch.equal(bits(a), bits(b))
+    want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), c.lens, c.qs, c.scale)
+    assert_latent_close(a.double().cpu().numpy(), want, 20000, "bf16")
+
+
+@pytest.mark.parametrize("splits", [0, 2])
+def test_absorbed_bad_pages_are_left_out(splits):
+    """One page of a sequence, every page of another (its rows get zeros)."""
+    c = Case([200, 40, 90], [2, 1, 1], heads=5, page=16, seed=9)
+    c.table[0, 3] = -1
+    c.table[1, :3] = c.num_pages + 9
+    d = Device(c, forced_splits=splits)
+    out = d.attention()
+    assert d.done() == binding.PA_DEV_BAD_PAGE
+    want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), c.lens, c.qs, c.scale,
+                                   bad_pages=[(0, 3), (1, 0), (1, 1), (1, 2)])
+    assert_latent_close(out.double().cpu().numpy(), want, 200, "fp16")
+    assert torch.all(out[2] == 0)
+
+
+@pytest.mark.parametrize("scale", [1e-4, 1.0])
+def test_absorbed_scale_extremes(scale):
+    """Near-uniform weights, and weights that are almost one-hot with scores of
+    hundreds (the running maximum moves)."""
+    c = Case([1200], [1], heads=16, page=16, seed=10, scale=scale)
+    d = Device(c)
+    out = d.attention()
+    assert d.done() == 0
+    want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), c.lens, c.qs, scale)
+    assert_latent_close(out.double().cpu().numpy(), want, 1200, "fp16")
+
+
+def test_absorbed_offsets_past_32_bits():
+    """Pages beyond 2^31 elements (and 4 GB) of the pool."""
+    pages = 2**32 // (16 * ROW * 2) + 40000       # 5 GB
+    c = Case([100, 300], [3, 1], heads=16, seed=11)
+    base = pages - c.num_pages
+    d = Device(c)
+    big = torch.empty(pages, 16, ROW, dtype=torch.float16, device="cuda")
+    big[base:] = d.pages
+    assert base * 16 * ROW > 2**31
+    d.pages, d.shape.num_pages = big, pages
+    d.table = torch.where(d.table >= 0, d.table + base, d.table)
+    d.append()
+    rows, out = d.gather(), d.attention()
+    assert d.done() == 0
+    after = oracle.latent_append(f64(c.pages), f64(c.c_new), f64(c.r_new), c.table.numpy(), c.lens,
+                                 c.qs)
+    assert np.array_equal(f64(rows.cpu()), oracle.latent_gather(after, c.table.numpy(), c.lens))
+    want = oracle.latent_attention(f64(c.q), after, c.table.numpy(), c.lens, c.qs, c.scale)
+    assert_latent_close(out.double().cpu().numpy(), want, 300, "fp16")
+
+
+# ---- expanded attention
+
+EXPANDED = [
+    # lens, q_lens, heads, head_dim
+    ([1], [1], 1, 64),
+    ([1, 2, 63, 64, 65, 0, 130], [1, 2, 63, 64, 65, 0, 130], 3, 128),
+    ([300, 129, 1000], [64, 129, 1], 5, 64),
+    ([513, 700], [513, 257], 2, 128),
+    ([260, 300], [255, 256], 4, 128),
+    ([1500], [511], 3, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("case", EXPANDED, ids=lambda c: f"L{c[0][:3]}_q{c[1][:2]}_H{c[2]}_D{c[3]}")
+def test_expanded_parity(case, dtype):
+    lens, qs, heads, hd = case
+    c = Case(lens, qs, heads=heads, head_dim=hd, dtype=dtype, seed=seed_of(case))
+    d = Device(c, form="expanded")
+    out = d.prefill()
+    assert d.done() == 0
+    want = oracle.latent_prefill(f64(c.qx), f64(c.k), f64(c.rows[:, LATENT:]), f64(c.v), lens, qs,
+                                 c.scale)
+    assert_latent_close(out.double().cpu().numpy(), want, max(lens), dtype, str(case))
+
+
+def test_expanded_takes_other_strides():
+    """Head-major keys, dense values, a dense rotary key."""
+    c = Case([90, 200], [90, 33], heads=3, head_dim=64, seed=12)
+    d = Device(c, form="expanded")
+    d.k = d.k.transpose(0, 1).contiguous().transpose(0, 1)
+    d.v = d.v.contiguous()
+    d.k_rope = d.k_rope.contiguous()
+    out = d.prefill()
+    assert d.done() == 0
+    want = oracle.latent_prefill(f64(c.qx), f64(c.k), f64(c.rows[:, LATENT:]), f64(c.v), c.lens,
+                                 c.qs, c.scale)
+    assert_latent_close(out.double().cpu().numpy(), want, 200, "fp16")
+
+
+def test_expanded_other_sequences_never_leak():
+    """The neighbours of a sequence in the packed rows hold NaN and infinity:
+    its own output stays finite and right."""
+    c = Case([100, 77, 100], [100, 50, 100], heads=2, head_dim=128, seed=13)
+    for x in (c.kv, c.rows):
+        x[:100] = float("nan")
+        x[177:] = float("inf")
+    d = Device(c, form="expanded")
+    out = d.prefill()[100:150]
+    assert d.done() == 0
+    s = slice(100, 177)
+    want = oracle.latent_prefill(f64(c.qx[100:150]), f64(c.k[s]), f64(c.rows[s, LATENT:]),
+                                 f64(c.v[s]), [77], [50], c.scale)
+    assert_latent_close(out.double().cpu().numpy(), want, 77, "fp16")
+
+
+@pytest.mark.parametrize("scale", [1e-4, 2.0])
+def test_expanded_scale_extremes(scale):
+    c = Case([700], [700], heads=2, seed=14, scale=scale)
+    d = Device(c, form="expanded")
+    out = d.prefill()
+    assert d.done() == 0
+    want = oracle.latent_prefill(f64(c.qx), f64(c.k), f64(c.rows[:, LATENT:]), f64(c.v), c.lens, c.qs,
+                                 scale)
+    assert_latent_close(out.double().cpu().numpy(), want, 700, "fp16")
+
+
+# ---- together
+
+def test_the_two_forms_agree_over_one_cache():
+    """append -> gather -> expand -> prefill against absorbed queries over the
+    same cache, with W (keys) and U (values) of each head: the two forms are the
+    same attention."""
+    lens, qs, H, D = [150, 75, 300], [150, 20, 64], 4, 128
+    c = Case(lens, qs, heads=H, head_dim=D, page=32, seed=15)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    W = torch.randn(H, D, LATENT, generator=g, device="cuda") * LATENT**-0.5
+    U = torch.randn(H, D, LATENT, generator=g, device="cuda") * LATENT**-0.5
+    e = Device(c, form="expanded")
+    e.append()
+    rows = e.gather()
+    c64 = rows[:, :LATENT].double()
+    e.k = torch.einsum("tc,hdc->thd", c64, W.double()).half()
+    e.v = torch.einsum("tc,hdc->thd", c64, U.double()).half()
+    e.k_rope = rows[:, LATENT:]
+    x = e.prefill()
+    assert e.done() == 0
+    a = Device(c)
+    a.pages = e.pages
+    a.q = torch.cat([torch.einsum("thd,hdc->thc", e.qx[..., :D].double(), W.double()).half(),
+                     e.qx[..., D:]], 2)
+    lat = a.attention()
+    assert a.done() == 0
+    y = torch.einsum("thc,hdc->thd", lat.double(), U.double())
+    # each form against its own 64-bit result above; here both against the other:
+    # k, v, q' and the latent output are each rounded once to fp16 (2^-11), which
+    # moves a score of size ~6 by a few 2^-11 of it
+    rel = float((x.double() - y).norm() / y.norm())
+    assert rel < 8 * 2.0**-11, rel
+
+
+def test_decode_steps_over_a_growing_cache():
+    """Prompt by the expanded form, then three decode steps: append one token,
+    attend; each step's plan goes into the same workspace."""
+    H, page = 16, 16
+    final = [40, 131]
+    c = Case(final, [1, 1], heads=H, page=page, seed=16, dtype="bf16")
+    pool = c.pages.clone()
+    ws = torch.empty(8 << 20, dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dev_pages, table = pool.cuda(), c.table.cuda()
+    for step in range(3):
+        lens = [n - 2 + step for n in final]
+        s = Case(final, [1, 1], heads=H, page=page, seed=100 + step, dtype="bf16")
+        plan = binding.LatentPlan(c.shape(), lens, [1, 1], 152)
+        binding.latent_upload(plan, ws)
+        cn, rn, q = s.c_new.cuda(), s.r_new.cuda(), s.q.cuda()
+        out = torch.empty(2, H, LATENT, dtype=DT["bf16"], device="cuda")
+        binding.latent_append(c.shape(), plan, cn, rn, dev_pages, table, ws, status)
+        binding.latent_attention(c.shape(), plan, q, dev_pages, table, c.scale, out, ws, status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        pool = oracle.latent_append(f64(pool) if step == 0 else pool, f64(s.c_new), f64(s.r_new),
+                                    c.table.numpy(), lens, [1, 1])
+        want = oracle.latent_attention(f64(s.q), pool, c.table.numpy(), lens, [1, 1], c.scale)
+        assert_latent_close(out.double().cpu().numpy(), want, 131, "bf16", f"step {step}")
+
+
+def test_captured_step_replays_and_follows_a_new_upload():
+    """append + attention in a CUDA graph; between replays a plan of the same
+    structure is uploaded (longer sequences), two graphs on workspaces of their
+    own run on two streams at once."""
+    lens0, lens1 = [120, 333], [125, 340]
+    c = Case([128, 352], [1, 1], heads=16, page=16, seed=17)
+    graphs = []
+    for _ in range(2):
+        d = Device(c, forced_splits=2)
+        plans = [binding.LatentPlan(d.shape, x, [1, 1], 152, forced_splits=2) for x in (lens0, lens1)]
+        assert plans[0].c.blob_bytes == plans[1].c.blob_bytes
+        d.plan = plans[0]
+        d.out = torch.empty(2, 16, LATENT, dtype=DT["fp16"], device="cuda")
+        binding.latent_upload(plans[0], d.ws)
+        d.append()
+        d.attention(d.out)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            d.append()
+            d.attention(d.out)
+        graphs.append((g, d, plans, torch.cuda.Stream()))
+    pool = f64(c.pages)
+    pool = oracle.latent_append(pool, f64(c.c_new), f64(c.r_new), c.table.numpy(), lens0, [1, 1])
+    for i, lens in enumerate((lens0, lens1)):
+        pool = oracle.latent_append(pool, f64(c.c_new), f64(c.r_new), c.table.numpy(), lens, [1, 1])
+        want = oracle.latent_attention(f64(c.q), pool, c.table.numpy(), lens, [1, 1], c.scale)
+        for g, d, plans, st in graphs:
+            binding.latent_upload(plans[i], d.ws)
+        torch.cuda.synchronize()
+        for g, d, plans, st in graphs:
+            with torch.cuda.stream(st):
+                for _ in range(4):
+                    g.replay()
+        for g, d, plans, st in graphs:
+            assert d.done() == 0
+            assert_latent_close(d.out.double().cpu().numpy(), want, 352, "fp16")
+
+
+def test_calls_on_another_stream():
+    c = Case([500, 90], [1, 1], heads=16, seed=18)
+    d = Device(c)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        a = d.attention()
+    b = d.attention(stream=s)
+    assert d.done() == 0
+    assert torch.equal(bits(a), bits(b))
+
+
+def test_workspace_of_another_plan_is_flagged():
+    c = Case([100, 50], [1, 1], heads=16, seed=19)
+    d = Device(c)
+    other = Device(Case([100, 50, 60], [1, 1, 1], heads=16, seed=20))
+    d.ws = torch.cat([other.ws, other.ws])
+    out = d.attention()
+    assert d.done() == binding.PA_DEV_PLAN_MISMATCH
+    assert torch.all(torch.isnan(out))
+    d.status.zero_()
+    d.append()
+    assert d.done() == binding.PA_DEV_PLAN_MISMATCH
+    assert torch.equal(d.pages.cpu(), c.pages)
+
+
+@pytest.mark.parametrize("splits", [1, 4])
+def test_waits_that_run_out_are_reported(splits):
+    """One nanosecond per wait: rows are left as they were or right, the status
+    says so, and the next call with the default limit is right."""
+    c = Case([900, 1500, 30], [1, 1, 1], heads=16, seed=21)
+    d = Device(c, forced_splits=splits, wait_limit_ns=1)
+    out = d.attention()
+    assert d.done() == binding.PA_DEV_TIMEOUT
+    got = out.double().cpu().numpy()
+    rows = np.isnan(got).all(axis=-1)
+    assert np.array_equal(rows, np.isnan(got).any(axis=-1)) and rows.any()
+    want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), c.lens, c.qs, c.scale)
+    keep = tuple(x[~rows] for x in want)
+    assert_latent_close(got[~rows], keep, 1500, "fp16")
+    d2 = Device(c, forced_splits=splits)
+    out = d2.attention()
+    assert d2.done() == 0
+    assert_latent_close(out.double().cpu().numpy(), want, 1500, "fp16")
