@@ -15,7 +15,7 @@ constexpr int kLatentRow = kLatent + kRope;   // elements of a cached row
 constexpr int kLatentStage = 64;              // tokens of a stage: pieces are cut at its multiples
 constexpr int kLatentBlock = 16;              // tokens of one page copy (divides every page size)
 constexpr int kLatentRowsMma = 16;            // rows of a tile: the mma.sync kernel
-constexpr int kLatentRowsExpanded = 64;       // query tokens of an expanded tile
+constexpr int kLatentRowsExpanded = 256;      // query tokens of an expanded tile
 constexpr uint32_t kLatentMagic = 0x564b414cu;  // "LAKV"
 
 // A piece of the absorbed work list: rows row0 .. row0 + nrows - 1 of

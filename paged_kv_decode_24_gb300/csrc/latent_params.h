@@ -67,6 +67,7 @@ struct LatentPrefillParams {
   uint64_t wait_ns;
   float qscale;
   int32_t batch, heads, num_tiles, total_q, total_k;
+  bool k_token_major, v_token_major;  // set by the launcher: tokens are further apart than heads
 };
 
 cudaError_t launch_latent_prefill(const LatentPrefillParams& p, int head_dim, int dtype,

@@ -1,196 +1,491 @@
-// Expanded latent attention of prompts (mma.sync): keys of D + 64 dims whose
-// last 64 are shared by the heads, values of D dims, causal.
+// Expanded latent attention of prompts on tcgen05: keys of D + 64 dims whose
+// last 64 (the rotary part) are shared by the heads, values of D dims, causal.
 //
-// A CTA owns 64 query tokens of one head, 16 per warp, with q in registers.
-// Stages of 64 tokens' keys and values are staged in shared memory; scores,
-// online softmax and output stay in registers.
+//   s[i][t] = q_i . [k_th ; r_t],  o_i = sum_t 2^(s qscale - m_i) v_th / sum_t 2^(s qscale - m_i)
+//
+// The work is 2 (2D + 64) operations per visible pair and head over data that
+// the tiles share through L2: it is bound by the tensor cores, then by the
+// exponentials.  A CTA (one per SM) owns 256 query tokens of one head as two
+// tiles of 128 rows, so that the softmax of one tile runs while the tensor
+// cores work on the other.
+//   warps 0-3: softmax and output of tile 0 (thread = row = TMEM lane)
+//   warps 4-7: the same of tile 1
+//   warp 8:    issues the MMAs
+//   warp 9:    copies q, then stages of 128 tokens' keys and values
+// TMEM (512 columns): S0, S1 (128 each), O0, O1 (128 each).  The weights
+// P_t take S_t's place, two 16-bit weights a column: the A operand of P V.
+// Shared memory (128-byte swizzle): q 2 x [DK/64][128 rows][128 B], two key
+// stages [DK/64][128 tokens][128 B], one value stage [D/64][128 tokens][128 B].
+//
+// Per stage j and tile t:
+//   S_t(j) = q_t K(j)^T             DK/16 MMAs, M = N = 128
+//   softmax in registers, P_t(j) over S_t(j)
+//   O_t += P_t(j) V(j)              8 MMAs, N = D
+//   S_t(j+1) once P V(j) of the tile is done, which reads the same columns
+// in the order PV_0, S_0, PV_1, S_1.  The weights are rounded to the element
+// type once: the product's time is what a second part of them would cost
+// again, and the error stays below that of rounding the result.  For fp16
+// they carry a factor 2^7, so that small weights stay normal numbers.  The
+// running maximum is raised only when a row's grows by more than 2^8
+// (p <= 2^8, 2^15 with the factor), which keeps O's rescaling rare.
+//
+// Value rows past the tile's last visible token (a neighbour's rows, which
+// may hold anything) become zeros before P V reads them.  Every wait is
+// bounded; a CTA that gave up writes nothing.
 #include <math.h>
 
-#include "decode_tc.cuh"
-#include "device_common.cuh"
-#include "elem.cuh"
 #include "latent_params.h"
+#include "prefill_tc5.cuh"
 #include "split_launch.cuh"
 
 namespace pa {
 
+namespace tc5 {
+
+// 32 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void ld32(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+}  // namespace tc5
+
 namespace {
 
-constexpr int kTok = 64;
+constexpr int kRows = 128;                  // query rows of a tile (TMEM lanes)
+constexpr int kTokens = 128;                // tokens of a stage
+constexpr int kPrefillThreads = 10 * 32;
+constexpr float kLazyLog2 = 8.f;            // the maximum is raised when it grows by more than 2^8
+static_assert(kLatentRowsExpanded == 2 * kRows, "a CTA has two tiles");
 
 template <int D>
-struct PrefillLayout1 {
-  static constexpr int KP = (D + kRope) * 2 + 16;  // bytes per key row (padded: conflict-free ldmatrix)
-  static constexpr int VP = D * 2 + 16;
-  static constexpr int K = 0;
-  static constexpr int V = K + kTok * KP;
-  static constexpr int BYTES = V + kTok * VP;
+struct XLayout {
+  static constexpr int DK = D + kRope;
+  static constexpr int BOX = kTokens * 128;             // 16 KB: 64 dims of 128 rows
+  static constexpr int QTILE = DK / 64 * BOX;
+  static constexpr int KSTAGE = DK / 64 * BOX;
+  static constexpr int VSTAGE = D / 64 * BOX;
+  static constexpr int NK = 2;
+  static constexpr int Q = 0;
+  static constexpr int K = Q + 2 * QTILE;
+  static constexpr int V = K + NK * KSTAGE;
+  static constexpr int BARS = V + VSTAGE;
+  // mbarriers
+  static constexpr int Q_FULL = BARS;
+  static constexpr int K_FULL = Q_FULL + 8;             // NK
+  static constexpr int K_FREE = K_FULL + 8 * NK;        // NK
+  static constexpr int V_FULL = K_FREE + 8 * NK;
+  static constexpr int V_FREE = V_FULL + 8;
+  static constexpr int S_DONE = V_FREE + 8;             // one per tile, as the next two
+  static constexpr int P_READY = S_DONE + 16;
+  static constexpr int PV_DONE = P_READY + 16;
+  static constexpr int DRAIN = PV_DONE + 16;
+  static constexpr int TMEM_SLOT = DRAIN + 8;
+  static constexpr int FLAG = TMEM_SLOT + 8;
+  static constexpr int BYTES = FLAG + 8 + 1024;
+};
+static_assert(XLayout<128>::BYTES <= kMaxCtaSmem, "stages do not fit in shared memory");
+
+struct XMaps {
+  CUtensorMap q, k, kr, v;
 };
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                            int c2, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(128)
-    latent_prefill_kernel(const __grid_constant__ LatentPrefillParams p) {
-  using L = PrefillLayout1<D>;
-  constexpr int DK = D + kRope;
-  extern __shared__ __align__(16) unsigned char sm[];
-  const uint32_t sbase = smem_u32(sm);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+__global__ void __launch_bounds__(kPrefillThreads, 1)
+    latent_prefill_kernel(const __grid_constant__ LatentPrefillParams p,
+                          const __grid_constant__ XMaps maps) {
+  using L = XLayout<D>;
+  constexpr int DK = L::DK;
+  extern __shared__ unsigned char smem_dyn[];
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(base);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* flag = reinterpret_cast<int*>(base + L::FLAG);
+
+  if (threadIdx.x == 0) {
+    *flag = 0;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.q)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.kr)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
+    mbar_init(sb + L::Q_FULL, 1);
+    for (int s = 0; s < L::NK; ++s) {
+      mbar_init(sb + L::K_FULL + 8 * s, 1);
+      mbar_init(sb + L::K_FREE + 8 * s, 1);
+    }
+    mbar_init(sb + L::V_FULL, 1);
+    mbar_init(sb + L::V_FREE, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(sb + L::S_DONE + 8 * t, 1);
+      mbar_init(sb + L::P_READY + 8 * t, 4);
+      mbar_init(sb + L::PV_DONE + 8 * t, 1);
+    }
+    mbar_init(sb + L::DRAIN, 1);
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     sb + L::TMEM_SLOT)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc5::fence_before();
+  __syncthreads();
+  tc5::fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + L::TMEM_SLOT);
   pdl_launch_dependents();
   pdl_wait_primary();
+
   const int4 h0 = reinterpret_cast<const int4*>(p.ws)[0];
-  if (h0.x != (int)kLatentMagic || h0.y != p.batch || h0.z != p.total_q || h0.w != p.total_k ||
-      p.ws[6] != PA_LATENT_EXPANDED || p.ws[7] != kLatentRowsExpanded || p.ws[8] != p.num_tiles) {
-    if (threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
-    return;
-  }
-  const LatentTile tile = p.tiles[blockIdx.x];
+  bool bad = h0.x != (int)kLatentMagic || h0.y != p.batch || h0.z != p.total_q || h0.w != p.total_k ||
+             p.ws[6] != PA_LATENT_EXPANDED || p.ws[7] != kLatentRowsExpanded || p.ws[8] != p.num_tiles;
+  LatentTile tile{};
   int cq = 0, qn = 0, ck = 0, len = 0;
-  bool bad = tile.b < 0 || tile.b >= p.batch || tile.head < 0 || tile.head >= p.heads || tile.tok0 < 0 ||
-             tile.ntok < 1 || tile.ntok > kLatentRowsExpanded;
+  if (!bad) {
+    tile = p.tiles[blockIdx.x];
+    bad = tile.b < 0 || tile.b >= p.batch || tile.head < 0 || tile.head >= p.heads || tile.tok0 < 0 ||
+          tile.ntok < 1 || tile.ntok > kLatentRowsExpanded;
+  }
   if (!bad) {
     cq = p.cu_q[tile.b];
     qn = p.cu_q[tile.b + 1] - cq;
     ck = p.cu_k[tile.b];
     len = p.cu_k[tile.b + 1] - ck;
-    bad = cq < 0 || ck < 0 || cq + qn > p.total_q || ck + len > p.total_k || qn > len ||
-          tile.tok0 + tile.ntok > qn;
+    bad = cq < 0 || ck < 0 || qn > len || tile.tok0 + tile.ntok > qn || cq + qn > p.total_q ||
+          ck + len > p.total_k;
   }
-  if (bad) {
-    if (threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
-    return;
-  }
-  const int pos0 = len - qn + tile.tok0;
+  if (bad && threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
+  const int pos0 = len - qn + tile.tok0;  // position of the first row
+  // stages of each tile (0: it has no rows)
+  const int n0 = bad ? 0 : (pos0 + min(tile.ntok, kRows) + kTokens - 1) / kTokens;
+  const int n1 = bad || tile.ntok <= kRows ? 0 : (pos0 + tile.ntok + kTokens - 1) / kTokens;
+  const int n = max(n0, n1);
   const int span = pos0 + tile.ntok;
-  const int row0 = 16 * warp + g;
-  uint32_t qa[DK / 16][4];
-  const T* q = static_cast<const T*>(p.q) + ((int64_t)(cq + tile.tok0) * p.heads + tile.head) * DK + 2 * t4;
-#pragma unroll
-  for (int ks = 0; ks < DK / 16; ++ks)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int row = row0 + (c & 1) * 8;
-      qa[ks][c] = row < tile.ntok ? __ldg(reinterpret_cast<const unsigned int*>(
-                                        q + (int64_t)row * p.heads * DK + ks * 16 + (c >> 1) * 8))
-                                  : 0u;
-    }
-  float o[D / 8][4];
-#pragma unroll
-  for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[n][c] = 0.f;
-  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-  const int lim[2] = {row0 < tile.ntok ? pos0 + row0 : -1,
-                      row0 + 8 < tile.ntok ? pos0 + row0 + 8 : -1};
-  const T* kp = static_cast<const T*>(p.k) + ck * p.k_token + tile.head * p.k_head;
-  const T* vp = static_cast<const T*>(p.v) + ck * p.v_token + tile.head * p.v_head;
-  const T* rp = static_cast<const T*>(p.k_rope) + ck * p.kr_token;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 
-  for (int t0 = 0; t0 < span; t0 += kTok) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kTok * (DK / 8); i += 128) {  // rows past the span become zeros
-      const int t = i / (DK / 8), c = i % (DK / 8);
-      uint4 v = zero;
-      if (t0 + t < span)
-        v = c < D / 8 ? *reinterpret_cast<const uint4*>(kp + (t0 + t) * p.k_token + c * 8)
-                      : *reinterpret_cast<const uint4*>(rp + (t0 + t) * p.kr_token + c * 8 - D);
-      *reinterpret_cast<uint4*>(sm + L::K + t * L::KP + c * 16) = v;
-    }
-    for (int i = threadIdx.x; i < kTok * (D / 8); i += 128) {
-      const int t = i / (D / 8), c = i % (D / 8);
-      *reinterpret_cast<uint4*>(sm + L::V + t * L::VP + c * 16) =
-          t0 + t < span ? *reinterpret_cast<const uint4*>(vp + (t0 + t) * p.v_token + c * 8) : zero;
-    }
-    __syncthreads();
-    float sc[kTok / 8][4];
-#pragma unroll
-    for (int n = 0; n < kTok / 8; ++n)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) sc[n][c] = 0.f;
-    const int krow = (lane & 7) + ((lane >> 4) & 1) * 8, kch = (lane >> 3) & 1;
-#pragma unroll
-    for (int ks = 0; ks < DK / 16; ++ks)
-#pragma unroll
-      for (int n = 0; n < kTok / 16; ++n) {
-        uint32_t r0, r1, r2, r3;
-        ldsm_x4(sbase + L::K + (n * 16 + krow) * L::KP + (ks * 2 + kch) * 16, r0, r1, r2, r3);
-        mma_16816<T>(sc[2 * n], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], r0, r1);
-        mma_16816<T>(sc[2 * n + 1], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], r2, r3);
+  if (warp == 9) {
+    // ================= copies =================
+    if (lane == 0 && n > 0) {
+      const uint64_t keep = tc5::l2_evict_normal_policy(), once = l2_evict_first_policy();
+      const int tiles = n1 > 0 ? 2 : 1;
+      mbar_arrive_expect_tx(sb + L::Q_FULL, (uint32_t)(tiles * L::QTILE));
+      for (int t = 0; t < tiles; ++t)
+        for (int b = 0; b < DK / 64; ++b)
+          tma_load_3d(sb + L::Q + t * L::QTILE + b * L::BOX, &maps.q, b * 64, tile.head,
+                      cq + tile.tok0 + t * kRows, sb + L::Q_FULL, once);
+      int j = 0, jv = 0;
+      bool good = true;
+      for (; j < n; ++j) {
+        const int s = j % L::NK, tok = ck + j * kTokens;
+        good = j < L::NK || mbar_wait_bounded_sleep(sb + L::K_FREE + 8 * s,
+                                                    (uint32_t)((j / L::NK - 1) & 1), p.wait_ns);
+        if (!good) break;
+        const uint32_t kb = sb + L::K + s * L::KSTAGE, kf = sb + L::K_FULL + 8 * s;
+        mbar_arrive_expect_tx(kf, L::KSTAGE);
+        for (int b = 0; b < D / 64; ++b)
+          tma_load_3d(kb + b * L::BOX, &maps.k, b * 64, p.k_token_major ? tile.head : tok,
+                      p.k_token_major ? tok : tile.head, kf, keep);
+        tma_load_3d(kb + D / 64 * L::BOX, &maps.kr, 0, tok, 0, kf, keep);
+        good = j < 1 || mbar_wait_bounded_sleep(sb + L::V_FREE, (uint32_t)((j - 1) & 1), p.wait_ns);
+        if (!good) break;
+        mbar_arrive_expect_tx(sb + L::V_FULL, L::VSTAGE);
+        for (int b = 0; b < D / 64; ++b)
+          tma_load_3d(sb + L::V + b * L::BOX, &maps.v, b * 64, p.v_token_major ? tile.head : tok,
+                      p.v_token_major ? tok : tile.head, sb + L::V_FULL, keep);
+        ++jv;
       }
-    uint32_t ph[kTok / 16][4], pl[kTok / 16][4];
+      if (!good) {
+        set_status(p.status, PA_DEV_TIMEOUT);
+        *flag = 1;
+        ++j;  // the stage whose keys were issued (or an older phase, complete already)
+      }
+      // copies in flight land before the CTA exits
+      mbar_wait_bounded_sleep(sb + L::Q_FULL, 0u, kDrainWaitNs);
+      for (int i = j < L::NK ? 0 : j - L::NK; i < j && i < n; ++i)
+        if (i < jv || !good)
+          mbar_wait_bounded_sleep(sb + L::K_FULL + 8 * (i % L::NK), (uint32_t)((i / L::NK) & 1),
+                                  kDrainWaitNs);
+      if (jv > 0) mbar_wait_bounded_sleep(sb + L::V_FULL, (uint32_t)((jv - 1) & 1), kDrainWaitNs);
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ================= MMAs =================
+    if (n > 0) {
+      const uint32_t idesc_s = tc5::instr_desc<T>(kRows, kTokens, false);
+      const uint32_t idesc_o = tc5::instr_desc<T>(kRows, D, true);
+      auto issue_s = [&](int t, int j) {
+        if (lane == 0) {
+          tc5::fence_after();
+          const uint32_t qb = sb + L::Q + t * L::QTILE, kb = sb + L::K + (j % L::NK) * L::KSTAGE;
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      float mx = -INFINITY;
-#pragma unroll
-      for (int n = 0; n < kTok / 8; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float& x = sc[n][2 * hh + c];
-          x = t0 + n * 8 + 2 * t4 + c <= lim[hh] ? x * p.qscale : -INFINITY;
-          mx = fmaxf(mx, x);
+          for (int k = 0; k < DK / 16; ++k)
+            tc5::mma(tmem + t * kTokens,
+                     tc5::smem_desc(qb + (k >> 2) * L::BOX + (k & 3) * 32, 16, 1024),
+                     tc5::smem_desc(kb + (k >> 2) * L::BOX + (k & 3) * 32, 16, 1024), idesc_s,
+                     k > 0 ? 1u : 0u);
+          tc5::commit(sb + L::S_DONE + 8 * t);
         }
-      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-      const float m_new = fmaxf(m_run[hh], mx);
-      const float ref = m_new == -INFINITY ? 0.f : m_new;
-      const float al = ex2(m_run[hh] - ref);
-      float ps = 0.f;
-#pragma unroll
-      for (int n = 0; n < kTok / 8; ++n) {
-        const float2 w = make_float2(ex2(sc[n][2 * hh] - ref), ex2(sc[n][2 * hh + 1] - ref));
-        ps += w.x + w.y;
-        // the A fragment of 16 tokens: (row, low 8), (row + 8, low 8), (row, high 8), (row + 8, high 8)
-        split_hi_lo<T>(w, ph[n / 2][hh + 2 * (n & 1)], pl[n / 2][hh + 2 * (n & 1)]);
+      };
+      auto wait = [&](int bar, uint32_t parity) {
+        return __all_sync(kFull, mbar_wait_bounded_sleep(sb + bar, parity, p.wait_ns)) != 0;
+      };
+      bool good = wait(L::Q_FULL, 0u) && wait(L::K_FULL, 0u);
+      if (good) {
+        if (n0 > 0) issue_s(0, 0);
+        if (n1 > 0) issue_s(1, 0);
+        if (lane == 0) tc5::commit(sb + L::K_FREE);
       }
-      ps += __shfl_xor_sync(kFull, ps, 1);
-      ps += __shfl_xor_sync(kFull, ps, 2);
-      l_run[hh] = l_run[hh] * al + ps;
-      m_run[hh] = m_new;
+      for (int j = 0; j < n && good; ++j) {
+        bool have_v = false;
+        const bool next = j + 1 < n;
+        bool have_k = false;
+        for (int t = 0; t < 2 && good; ++t) {
+          const int nt = t ? n1 : n0;
+          if (j < nt) {
+            good = wait(L::P_READY + 8 * t, (uint32_t)(j & 1));
+            if (good && !have_v) {
+              good = wait(L::V_FULL, (uint32_t)(j & 1));
+              have_v = true;
+              const int valid = span - j * kTokens;  // rows of the stage that some row sees
+              if (good && valid < kTokens) {
+                for (int i = lane; i < (kTokens - valid) * 8 * (D / 64); i += 32) {
+                  const int b = i / ((kTokens - valid) * 8), c = i % ((kTokens - valid) * 8);
+                  *reinterpret_cast<uint4*>(base + L::V + b * L::BOX + valid * 128 + c * 16) =
+                      make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();  // the tensor core reads them (async proxy)
+                __syncwarp();
+              }
+            }
+            if (!good) break;
+            if (lane == 0) {
+              tc5::fence_after();
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        o[n][2 * hh] *= al;
-        o[n][2 * hh + 1] *= al;
+              for (int k = 0; k < kTokens / 16; ++k)
+                tc5::mma_tmem_a(tmem + 2 * kTokens + t * D, tmem + t * kTokens + 8 * k,
+                                tc5::smem_desc(sb + L::V + k * 2048, L::BOX, 1024), idesc_o,
+                                j > 0 || k > 0 ? 1u : 0u);
+              tc5::commit(sb + L::PV_DONE + 8 * t);
+              if (t == (n1 > j ? 1 : 0)) tc5::commit(sb + L::V_FREE);
+            }
+          }
+          if (j + 1 < nt) {
+            if (!have_k) good = wait(L::K_FULL + 8 * ((j + 1) % L::NK), (uint32_t)(((j + 1) / L::NK) & 1));
+            have_k = true;
+            // P V(j) reads P_t from the columns that S_t(j + 1) overwrites
+            good = good && wait(L::PV_DONE + 8 * t, (uint32_t)(j & 1));
+            if (!good) break;
+            issue_s(t, j + 1);
+          }
+        }
+        if (good && next && lane == 0) tc5::commit(sb + L::K_FREE + 8 * ((j + 1) % L::NK));
+      }
+      if (!good && lane == 0) {
+        set_status(p.status, PA_DEV_TIMEOUT);
+        *flag = 1;
+      }
+      // every MMA issued finishes before TMEM is freed
+      if (lane == 0) {
+        tc5::commit(sb + L::DRAIN);
+        mbar_wait_bounded_sleep(sb + L::DRAIN, 0u, kDrainWaitNs);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ================= softmax and output =================
+    const int t = warp >> 2;
+    const int row = threadIdx.x & 127;                 // of the tile
+    const int nt = t ? n1 : n0;
+    const bool ok = !bad && t * kRows + row < tile.ntok;
+    const int qpos = ok ? pos0 + t * kRows + row : -1;  // last visible token
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t t_s = tmem + t * kTokens + lane_off, t_o = tmem + 2 * kTokens + t * D + lane_off;
+    constexpr float kBias = std::is_same<T, __half>::value ? 7.f : 0.f;
+    float m_run = -INFINITY, l_run = 0.f;
+    bool good = true;
+    for (int j = 0; j < nt; ++j) {
+      good = __all_sync(kFull, mbar_wait_bounded_sleep(sb + L::S_DONE + 8 * t, (uint32_t)(j & 1), p.wait_ns));
+      if (!good) break;
+      tc5::fence_after();
+      float sv[kTokens];
+#pragma unroll
+      for (int c = 0; c < kTokens; c += 32) tc5::ld32(t_s + (uint32_t)c, sv + c);
+      tc5::wait_ld();
+      const int lim = qpos - j * kTokens;  // last visible column of the stage
+      if (!__all_sync(kFull, lim >= kTokens - 1)) {
+#pragma unroll
+        for (int c = 0; c < kTokens; ++c) sv[c] = c <= lim ? sv[c] : -INFINITY;
+      }
+      float mx4[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+      for (int c = 4; c < kTokens; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], sv[c]);
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.qscale;
+      float al = 1.f;
+      bool resc = false;
+      if (mx > m_run + kLazyLog2) {
+        al = ex2(m_run - mx);  // 0 when the row had no weight yet
+        resc = m_run != -INFINITY;
+        m_run = mx;
+      }
+      const float nm = m_run == -INFINITY ? -INFINITY : kBias - m_run;  // no token yet: weights 0
+      const float2 qs2 = make_float2(p.qscale, p.qscale), nm2 = make_float2(nm, nm);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int c0 = 0; c0 < kTokens; c0 += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const float2 x = ffma2(make_float2(sv[c0 + c], sv[c0 + c + 1]), qs2, nm2);
+          const float2 w = make_float2(ex2(x.x), ex2(x.y));
+          sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], w);
+          pk[c >> 1] = Elem<T>::from_f2(w.x, w.y);
+        }
+        tc5::st16u(t_s + (uint32_t)(c0 / 2), pk);
+      }
+      const float2 s2 = fadd2(sum[0], sum[1]);
+      l_run = l_run * al + (s2.x + s2.y);
+      // S(j) was issued after P V(j - 1) was done, so O may be rescaled now
+      if (j > 0 && __any_sync(kFull, resc)) {
+        const float f = resc ? al : 1.f;
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+          float ov[16];
+          tc5::ld16(t_o + (uint32_t)c, ov);
+          tc5::wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) ov[i] *= f;
+          tc5::st16(t_o + (uint32_t)c, ov);
+        }
+      }
+      tc5::wait_st();
+      tc5::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sb + L::P_READY + 8 * t);
+    }
+    if (nt > 0 && good) {
+      good = __all_sync(kFull, mbar_wait_bounded_sleep(sb + L::PV_DONE + 8 * t, (uint32_t)((nt - 1) & 1),
+                                                       p.wait_ns));
+      if (good) {
+        tc5::fence_after();
+        const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
+        T* out = static_cast<T*>(p.out) +
+                 ((int64_t)(cq + tile.tok0 + t * kRows + row) * p.heads + tile.head) * D;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float ov[32];
+          tc5::ld32(t_o + (uint32_t)c, ov);
+          tc5::wait_ld();
+          if (ok) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint4 w;
+              w.x = Elem<T>::from_f2(ov[i] * inv, ov[i + 1] * inv);
+              w.y = Elem<T>::from_f2(ov[i + 2] * inv, ov[i + 3] * inv);
+              w.z = Elem<T>::from_f2(ov[i + 4] * inv, ov[i + 5] * inv);
+              w.w = Elem<T>::from_f2(ov[i + 6] * inv, ov[i + 7] * inv);
+              *reinterpret_cast<uint4*>(out + c + i) = w;
+            }
+          }
+        }
       }
     }
-    const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8, vch = lane >> 4;
-#pragma unroll
-    for (int u = 0; u < kTok / 16; ++u)
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d) {
-        uint32_t r0, r1, r2, r3;
-        ldsm_x4_t(sbase + L::V + (u * 16 + vrow) * L::VP + (d * 2 + vch) * 16, r0, r1, r2, r3);
-        mma_16816<T>(o[2 * d], ph[u][0], ph[u][1], ph[u][2], ph[u][3], r0, r1);
-        mma_16816<T>(o[2 * d + 1], ph[u][0], ph[u][1], ph[u][2], ph[u][3], r2, r3);
-        mma_16816<T>(o[2 * d], pl[u][0], pl[u][1], pl[u][2], pl[u][3], r0, r1);
-        mma_16816<T>(o[2 * d + 1], pl[u][0], pl[u][1], pl[u][2], pl[u][3], r2, r3);
-      }
+    if (!good && lane == 0) set_status(p.status, PA_DEV_TIMEOUT);
   }
-#pragma unroll
-  for (int hh = 0; hh < 2; ++hh) {
-    const int row = row0 + 8 * hh;
-    if (row >= tile.ntok) continue;
-    const float inv = 1.f / l_run[hh];  // every row sees its own token
-    T* out = static_cast<T*>(p.out) + ((int64_t)(cq + tile.tok0 + row) * p.heads + tile.head) * D + 2 * t4;
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-      *reinterpret_cast<uint32_t*>(out + 8 * n) = Elem<T>::from_f2(o[n][2 * hh] * inv, o[n][2 * hh + 1] * inv);
+
+  tc5::fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc5::fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
 
+// Rows [outer][inner] of `width` dense elements, as a 3-D map with boxes of
+// 64 elements by 128 tokens of one head.  token_major: tokens are the outer
+// dimension.
+bool encode_rows(CUtensorMap* map, const void* ptr, int dtype, int width, int64_t tokens,
+                 int64_t token_stride, int64_t heads, int64_t head_stride, bool token_major) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t nt = (cuuint64_t)tokens, nh = (cuuint64_t)heads;
+  cuuint64_t dims[3] = {(cuuint64_t)width, token_major ? nh : nt, token_major ? nt : nh};
+  cuuint64_t strides[2] = {(cuuint64_t)(token_major ? head_stride : token_stride) * 2,
+                           (cuuint64_t)(token_major ? token_stride : head_stride) * 2};
+  cuuint32_t box[3] = {64, token_major ? 1u : (cuuint32_t)kTokens, token_major ? (cuuint32_t)kTokens : 1u};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType ty = dtype == PA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(map, ty, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int D>
-cudaError_t launch_t(const LatentPrefillParams& p, cudaStream_t stream) {
+cudaError_t launch_t(const LatentPrefillParams& p, const XMaps& maps, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
-  return launch_pdl(latent_prefill_kernel<T, D>, PrefillLayout1<D>::BYTES, configured, p, p.num_tiles, 128,
-                    stream);
+  auto kern = latent_prefill_kernel<T, D>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(configured.load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, XLayout<D>::BYTES);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.num_tiles);
+  cfg.blockDim = dim3(kPrefillThreads);
+  cfg.dynamicSmemBytes = XLayout<D>::BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p, maps);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_prefill(const LatentPrefillParams& p, int head_dim, int dtype,
+cudaError_t launch_latent_prefill(const LatentPrefillParams& params, int head_dim, int dtype,
                                   cudaStream_t stream) {
+  LatentPrefillParams p = params;
+  const int64_t dk = head_dim + kRope;
+  // the outer dimension of a map is the one with the larger stride
+  p.k_token_major = p.k_token >= p.k_head;
+  p.v_token_major = p.v_token >= p.v_head;
+  XMaps maps{};
+  if (!encode_rows(&maps.q, p.q, dtype, (int)dk, p.total_q, p.heads * dk, p.heads, dk, true) ||
+      !encode_rows(&maps.k, p.k, dtype, head_dim, p.total_k, p.k_token, p.heads, p.k_head,
+                   p.k_token_major) ||
+      !encode_rows(&maps.kr, p.k_rope, dtype, kRope, p.total_k, p.kr_token, 1,
+                   p.kr_token * p.total_k, false) ||
+      !encode_rows(&maps.v, p.v, dtype, head_dim, p.total_k, p.v_token, p.heads, p.v_head,
+                   p.v_token_major))
+    return cudaErrorInvalidValue;
   const bool bf = dtype == PA_DTYPE_BF16;
-  if (head_dim == 64) return bf ? launch_t<__nv_bfloat16, 64>(p, stream) : launch_t<__half, 64>(p, stream);
-  return bf ? launch_t<__nv_bfloat16, 128>(p, stream) : launch_t<__half, 128>(p, stream);
+  if (head_dim == 64)
+    return bf ? launch_t<__nv_bfloat16, 64>(p, maps, stream) : launch_t<__half, 64>(p, maps, stream);
+  return bf ? launch_t<__nv_bfloat16, 128>(p, maps, stream) : launch_t<__half, 128>(p, maps, stream);
 }
 
 }  // namespace pa
