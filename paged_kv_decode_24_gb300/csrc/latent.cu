@@ -117,8 +117,9 @@ pa_status_t check_latent_call(const pa_latent_shape_t* s, const pa_latent_plan_t
   if ((plan->form != PA_LATENT_ABSORBED && plan->form != PA_LATENT_EXPANDED) ||
       (form >= 0 && plan->form != form))
     return PA_ERR_PLAN;
-  if (plan->form == PA_LATENT_ABSORBED ? plan->rows_per_tile != kLatentRowsMma
-                                       : plan->rows_per_tile != kLatentRowsExpanded)
+  const int rows = plan->rows_per_tile;
+  if (plan->form == PA_LATENT_ABSORBED ? rows != kLatentRowsMma && rows != kLatentRowsPair
+                                       : rows != kLatentRowsExpanded)
     return PA_ERR_PLAN;
   if (plan->num_ranges < 0 || plan->num_segments < 0 || plan->num_merges < 0 ||
       plan->num_slots < 0 || plan->total_q < 0 || plan->total_k < 0)
@@ -153,14 +154,15 @@ LatentRowsParams rows_params(const pa_latent_shape_t* s, const int32_t* block_ta
 }
 
 // The pool [P][S][576] with boxes of `cols` column blocks (64 elements each)
-// by 16 tokens, 128-byte swizzle.
-bool encode_latent_map(CUtensorMap* map, const void* pages, const pa_latent_shape_t& s, int cols) {
+// by `tokens` tokens, 128-byte swizzle.
+bool encode_latent_map(CUtensorMap* map, const void* pages, const pa_latent_shape_t& s, int cols,
+                       int tokens) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t row = kLatentRow * 2;
   cuuint64_t dims[4] = {64, kLatentRow / 64, (cuuint64_t)s.page_size, (cuuint64_t)s.num_pages};
   cuuint64_t strides[3] = {128, row, row * s.page_size};
-  cuuint32_t box[4] = {64, (cuuint32_t)cols, kLatentBlock, 1};
+  cuuint32_t box[4] = {64, (cuuint32_t)cols, (cuuint32_t)tokens, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUtensorMapDataType ty = s.dtype == PA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -268,8 +270,13 @@ extern "C" pa_status_t pa_latent_attention(const pa_latent_shape_t* shape,
   p.total_q = plan->total_q;
   p.rows = plan->rows_per_tile;
   cudaStream_t s = (cudaStream_t)stream;
-  if (!encode_latent_map(&p.pages_map, pages, *shape, kLatentRow / 64)) return PA_ERR_CUDA;
-  cudaError_t e = launch_latent_mma(p, shape->dtype, s);
+  const bool pair = plan->rows_per_tile == kLatentRowsPair;
+  const int box = shape->page_size < 64 ? shape->page_size : 64;
+  if (!encode_latent_map(&p.pages_map, pages, *shape, pair ? 1 : kLatentRow / 64,
+                         pair ? box : kLatentBlock))
+    return PA_ERR_CUDA;
+  cudaError_t e = pair ? launch_latent_pair(p, shape->dtype, s)
+                       : launch_latent_mma(p, shape->dtype, s);
   if (e == cudaSuccess && p.num_merges > 0) e = launch_latent_merge(p, shape->dtype, s);
   return cuda_status(e);
 }

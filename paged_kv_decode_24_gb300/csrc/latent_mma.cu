@@ -29,7 +29,7 @@
 #include "decode_tc.cuh"
 #include "device_common.cuh"
 #include "elem.cuh"
-#include "latent_params.h"
+#include "latent_segment.cuh"
 #include "split_launch.cuh"
 
 namespace pa {
@@ -66,17 +66,6 @@ __device__ __forceinline__ void work_barrier() {
 __device__ __forceinline__ uint32_t block_chunk(uint32_t block, int row, int chunk) {
   const int line = row * (kLatentRow / 64) + (chunk >> 3);
   return block + (uint32_t)(line * 128 + (((chunk ^ line) & 7) << 4));
-}
-
-// A segment of this call's plan whose rows and tokens are its sequence's.
-__device__ __forceinline__ bool segment_ok(const LatentParams& p, const LatentSegment& s, int rows) {
-  if (s.b < 0 || s.b >= p.batch || s.nrows < 1 || s.nrows > rows || s.row0 < 0 ||
-      s.slot >= p.num_slots || s.tok0 < 0 || s.tok0 % kLatentStage != 0 || s.tok1 <= s.tok0)
-    return false;
-  const int cq = p.cu_q[s.b], qn = p.cu_q[s.b + 1] - cq, len = p.cu_k[s.b + 1] - p.cu_k[s.b];
-  return cq >= 0 && p.cu_q[s.b + 1] <= p.total_q &&
-         (int64_t)s.row0 + s.nrows <= (int64_t)qn * p.heads && qn <= len && s.tok1 <= len &&
-         (int64_t)len <= (int64_t)p.max_pages * p.page_size;
 }
 
 template <typename T>
@@ -123,7 +112,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     bool good = true;
     for (int i = first; i < last && good; ++i) {
       const LatentSegment s = p.segments[i];
-      if (!segment_ok(p, s, kLatentRowsMma)) continue;  // the working warps report it
+      if (!latent_segment_ok(p, s, kLatentRowsMma)) continue;  // the working warps report it
       const int32_t* table = p.block_table + (int64_t)s.b * p.max_pages;
       const int blocks = (s.tok1 - s.tok0 + kLatentBlock - 1) / kLatentBlock;
       int entry = -1;
@@ -178,7 +167,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   bool good = true;  // after a wait that gave up, a warp only keeps its place in the barriers
   for (int i = first; i < last; ++i) {
     const LatentSegment s = p.segments[i];
-    if (!segment_ok(p, s, kLatentRowsMma)) {  // the same for every warp
+    if (!latent_segment_ok(p, s, kLatentRowsMma)) {  // the same for every warp
       if (threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
       continue;
     }

@@ -1,0 +1,615 @@
+// Absorbed latent attention for tiles of up to 128 query rows, on pairs of
+// SMs (tcgen05 with cta_group::2).
+//
+//   s[i][t] = q_i . [c_t ; r_t],  o_i = sum_t 2^(s qscale - m_i) c_t / sum_t 2^(s qscale - m_i)
+//
+// With 128 rows a cached row of 1152 bytes feeds 2 x 128 x 1088 operations,
+// 242 a byte: the card does 280 a byte, so HBM bounds the work and the tensor
+// cores have to run at more than three quarters of their rate under it.  What
+// makes that hard is the output: 128 rows x 512 values of fp32 would fill one
+// SM's TMEM.  A pair of SMs shares the tile instead: each CTA keeps 64 rows
+// (M = 128 over the pair puts 64 rows in 128 lanes, the second half of the
+// columns in lanes 64-127), so O takes 256 columns and S 64, and each MMA
+// reads half of its B operand from either SM.  Per stage of 128 tokens a CTA
+// holds
+//   K [9 boxes of 64 dims][64 tokens][128 B]   its half of the stage's tokens
+//   V [4 boxes][128 tokens][128 B]             its half of the 512 values
+// of which K is refilled in three groups of boxes and V in two groups of
+// tokens, each as soon as the MMAs that read it are done.
+//   warps 0-3: softmax and output.  Thread (warp, lane) owns row
+//              32 (warp % 2) + lane of the CTA's 64: tokens 0-63 of the stage
+//              in warps 0-1, 64-127 in warps 2-3; the two threads of a row
+//              exchange their maxima through shared memory.
+//   warp 4:    in the pair's first CTA issues the MMAs of both; in the second
+//              tells the first when its buffers have landed
+//   warp 5:    copies q and K;  warp 6: copies V
+// Per stage j: S(j+1) = q K^T into one of two TMEM buffers; softmax(j);
+// O += P(j) V(j), P from shared memory [2 boxes of 64 tokens][64 rows][128 B].
+// The weights are rounded to the element type once (fp16: times 2^7, so that
+// small ones stay normal): a second part would cost the product again, and
+// the error stays below that of rounding the result.
+//
+// Value rows of tokens past the piece's end or of a bad page become zeros
+// before they are used (their weight is 0, but they may hold anything).
+// Every wait is bounded; a CTA that gave up keeps its place in the barriers
+// between its own warps, writes nothing, and meets the other CTA at the end.
+#include <math.h>
+
+#include "latent_segment.cuh"
+#include "prefill_tc5.cuh"
+#include "split_launch.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kPairRows = 64;          // rows of one CTA
+constexpr int kPairTokens = 128;       // tokens of a stage
+constexpr int kPairThreads = 7 * 32;
+constexpr float kPairLazyLog2 = 8.f;   // the maximum is raised when it grows by more than 2^8
+static_assert(kLatentRowsPair == 2 * kPairRows && kLatentStagePair == kPairTokens, "plan and kernel");
+
+struct PLayout {
+  static constexpr int QBOX = kPairRows * 128;            // 8 KB
+  static constexpr int KBOX = kPairTokens / 2 * 128;      // 8 KB
+  static constexpr int VBOX = kPairTokens * 128;          // 16 KB
+  static constexpr int NG = 3, NV = 2;                    // groups of K boxes, of V tokens
+  static constexpr int Q = 0;
+  static constexpr int K = Q + 9 * QBOX;
+  static constexpr int V = K + 9 * KBOX;
+  static constexpr int P = V + 4 * VBOX;
+  static constexpr int PBOX = kPairRows * 128;
+  static constexpr int BARS = P + 2 * PBOX;
+  // mbarriers.  In both CTAs:
+  static constexpr int Q_FULL = BARS;
+  static constexpr int K_FULL = Q_FULL + 8;               // NG
+  static constexpr int V_FULL = K_FULL + 8 * NG;          // NV
+  static constexpr int Q_FREE = V_FULL + 8 * NV;
+  static constexpr int K_FREE = Q_FREE + 8;               // NG
+  static constexpr int V_FREE = K_FREE + 8 * NG;          // NV
+  static constexpr int S_DONE = V_FREE + 8 * NV;          // 2
+  static constexpr int PV_DONE = S_DONE + 16;
+  static constexpr int DRAIN = PV_DONE + 8;
+  // used in the first CTA only: the other CTA's buffers, the weights of both
+  static constexpr int Q_PEER = DRAIN + 8;
+  static constexpr int K_PEER = Q_PEER + 8;               // NG
+  static constexpr int V_PEER = K_PEER + 8 * NG;          // NV
+  static constexpr int P_READY = V_PEER + 8 * NV;
+  static constexpr int TMEM_SLOT = P_READY + 8;
+  static constexpr int XMAX = align_up(TMEM_SLOT + 8, 16);  // [2][128] floats: row maxima, sums
+  static constexpr int BYTES = XMAX + 2 * 128 * 4 + 1024;
+};
+static_assert(PLayout::BYTES <= kMaxCtaSmem, "stages do not fit in shared memory");
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// Arrive on the first CTA's barrier at this offset of its shared memory.
+__device__ __forceinline__ void arrive_first_cta(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\t"
+      "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n\t}" ::"r"(bar)
+      : "memory");
+}
+
+// A bounded wait that acquires what the other CTA released.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(limit_ns < kShortWaitNs ? 0u : kSuspendHintNs)
+        : "memory");
+    if (ok) return true;
+    if (global_timer_ns() - t0 > limit_ns) return false;
+  }
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The barrier at this offset in both CTAs, once every MMA issued so far is done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                            uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void row_pair_barrier(int warp) {  // the two warps that share 32 rows
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 1)) : "memory");
+}
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    latent_pair_kernel(const __grid_constant__ LatentParams p,
+                       const __grid_constant__ CUtensorMap q_map) {
+  using L = PLayout;
+  extern __shared__ unsigned char smem_dyn[];
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(base);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cta_rank();
+
+  if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.pages_map)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&q_map)) : "memory");
+    for (int b = L::Q_FULL; b < L::P_READY; b += 8) mbar_init(sb + b, 1);
+    mbar_init(sb + L::P_READY, 8);
+    fence_barrier_init();
+  }
+  if (warp == 4) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     sb + L::TMEM_SLOT)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc5::fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before either is arrived on
+  tc5::fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + L::TMEM_SLOT);
+  const uint32_t t_o = tmem, t_s = tmem + 256;  // O 256 columns, S two buffers of 64
+  pdl_launch_dependents();
+  pdl_wait_primary();
+
+  const int4 h0 = reinterpret_cast<const int4*>(p.ws)[0], h2 = reinterpret_cast<const int4*>(p.ws)[2];
+  int first = 0, last = 0;
+  if (h0.x == (int)kLatentMagic && h0.y == p.batch && h0.z == p.total_q && h2.x == p.num_ranges &&
+      h2.y == p.num_segments && h2.z == p.num_merges && h2.w == p.num_slots &&
+      p.ws[6] == PA_LATENT_ABSORBED && p.ws[7] == kLatentRowsPair) {
+    const int range = (int)(blockIdx.x >> 1);
+    first = p.ranges[range];
+    last = min(p.ranges[range + 1], p.num_segments);
+    if (first < 0) first = last;
+  } else if (threadIdx.x == 0) {
+    set_status(p.status, PA_DEV_PLAN_MISMATCH);
+  }
+  auto usable = [&](const LatentSegment& s) {  // the same answer in every warp of both CTAs
+    return latent_segment_ok(p, s, kLatentRowsPair);
+  };
+  auto stages_of = [](const LatentSegment& s) {
+    return (s.tok1 - s.tok0 + kPairTokens - 1) / kPairTokens;
+  };
+
+  if (warp == 5 || warp == 6) {
+    // ================= copies =================
+    // Stages are counted over all segments: use c of a buffer has parity c & 1.
+    const bool keys = warp == 5;
+    int c = 0, qc = 0;
+    bool good = true;
+    const uint64_t policy = l2_evict_first_policy();
+    const uint64_t keep = tc5::l2_evict_normal_policy();
+    const int box = p.page_size < 64 ? p.page_size : 64;  // tokens of one copy
+    const int groups = keys ? L::NG : L::NV;
+    int issued[3] = {0, 0, 0};  // uses of each group
+    for (int i = first; i < last && good; ++i) {
+      const LatentSegment s = p.segments[i];
+      if (!usable(s)) continue;
+      const int32_t* table = p.block_table + (int64_t)s.b * p.max_pages;
+      if (keys) {  // q: the CTA's 64 rows
+        if (lane == 0) {
+          good = qc == 0 || wait_cluster(sb + L::Q_FREE, (uint32_t)((qc - 1) & 1), p.wait_ns);
+          if (good) {
+            mbar_arrive_expect_tx(sb + L::Q_FULL, 9 * L::QBOX);
+            const int row = (int)((int64_t)p.cu_q[s.b] * p.heads + s.row0) + rank * kPairRows;
+            for (int b = 0; b < 9; ++b)
+              tma_load_2d(sb + L::Q + b * L::QBOX, &q_map, b * 64, row, sb + L::Q_FULL, policy);
+          }
+        }
+        good = __shfl_sync(kFull, good, 0);
+        if (!good) break;
+        ++qc;
+      }
+      const int n = stages_of(s);
+      for (int j = 0; j < n && good; ++j, ++c) {
+        // lane u: the page of copy u (its tokens: the CTA's half of the stage, or all of it)
+        const int copies = (keys ? 64 : kPairTokens) / box;
+        const int tok = s.tok0 + j * kPairTokens + (keys ? rank * 64 : 0) + lane * box;
+        int page = -1;
+        if (lane < copies && tok < s.tok1) {
+          page = table[tok / p.page_size];
+          if (page < 0 || page >= p.num_pages) {
+            page = -1;
+            set_status(p.status, PA_DEV_BAD_PAGE);
+          }
+        }
+        const unsigned have = __ballot_sync(kFull, page >= 0);
+        for (int g = 0; g < groups && good; ++g) {
+          const int free_bar = (keys ? L::K_FREE : L::V_FREE) + 8 * g;
+          const uint32_t full = sb + (keys ? L::K_FULL : L::V_FULL) + 8 * g;
+          good = c == 0 || __all_sync(kFull, wait_cluster(sb + free_bar, (uint32_t)((c - 1) & 1), p.wait_ns));
+          if (!good) break;
+          // copies of this group: every one for three boxes of K, half of them for four of V
+          const int per = copies / (keys ? 1 : L::NV);
+          const unsigned mine = keys ? have : have >> (g * per) & ((1u << per) - 1u);
+          if (lane == 0) {
+            if (mine)
+              mbar_arrive_expect_tx(full, (uint32_t)(__popc(mine) * box * 128 * (keys ? 3 : 4)));
+            else
+              mbar_arrive(full);
+          }
+          __syncwarp();
+          const int u0 = keys ? 0 : g * per;
+          if (lane >= u0 && lane < u0 + per && page >= 0) {  // each lane issues its own copies
+            const int row = tok % p.page_size;
+            if (keys) {
+#pragma unroll
+              for (int b = 0; b < 3; ++b)
+                tma_load_4d(sb + L::K + (3 * g + b) * L::KBOX + lane * box * 128, &p.pages_map, 0,
+                            3 * g + b, row, page, full, keep);
+            } else {
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                tma_load_4d(sb + L::V + b * L::VBOX + lane * box * 128, &p.pages_map, 0,
+                            (b >> 1) * 4 + rank * 2 + (b & 1), row, page, full, keep);
+            }
+          }
+          issued[g] = c + 1;
+          __syncwarp();
+        }
+      }
+    }
+    if (!good && lane == 0) set_status(p.status, PA_DEV_TIMEOUT);
+    // every copy has landed, and every arrival that the MMAs send here, before
+    // the CTA ends
+    for (int g = 0; g < groups; ++g)
+      if (issued[g] > 0) {
+        mbar_wait_bounded_sleep(sb + (keys ? L::K_FULL : L::V_FULL) + 8 * g,
+                                (uint32_t)((issued[g] - 1) & 1), kDrainWaitNs);
+        wait_cluster(sb + (keys ? L::K_FREE : L::V_FREE) + 8 * g, (uint32_t)((issued[g] - 1) & 1),
+                     kDrainWaitNs);
+      }
+    if (keys && qc > 0) {
+      mbar_wait_bounded_sleep(sb + L::Q_FULL, (uint32_t)((qc - 1) & 1), kDrainWaitNs);
+      wait_cluster(sb + L::Q_FREE, (uint32_t)((qc - 1) & 1), kDrainWaitNs);
+    }
+    __syncwarp();
+  } else if (warp == 4) {
+    // ================= MMAs (first CTA), news of the buffers (second) =================
+    const uint32_t idesc_s = tc5::instr_desc<T>(128, kPairTokens, false);
+    const uint32_t idesc_o = tc5::instr_desc<T>(128, 256, true);
+    bool good = true;
+    int c = 0, qc = 0;  // stages, segments
+    auto wait = [&](int bar, int count) {
+      return __all_sync(kFull, wait_cluster(sb + bar, (uint32_t)(count & 1), p.wait_ns)) != 0;
+    };
+    // S of stage number cs: the group's buffers of both CTAs, then its MMAs
+    auto scores = [&](int cs, bool last_of_segment) {
+      for (int g = 0; g < L::NG; ++g) {
+        if (!wait(L::K_FULL + 8 * g, cs)) return false;
+        if (rank != 0) {
+          if (lane == 0) arrive_first_cta(sb + L::K_PEER + 8 * g);
+          continue;
+        }
+        if (!wait(L::K_PEER + 8 * g, cs)) return false;
+        if (lane == 0) {
+          tc5::fence_after();
+#pragma unroll
+          for (int k = 12 * g; k < 12 * g + 12; ++k)
+            mma_pair(t_s + (uint32_t)(64 * (cs & 1)),
+                     tc5::smem_desc(sb + L::Q + (k >> 2) * L::QBOX + (k & 3) * 32, 16, 1024),
+                     tc5::smem_desc(sb + L::K + (k >> 2) * L::KBOX + (k & 3) * 32, 16, 1024),
+                     idesc_s, k > 0 ? 1u : 0u);
+          commit_pair(sb + L::K_FREE + 8 * g);
+        }
+        __syncwarp();
+      }
+      if (rank == 0 && lane == 0) {
+        commit_pair(sb + L::S_DONE + 8 * (cs & 1));
+        if (last_of_segment) commit_pair(sb + L::Q_FREE);
+      }
+      return true;
+    };
+    for (int i = first; i < last && good; ++i) {
+      const LatentSegment s = p.segments[i];
+      if (!usable(s)) continue;
+      const int32_t* table = p.block_table + (int64_t)s.b * p.max_pages;
+      const int n = stages_of(s);
+      good = wait(L::Q_FULL, qc);
+      if (good && rank != 0 && lane == 0) arrive_first_cta(sb + L::Q_PEER);
+      if (good && rank == 0) good = wait(L::Q_PEER, qc);
+      good = good && scores(c, n == 1);
+      for (int j = 0; j < n && good; ++j) {
+        // lane u < 8: is the page of tokens 16 u .. of the stage bad?
+        const int tok = s.tok0 + j * kPairTokens + lane * kLatentBlock;
+        const int page = lane < 8 && tok < s.tok1 ? table[tok / p.page_size] : 0;
+        const unsigned bad = __ballot_sync(kFull, page < 0 || page >= p.num_pages);
+        if (j + 1 < n) {
+          good = scores(c + j + 1, j + 2 == n);
+          if (!good) break;
+        }
+        if (rank == 0) {
+          good = wait(L::P_READY, c + j);
+          if (!good) break;
+        }
+        const int valid = min(kPairTokens, s.tok1 - s.tok0 - j * kPairTokens);
+        for (int g = 0; g < L::NV; ++g) {
+          good = wait(L::V_FULL + 8 * g, c + j);
+          if (!good) break;
+          // rows to clear: the rest of the last 16 tokens, and those of bad pages
+          for (int u = 4 * g; u < 4 * g + 4; ++u) {
+            if (u * 16 >= valid) break;
+            const int from = bad >> u & 1 ? 0 : valid - u * 16;
+            if (from < 16) {
+              for (int x = lane; x < (16 - from) * 8 * 4; x += 32) {
+                const int b = x / ((16 - from) * 8), k = x % ((16 - from) * 8);
+                *reinterpret_cast<uint4*>(base + L::V + b * L::VBOX + (u * 16 + from) * 128 + k * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();  // the tensor core reads them (async proxy)
+            }
+          }
+          __syncwarp();
+          if (rank != 0) {
+            if (lane == 0) arrive_first_cta(sb + L::V_PEER + 8 * g);
+            continue;
+          }
+          good = wait(L::V_PEER + 8 * g, c + j);
+          if (!good) break;
+          if (lane == 0) {
+            tc5::fence_after();
+            for (int k = 4 * g; k < 4 * g + 4 && k * 16 < valid; ++k) {
+              const uint64_t ad = tc5::smem_desc(sb + L::P + (k >> 2) * L::PBOX + (k & 3) * 32, 16, 1024);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                mma_pair(t_o + (uint32_t)(128 * h), ad,
+                         tc5::smem_desc(sb + L::V + 2 * h * L::VBOX + k * 2048, L::VBOX, 1024), idesc_o,
+                         j > 0 || k > 0 ? 1u : 0u);
+            }
+            commit_pair(sb + L::V_FREE + 8 * g);
+          }
+          __syncwarp();
+        }
+        if (good && rank == 0 && lane == 0) commit_pair(sb + L::PV_DONE);
+      }
+      c += n;
+      ++qc;
+    }
+    if (!good && lane == 0) set_status(p.status, PA_DEV_TIMEOUT);
+    // every MMA issued has finished before either CTA goes on
+    if (rank == 0 && lane == 0) commit_pair(sb + L::DRAIN);
+    wait_cluster(sb + L::DRAIN, 0u, kDrainWaitNs);
+    __syncwarp();
+  } else {
+    // ================= softmax and output =================
+    const int row = (warp & 1) * 32 + lane;        // of the CTA's 64
+    const int half = warp >> 1;                    // tokens 64 half .. of a stage; the same part of O
+    const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
+    volatile float* xmax = reinterpret_cast<float*>(base + L::XMAX);  // [2 uses][2 halves][64 rows]
+    constexpr float kBias = std::is_same<T, __half>::value ? 7.f : 0.f;
+    bool good = true;  // after a wait that gave up, a warp only keeps its place in the pair barriers
+    int c = 0;
+    auto wait = [&](int bar, uint32_t parity) {
+      if (good) good = __all_sync(kFull, wait_cluster(sb + bar, parity, p.wait_ns));
+    };
+    for (int i = first; i < last; ++i) {
+      const LatentSegment s = p.segments[i];
+      if (!usable(s)) {
+        if (threadIdx.x == 0 && rank == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
+        continue;
+      }
+      const int32_t* table = p.block_table + (int64_t)s.b * p.max_pages;
+      const int n = stages_of(s);
+      const int cq = p.cu_q[s.b], qn = p.cu_q[s.b + 1] - cq, len = p.cu_k[s.b + 1] - p.cu_k[s.b];
+      const int trow = rank * kPairRows + row;     // of the tile
+      const int lim0 = trow < s.nrows ? len - qn + (s.row0 + trow) / p.heads : -1;  // last visible token
+      const bool idle = rank * kPairRows + (warp & 1) * 32 >= s.nrows;  // no row of the warp's is real
+      float m_run = -INFINITY, l_run = 0.f;
+      int nph[4];  // pages of the thread's 64 tokens, a stage ahead
+      auto load_pages = [&](int j) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int tok = s.tok0 + j * kPairTokens + half * 64 + u * 16;
+          nph[u] = -1;
+          if (!idle && tok < s.tok1)
+            asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(nph[u]) : "l"(table + tok / p.page_size));
+        }
+      };
+      load_pages(0);
+      for (int j = 0; j < n; ++j) {
+        const int cs = c + j;
+        if (!idle) {
+          bool ok_page[4];
+          bool all_ok = true;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            ok_page[u] = nph[u] >= 0 && nph[u] < p.num_pages;
+            all_ok = all_ok && ok_page[u];
+          }
+          if (j + 1 < n) load_pages(j + 1);
+          wait(L::S_DONE + 8 * (cs & 1), (uint32_t)((cs >> 1) & 1));
+          tc5::fence_after();
+          float sv[64];
+#pragma unroll
+          for (int x = 0; x < 64; x += 16) tc5::ld16(t_s + (uint32_t)(64 * (cs & 1) + x) + lane_off, sv + x);
+          tc5::wait_ld();
+          const int tok = s.tok0 + j * kPairTokens + half * 64;
+          const int lim = min(lim0, s.tok1 - 1) - tok;  // last visible column
+          if (!__all_sync(kFull, all_ok && lim >= 63)) {
+#pragma unroll
+            for (int x = 0; x < 64; ++x) sv[x] = ok_page[x / 16] && x <= lim ? sv[x] : -INFINITY;
+          }
+          float mx4[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+          for (int x = 4; x < 64; ++x) mx4[x & 3] = fmaxf(mx4[x & 3], sv[x]);
+          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.qscale;
+          // the maximum over both halves; two uses in turn, so one barrier a stage
+          volatile float* xm = xmax + (cs & 1) * 128;
+          xm[half * 64 + row] = mx;
+          row_pair_barrier(warp);
+          mx = fmaxf(mx, xm[(half ^ 1) * 64 + row]);
+          float al = 1.f;
+          bool resc = false;
+          if (mx > m_run + kPairLazyLog2) {
+            al = ex2(m_run - mx);  // 0 when the row had no weight yet
+            resc = m_run != -INFINITY;
+            m_run = mx;
+          }
+          const float nm = m_run == -INFINITY ? -INFINITY : kBias - m_run;  // no token yet: weights 0
+          const float2 qs2 = make_float2(p.qscale, p.qscale), nm2 = make_float2(nm, nm);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          uint32_t pk[32];
+#pragma unroll
+          for (int x = 0; x < 64; x += 2) {
+            const float2 e = ffma2(make_float2(sv[x], sv[x + 1]), qs2, nm2);
+            const float2 w = make_float2(ex2(e.x), ex2(e.y));
+            sum[(x >> 1) & 1] = fadd2(sum[(x >> 1) & 1], w);
+            pk[x >> 1] = Elem<T>::from_f2(w.x, w.y);
+          }
+          const float2 s2 = fadd2(sum[0], sum[1]);
+          l_run = l_run * al + (s2.x + s2.y);
+          // P and O are free once the product before is done
+          if (cs > 0) wait(L::PV_DONE, (uint32_t)((cs - 1) & 1));
+          tc5::fence_after();
+          unsigned char* pr = base + L::P + half * L::PBOX + row * 128;
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            *reinterpret_cast<uint4*>(pr + ((x ^ (row & 7)) << 4)) =
+                make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+          if (j > 0 && __any_sync(kFull, resc)) {
+            const float f = resc ? al : 1.f;
+#pragma unroll 4
+            for (int x = 0; x < 256; x += 16) {
+              float ov[16];
+              tc5::ld16(t_o + (uint32_t)x + lane_off, ov);
+              tc5::wait_ld();
+#pragma unroll
+              for (int y = 0; y < 16; ++y) ov[y] *= f;
+              tc5::st16(t_o + (uint32_t)x + lane_off, ov);
+            }
+            tc5::wait_st();
+          }
+          fence_proxy_async_smem();  // the tensor core reads P (async proxy)
+          tc5::fence_before();
+        } else if (cs > 0) {
+          wait(L::PV_DONE, (uint32_t)((cs - 1) & 1));
+        }
+        __syncwarp();
+        if (good && lane == 0) arrive_first_cta(sb + L::P_READY);
+      }
+      c += n;
+      wait(L::PV_DONE, (uint32_t)((c - 1) & 1));
+      if (!idle) {
+        // the row's sum over both halves, and whether both warps got here in order
+        volatile float* xs = xmax + (c & 1) * 128;
+        xs[half * 64 + row] = good ? l_run : -1.f;
+        row_pair_barrier(warp);
+        const float other = xs[(half ^ 1) * 64 + row];
+        const bool whole = good && !(other < 0.f);
+        const float l = l_run + other;
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a NaN sum stays NaN
+        const bool mine = trow < s.nrows;
+        const int64_t grow = (int64_t)cq * p.heads + s.row0 + trow;
+        const int64_t at = (int64_t)s.slot * p.rows + trow;
+        if (whole) {
+          tc5::fence_after();
+#pragma unroll 2
+          for (int x = 0; x < 256; x += 32) {
+            float ov[32];
+            tc5::ld16(t_o + (uint32_t)x + lane_off, ov);
+            tc5::ld16(t_o + (uint32_t)x + 16u + lane_off, ov + 16);
+            tc5::wait_ld();
+            const int dim = (x >> 7) * 256 + half * 128 + (x & 127);
+            if (mine && s.slot < 0) {
+              T* out = static_cast<T*>(p.out) + grow * kLatent + dim;
+#pragma unroll
+              for (int y = 0; y < 32; y += 8) {
+                uint4 w;
+                w.x = Elem<T>::from_f2(ov[y] * inv, ov[y + 1] * inv);
+                w.y = Elem<T>::from_f2(ov[y + 2] * inv, ov[y + 3] * inv);
+                w.z = Elem<T>::from_f2(ov[y + 4] * inv, ov[y + 5] * inv);
+                w.w = Elem<T>::from_f2(ov[y + 6] * inv, ov[y + 7] * inv);
+                *reinterpret_cast<uint4*>(out + y) = w;
+              }
+            } else if (mine) {
+              float* po = p.part_o + at * kLatent + dim;
+#pragma unroll
+              for (int y = 0; y < 32; y += 4)
+                *reinterpret_cast<float4*>(po + y) =
+                    make_float4(ov[y] * inv, ov[y + 1] * inv, ov[y + 2] * inv, ov[y + 3] * inv);
+            }
+          }
+        }
+        if (mine && s.slot >= 0 && half == 0)
+          // a row that was not written keeps its whole tile's row unwritten
+          p.part_lse[at] = !whole ? INFINITY : l > 0.f || l != l ? m_run + lg2(l) - kBias : -INFINITY;
+        if (!whole && lane == 0) set_status(p.status, PA_DEV_TIMEOUT);
+        tc5::fence_before();  // O is read before the next segment's first product
+        row_pair_barrier(warp);
+      }
+    }
+    if (!good && lane == 0) set_status(p.status, PA_DEV_TIMEOUT);
+  }
+
+  tc5::fence_before();
+  __syncthreads();
+  cluster_sync();  // nothing is in flight between the CTAs any more
+  if (warp == 4) {
+    tc5::fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+  cluster_sync();
+}
+
+bool encode_q(CUtensorMap* map, const LatentParams& p, int dtype) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {kLatentRow, (cuuint64_t)p.total_q * (cuuint64_t)p.heads};
+  cuuint64_t strides[1] = {kLatentRow * 2};
+  cuuint32_t box[2] = {64, kPairRows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType ty = dtype == PA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(map, ty, 2, const_cast<void*>(p.q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T>
+cudaError_t launch_t(const LatentParams& p, const CUtensorMap& q_map, cudaStream_t stream) {
+  static std::atomic<unsigned long long> configured{0};
+  return launch_pdl(latent_pair_kernel<T>, PLayout::BYTES, configured, p, 2 * p.num_ranges,
+                    kPairThreads, stream, q_map);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_pair(const LatentParams& p, int dtype, cudaStream_t stream) {
+  CUtensorMap q_map;
+  if (!encode_q(&q_map, p, dtype)) return cudaErrorInvalidValue;
+  if (dtype == PA_DTYPE_BF16) return launch_t<__nv_bfloat16>(p, q_map, stream);
+  return launch_t<__half>(p, q_map, stream);
+}
+
+}  // namespace pa

@@ -29,7 +29,7 @@ cudaError_t launch_latent_gather(const LatentRowsParams& p, cudaStream_t stream)
 
 // Absorbed attention.
 struct LatentParams {
-  CUtensorMap pages_map;  // the pool, boxes of 16 tokens
+  CUtensorMap pages_map;  // the pool, in the boxes of the plan's kernel
   const void* q;
   void* out;
   const int32_t* block_table;
@@ -49,6 +49,7 @@ struct LatentParams {
 };
 
 cudaError_t launch_latent_mma(const LatentParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_latent_pair(const LatentParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_latent_merge(const LatentParams& p, int dtype, cudaStream_t stream);
 
 // Expanded attention.

@@ -2,7 +2,7 @@
 //
 // Absorbed form.  A tile is up to `rows` consecutive query rows of one
 // sequence (its tokens x heads, which lie next to each other in q and out);
-// its work is the stages of 64 tokens its last row sees.  The GPU runs one
+// its work is the stages of 64 or 128 tokens its last row sees.  The GPU runs one
 // CTA (or CTA pair) per SM (pair of SMs), each of which takes one range of
 // the list of all tiles' stages: the list is cut into ranges of equal work,
 // wherever that falls, so that the CTAs end together whatever the lengths.
@@ -56,8 +56,6 @@ struct Work {
   int64_t slots = 0;
 };
 
-int64_t stages_of(int64_t tokens) { return (tokens + kLatentStage - 1) / kLatentStage; }
-
 // One tile's pieces: cuts (in stages, ascending, first 0 and last the tile's
 // stages) become segments; several of them a merge.
 struct AbsorbedTile {
@@ -66,6 +64,8 @@ struct AbsorbedTile {
 
 void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_t* qs,
                    const std::vector<int32_t>& cu_q, int rows, int workers, int forced, Work* w) {
+  const int64_t stage = rows == kLatentRowsPair ? kLatentStagePair : kLatentStage;
+  auto stages_of = [&](int64_t tokens) { return (tokens + stage - 1) / stage; };
   std::vector<AbsorbedTile> tiles;
   int64_t total = 0;
   for (int b = 0; b < s.batch; ++b) {
@@ -114,8 +114,8 @@ void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_
         take = std::min<int64_t>(take, std::max<int64_t>(left - kPieceStages, kMinPiece));
         if (n - at - take < kMinPiece) take = n - at;
       }
-      const int32_t tok1 = (int32_t)std::min<int64_t>((at + take) * kLatentStage, t.span);
-      w->segments.push_back({t.b, t.row0, t.nrows, (int32_t)(at * kLatentStage), tok1, -1, 0, 0});
+      const int32_t tok1 = (int32_t)std::min<int64_t>((at + take) * stage, t.span);
+      w->segments.push_back({t.b, t.row0, t.nrows, (int32_t)(at * stage), tok1, -1, 0, 0});
       at += take;
       left -= take + kPieceStages;
       total -= take + (at == n ? kPieceStages : 0);
@@ -169,7 +169,8 @@ extern "C" pa_status_t pa_latent_plan(const pa_latent_shape_t* shape, const int3
   if ((!absorbed && form != PA_LATENT_EXPANDED) || num_sms <= 0 || o.forced_splits < 0 ||
       o.rows_per_tile < 0)
     return PA_ERR_INVALID_ARG;
-  if (absorbed ? (o.rows_per_tile != 0 && o.rows_per_tile != kLatentRowsMma)
+  if (absorbed ? (o.rows_per_tile != 0 && o.rows_per_tile != kLatentRowsMma &&
+                  o.rows_per_tile != kLatentRowsPair)
                : (o.rows_per_tile != 0 || o.forced_splits != 0))
     return PA_ERR_INVALID_ARG;
   const int B = shape->batch;
@@ -188,9 +189,16 @@ extern "C" pa_status_t pa_latent_plan(const pa_latent_shape_t* shape, const int3
     cu_k[(size_t)b + 1] = cu_k[(size_t)b] + len;
   }
   Work w;
-  const int rows = absorbed ? kLatentRowsMma : kLatentRowsExpanded;
+  int rows = kLatentRowsExpanded;
+  if (absorbed) {
+    int64_t most = 0;  // query rows of one sequence
+    for (int b = 0; b < B; ++b)
+      most = std::max(most, (int64_t)q_lens_host[b] * shape->num_heads);
+    rows = o.rows_per_tile ? o.rows_per_tile : most <= kLatentRowsMma ? kLatentRowsMma : kLatentRowsPair;
+  }
   if (absorbed)
-    absorbed_work(*shape, seq_lens_host, q_lens_host, cu_q, rows, num_sms, o.forced_splits, &w);
+    absorbed_work(*shape, seq_lens_host, q_lens_host, cu_q, rows,
+                  rows == kLatentRowsPair ? std::max(1, num_sms / 2) : num_sms, o.forced_splits, &w);
   else
     expanded_work(*shape, seq_lens_host, q_lens_host, rows, &w);
   const size_t ranges = absorbed ? w.ranges.size() - 1 : w.tiles.size();

@@ -441,27 +441,8 @@ bool encode_rows(CUtensorMap* map, const void* ptr, int dtype, int width, int64_
 template <typename T, int D>
 cudaError_t launch_t(const LatentPrefillParams& p, const XMaps& maps, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
-  auto kern = latent_prefill_kernel<T, D>;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (!(configured.load() & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, XLayout<D>::BYTES);
-    if (e != cudaSuccess) return e;
-    configured.fetch_or(bit);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.num_tiles);
-  cfg.blockDim = dim3(kPrefillThreads);
-  cfg.dynamicSmemBytes = XLayout<D>::BYTES;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p, maps);
+  return launch_pdl(latent_prefill_kernel<T, D>, XLayout<D>::BYTES, configured, p, p.num_tiles,
+                    kPrefillThreads, stream, maps);
 }
 
 }  // namespace

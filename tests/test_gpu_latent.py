@@ -91,25 +91,33 @@ ABSORBED = [
     ([70, 513], [7, 2], 20, 128),                 # tiles that begin inside a token
     ([257, 31], [1, 31], 128, 64),
     ([2000, 333], [1, 4], 40, 16),
+    ([129, 128, 127, 192], [1, 2, 1, 1], 64, 32),  # ends at and around a stage of 128
 ]
 
 
+# the two kernels: 16-row tiles (mma.sync), 128-row tiles on SM pairs (tcgen05)
+both_kernels = pytest.mark.parametrize("rows", [16, 128], ids=["mma_sync", "tcgen05"])
+
+
+@both_kernels
 @pytest.mark.parametrize("splits", [0, 3])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("case", ABSORBED, ids=lambda c: f"L{c[0][:3]}_q{c[1][:2]}_H{c[2]}_S{c[3]}")
-def test_absorbed_parity(case, dtype, splits):
+def test_absorbed_parity(case, dtype, splits, rows):
     lens, qs, heads, page = case
     c = Case(lens, qs, heads=heads, page=page, dtype=dtype, seed=seed_of(case), poison=True)
-    d = Device(c, forced_splits=splits)
+    d = Device(c, forced_splits=splits, rows_per_tile=rows)
+    assert d.plan.c.rows_per_tile == rows
     out = d.attention()
     assert d.done() == 0
     want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), lens, qs, c.scale)
     assert_latent_close(out.double().cpu().numpy(), want, max(lens), dtype, str(case))
 
 
-def test_absorbed_planner_splits_and_reruns_give_the_same_bits():
+@both_kernels
+def test_absorbed_planner_splits_and_reruns_give_the_same_bits(rows):
     c = Case([20000, 777], [1, 1], heads=16, page=64, dtype="bf16", seed=8)
-    d = Device(c)
+    d = Device(c, rows_per_tile=rows)
     assert d.plan.c.num_merges >= 1
     a, b = d.attention(), d.attention()
     assert d.done() == 0
@@ -118,13 +126,14 @@ def test_absorbed_planner_splits_and_reruns_give_the_same_bits():
     assert_latent_close(a.double().cpu().numpy(), want, 20000, "bf16")
 
 
+@both_kernels
 @pytest.mark.parametrize("splits", [0, 2])
-def test_absorbed_bad_pages_are_left_out(splits):
+def test_absorbed_bad_pages_are_left_out(splits, rows):
     """One page of a sequence, every page of another (its rows get zeros)."""
     c = Case([200, 40, 90], [2, 1, 1], heads=5, page=16, seed=9)
     c.table[0, 3] = -1
     c.table[1, :3] = c.num_pages + 9
-    d = Device(c, forced_splits=splits)
+    d = Device(c, forced_splits=splits, rows_per_tile=rows)
     out = d.attention()
     assert d.done() == binding.PA_DEV_BAD_PAGE
     want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), c.lens, c.qs, c.scale,
@@ -133,24 +142,26 @@ def test_absorbed_bad_pages_are_left_out(splits):
     assert torch.all(out[2] == 0)
 
 
+@both_kernels
 @pytest.mark.parametrize("scale", [1e-4, 1.0])
-def test_absorbed_scale_extremes(scale):
+def test_absorbed_scale_extremes(scale, rows):
     """Near-uniform weights, and weights that are almost one-hot with scores of
     hundreds (the running maximum moves)."""
     c = Case([1200], [1], heads=16, page=16, seed=10, scale=scale)
-    d = Device(c)
+    d = Device(c, rows_per_tile=rows)
     out = d.attention()
     assert d.done() == 0
     want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), c.lens, c.qs, scale)
     assert_latent_close(out.double().cpu().numpy(), want, 1200, "fp16")
 
 
-def test_absorbed_offsets_past_32_bits():
+@both_kernels
+def test_absorbed_offsets_past_32_bits(rows):
     """Pages beyond 2^31 elements (and 4 GB) of the pool."""
     pages = 2**32 // (16 * ROW * 2) + 40000       # 5 GB
     c = Case([100, 300], [3, 1], heads=16, seed=11)
     base = pages - c.num_pages
-    d = Device(c)
+    d = Device(c, rows_per_tile=rows)
     big = torch.empty(pages, 16, ROW, dtype=torch.float16, device="cuda")
     big[base:] = d.pages
     assert base * 16 * ROW > 2**31
@@ -294,7 +305,8 @@ def test_decode_steps_over_a_growing_cache():
         assert_latent_close(out.double().cpu().numpy(), want, 131, "bf16", f"step {step}")
 
 
-def test_captured_step_replays_and_follows_a_new_upload():
+@both_kernels
+def test_captured_step_replays_and_follows_a_new_upload(rows):
     """append + attention in a CUDA graph; between replays a plan of the same
     structure is uploaded (longer sequences), two graphs on workspaces of their
     own run on two streams at once."""
@@ -303,7 +315,9 @@ def test_captured_step_replays_and_follows_a_new_upload():
     graphs = []
     for _ in range(2):
         d = Device(c, forced_splits=2)
-        plans = [binding.LatentPlan(d.shape, x, [1, 1], 152, forced_splits=2) for x in (lens0, lens1)]
+        plans = [binding.LatentPlan(d.shape, x, [1, 1], 152, forced_splits=2, rows_per_tile=rows)
+                 for x in (lens0, lens1)]
+        d.ws = binding.alloc_workspace(plans[0])
         assert plans[0].c.blob_bytes == plans[1].c.blob_bytes
         d.plan = plans[0]
         d.out = torch.empty(2, 16, LATENT, dtype=DT["fp16"], device="cuda")
@@ -359,21 +373,39 @@ def test_workspace_of_another_plan_is_flagged():
     assert torch.equal(d.pages.cpu(), c.pages)
 
 
+@both_kernels
 @pytest.mark.parametrize("splits", [1, 4])
-def test_waits_that_run_out_are_reported(splits):
+def test_waits_that_run_out_are_reported(splits, rows):
     """One nanosecond per wait: rows are left as they were or right, the status
     says so, and the next call with the default limit is right."""
     c = Case([900, 1500, 30], [1, 1, 1], heads=16, seed=21)
-    d = Device(c, forced_splits=splits, wait_limit_ns=1)
+    d = Device(c, forced_splits=splits, rows_per_tile=rows, wait_limit_ns=1)
     out = d.attention()
+    assert d.done() == binding.PA_DEV_TIMEOUT
+    got = out.double().cpu().numpy()
+    left = np.isnan(got).all(axis=-1)
+    assert np.array_equal(left, np.isnan(got).any(axis=-1)) and left.any()
+    want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), c.lens, c.qs, c.scale)
+    keep = tuple(x[~left] for x in want)
+    assert_latent_close(got[~left], keep, 1500, "fp16")
+    d2 = Device(c, forced_splits=splits, rows_per_tile=rows)
+    out = d2.attention()
+    assert d2.done() == 0
+    assert_latent_close(out.double().cpu().numpy(), want, 1500, "fp16")
+
+
+def test_expanded_waits_that_run_out_are_reported():
+    c = Case([900, 300], [900, 40], heads=3, seed=22)
+    d = Device(c, form="expanded", wait_limit_ns=1)
+    out = d.prefill()
     assert d.done() == binding.PA_DEV_TIMEOUT
     got = out.double().cpu().numpy()
     rows = np.isnan(got).all(axis=-1)
     assert np.array_equal(rows, np.isnan(got).any(axis=-1)) and rows.any()
-    want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), c.lens, c.qs, c.scale)
-    keep = tuple(x[~rows] for x in want)
-    assert_latent_close(got[~rows], keep, 1500, "fp16")
-    d2 = Device(c, forced_splits=splits)
-    out = d2.attention()
+    want = oracle.latent_prefill(f64(c.qx), f64(c.k), f64(c.rows[:, LATENT:]), f64(c.v), c.lens, c.qs,
+                                 c.scale)
+    assert_latent_close(got[~rows], tuple(x[~rows] for x in want), 900, "fp16")
+    d2 = Device(c, form="expanded")
+    out = d2.prefill()
     assert d2.done() == 0
-    assert_latent_close(out.double().cpu().numpy(), want, 1500, "fp16")
+    assert_latent_close(out.double().cpu().numpy(), want, 900, "fp16")
