@@ -20,8 +20,8 @@
 //              32 (warp % 2) + lane of the CTA's 64: tokens 0-63 of the stage
 //              in warps 0-1, 64-127 in warps 2-3; the two threads of a row
 //              exchange their maxima through shared memory.
-//   warp 4:    in the pair's first CTA issues the MMAs of both; in the second
-//              tells the first when its buffers have landed
+//   warp 4:    in the pair's first CTA issues the MMAs of both; in either
+//              clears value rows
 //   warp 5:    copies q and K;  warp 6: copies V
 // Per stage j: S(j+1) = q K^T into one of two TMEM buffers; softmax(j);
 // O += P(j) V(j), P from shared memory [2 boxes of 64 tokens][64 rows][128 B].
@@ -60,20 +60,22 @@ struct PLayout {
   static constexpr int P = V + 4 * VBOX;
   static constexpr int PBOX = kPairRows * 128;
   static constexpr int BARS = P + 2 * PBOX;
-  // mbarriers.  In both CTAs:
-  static constexpr int Q_FULL = BARS;
-  static constexpr int K_FULL = Q_FULL + 8;               // NG
-  static constexpr int V_FULL = K_FULL + 8 * NG;          // NV
-  static constexpr int Q_FREE = V_FULL + 8 * NV;
+  // mbarriers that the MMAs arrive on, in both CTAs
+  static constexpr int Q_FREE = BARS;
   static constexpr int K_FREE = Q_FREE + 8;               // NG
   static constexpr int V_FREE = K_FREE + 8 * NG;          // NV
   static constexpr int S_DONE = V_FREE + 8 * NV;          // 2
   static constexpr int PV_DONE = S_DONE + 16;
   static constexpr int DRAIN = PV_DONE + 8;
-  // used in the first CTA only: the other CTA's buffers, the weights of both
-  static constexpr int Q_PEER = DRAIN + 8;
-  static constexpr int K_PEER = Q_PEER + 8;               // NG
-  static constexpr int V_PEER = K_PEER + 8 * NG;          // NV
+  // in the first CTA: the copies of both have landed
+  static constexpr int Q_FULL = DRAIN + 8;
+  static constexpr int K_FULL = Q_FULL + 8;               // NG
+  static constexpr int V_FULL = K_FULL + 8 * NG;          // NV
+  // values with rows to clear: landed in the second CTA (there), cleared in
+  // it (in the first CTA)
+  static constexpr int V_HERE = V_FULL + 8 * NV;          // NV
+  static constexpr int V_PEER = V_HERE + 8 * NV;          // NV
+  // in the first CTA: the weights of both are written
   static constexpr int P_READY = V_PEER + 8 * NV;
   static constexpr int TMEM_SLOT = P_READY + 8;
   static constexpr int XMAX = align_up(TMEM_SLOT + 8, 16);  // [2][128] floats: row maxima, sums
@@ -101,21 +103,52 @@ __device__ __forceinline__ void arrive_first_cta(uint32_t bar) {
       : "memory");
 }
 
-// A bounded wait that acquires what the other CTA released.
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  const uint64_t t0 = global_timer_ns();
-  for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(limit_ns < kShortWaitNs ? 0u : kSuspendHintNs)
-        : "memory");
-    if (ok) return true;
-    if (global_timer_ns() - t0 > limit_ns) return false;
+// A bounded wait of the whole warp: one lane polls, so that waiting warps
+// leave shared memory and the issue slots to the copies and the others.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  bool ok = false;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait_bounded_sleep(bar, parity, limit_ns);
+  return __shfl_sync(kFull, ok, 0);
+}
+
+// The same for a barrier that the other CTA's threads arrive on: acquires
+// what they released.
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  bool good = false;
+  if ((threadIdx.x & 31) == 0) {
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+      uint32_t ok;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(bar), "r"(parity), "r"(limit_ns < kShortWaitNs ? 0u : kSuspendHintNs)
+          : "memory");
+      good = ok != 0;
+      if (good || global_timer_ns() - t0 > limit_ns) break;
+    }
   }
+  return __shfl_sync(kFull, good, 0);
+}
+
+// The address of this offset of the first CTA's shared memory.
+__device__ __forceinline__ uint32_t in_first_cta(uint32_t addr) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+
+// TMA copies into this CTA whose barrier may be the other CTA's.
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                                 int c2, int c3, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2.L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar),
+      "l"(policy)
+      : "memory");
 }
 
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
@@ -136,11 +169,11 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
-                                            uint32_t bar, uint64_t policy) {
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                                 uint32_t bar, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      ".cta_group::2.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
       : "memory");
 }
@@ -164,7 +197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.pages_map)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&q_map)) : "memory");
-    for (int b = L::Q_FULL; b < L::P_READY; b += 8) mbar_init(sb + b, 1);
+    for (int b = L::Q_FREE; b < L::P_READY; b += 8) mbar_init(sb + b, 1);
     mbar_init(sb + L::P_READY, 8);
     fence_barrier_init();
   }
@@ -204,115 +237,112 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   if (warp == 5 || warp == 6) {
     // ================= copies =================
-    // Stages are counted over all segments: use c of a buffer has parity c & 1.
+    // Stages are counted over all segments: use c of a buffer has parity
+    // c & 1.  The copies of both CTAs complete on the first CTA's barriers,
+    // whose own copy warps announce the bytes of both.
     const bool keys = warp == 5;
     int c = 0, qc = 0;
     bool good = true;
-    const uint64_t policy = l2_evict_first_policy();
-    const uint64_t keep = tc5::l2_evict_normal_policy();
+    const uint64_t once = l2_evict_first_policy(), keep = tc5::l2_evict_normal_policy();
     const int box = p.page_size < 64 ? p.page_size : 64;  // tokens of one copy
+    const int copies = kPairTokens / box;                 // of a stage
     const int groups = keys ? L::NG : L::NV;
-    int issued[3] = {0, 0, 0};  // uses of each group
+    const uint32_t full0 = in_first_cta(sb + (keys ? L::K_FULL : L::V_FULL));
     for (int i = first; i < last && good; ++i) {
       const LatentSegment s = p.segments[i];
       if (!usable(s)) continue;
       const int32_t* table = p.block_table + (int64_t)s.b * p.max_pages;
       if (keys) {  // q: the CTA's 64 rows
-        if (lane == 0) {
-          good = qc == 0 || wait_cluster(sb + L::Q_FREE, (uint32_t)((qc - 1) & 1), p.wait_ns);
-          if (good) {
-            mbar_arrive_expect_tx(sb + L::Q_FULL, 9 * L::QBOX);
-            const int row = (int)((int64_t)p.cu_q[s.b] * p.heads + s.row0) + rank * kPairRows;
-            for (int b = 0; b < 9; ++b)
-              tma_load_2d(sb + L::Q + b * L::QBOX, &q_map, b * 64, row, sb + L::Q_FULL, policy);
-          }
-        }
-        good = __shfl_sync(kFull, good, 0);
+        good = qc == 0 || warp_wait(sb + L::Q_FREE, (uint32_t)((qc - 1) & 1), p.wait_ns);
         if (!good) break;
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive_expect_tx(sb + L::Q_FULL, 2 * 9 * L::QBOX);
+          const int row = (int)((int64_t)p.cu_q[s.b] * p.heads + s.row0) + rank * kPairRows;
+          const uint32_t bar = in_first_cta(sb + L::Q_FULL);
+          for (int b = 0; b < 9; ++b)
+            tma_load_2d_pair(sb + L::Q + b * L::QBOX, &q_map, b * 64, row, bar, once);
+        }
         ++qc;
       }
       const int n = stages_of(s);
       for (int j = 0; j < n && good; ++j, ++c) {
-        // lane u: the page of copy u (its tokens: the CTA's half of the stage, or all of it)
-        const int copies = (keys ? 64 : kPairTokens) / box;
-        const int tok = s.tok0 + j * kPairTokens + (keys ? rank * 64 : 0) + lane * box;
-        int page = -1;
-        if (lane < copies && tok < s.tok1) {
-          page = table[tok / p.page_size];
-          if (page < 0 || page >= p.num_pages) {
-            page = -1;
-            set_status(p.status, PA_DEV_BAD_PAGE);
-          }
-        }
+        // lane u: the page of tokens u * box .. of the stage
+        const int tok = s.tok0 + j * kPairTokens + lane * box;
+        const bool wanted = lane < copies && tok < s.tok1;
+        int page = wanted ? table[tok / p.page_size] : -1;
+        if (page >= p.num_pages) page = -1;
+        if (wanted && page < 0) set_status(p.status, PA_DEV_BAD_PAGE);
         const unsigned have = __ballot_sync(kFull, page >= 0);
-        for (int g = 0; g < groups && good; ++g) {
-          const int free_bar = (keys ? L::K_FREE : L::V_FREE) + 8 * g;
-          const uint32_t full = sb + (keys ? L::K_FULL : L::V_FULL) + 8 * g;
-          good = c == 0 || __all_sync(kFull, wait_cluster(sb + free_bar, (uint32_t)((c - 1) & 1), p.wait_ns));
+        const unsigned missing = __ballot_sync(kFull, wanted && page < 0);
+        const int row = tok % p.page_size;
+        const int valid = min(kPairTokens, s.tok1 - s.tok0 - j * kPairTokens);
+        for (int g = 0; g < groups; ++g) {
+          good = c == 0 || warp_wait(sb + (keys ? L::K_FREE : L::V_FREE) + 8 * g,
+                                     (uint32_t)((c - 1) & 1), p.wait_ns);
           if (!good) break;
-          // copies of this group: every one for three boxes of K, half of them for four of V
-          const int per = copies / (keys ? 1 : L::NV);
-          const unsigned mine = keys ? have : have >> (g * per) & ((1u << per) - 1u);
-          if (lane == 0) {
-            if (mine)
-              mbar_arrive_expect_tx(full, (uint32_t)(__popc(mine) * box * 128 * (keys ? 3 : 4)));
-            else
-              mbar_arrive(full);
-          }
-          __syncwarp();
-          const int u0 = keys ? 0 : g * per;
-          if (lane >= u0 && lane < u0 + per && page >= 0) {  // each lane issues its own copies
-            const int row = tok % p.page_size;
-            if (keys) {
+          if (keys) {  // three boxes of the CTA's half of the tokens
+            if (rank == 0 && lane == 0) {
+              const uint32_t bytes = (uint32_t)(__popc(have) * box * 128 * 3);
+              if (bytes) mbar_arrive_expect_tx(sb + L::K_FULL + 8 * g, bytes);
+              else mbar_arrive(sb + L::K_FULL + 8 * g);
+            }
+            const int u = lane - rank * (copies / 2);  // of the half
+            if (page >= 0 && u >= 0 && u < copies / 2)
 #pragma unroll
               for (int b = 0; b < 3; ++b)
-                tma_load_4d(sb + L::K + (3 * g + b) * L::KBOX + lane * box * 128, &p.pages_map, 0,
-                            3 * g + b, row, page, full, keep);
-            } else {
+                tma_load_4d_pair(sb + L::K + (3 * g + b) * L::KBOX + u * box * 128, &p.pages_map, 0,
+                                 3 * g + b, row, page, full0 + 8 * g, keep);
+          } else {     // four boxes, the CTA's half of the values, of 64 tokens
+            const int per = copies / L::NV;
+            const unsigned mask = ((1u << per) - 1u) << (g * per);
+            // rows to clear: the second CTA's copies complete on its own barrier
+            const bool clear = (missing & mask) != 0 || (valid % kLatentBlock != 0 && (valid - 1) / 64 == g);
+            const uint32_t bytes = (uint32_t)(__popc(have & mask) * box * 128 * 4);
+            if (lane == 0 && (rank == 0 || clear)) {
+              const uint32_t bar = sb + (rank == 0 ? L::V_FULL : L::V_HERE) + 8 * g;
+              if (bytes) mbar_arrive_expect_tx(bar, rank == 0 && !clear ? 2 * bytes : bytes);
+              else mbar_arrive(bar);
+            }
+            const uint32_t bar = rank != 0 && clear ? sb + L::V_HERE + 8 * g : full0 + 8 * g;
+            __syncwarp();
+            if (page >= 0 && (mask >> lane & 1))
 #pragma unroll
               for (int b = 0; b < 4; ++b)
-                tma_load_4d(sb + L::V + b * L::VBOX + lane * box * 128, &p.pages_map, 0,
-                            (b >> 1) * 4 + rank * 2 + (b & 1), row, page, full, keep);
-            }
+                tma_load_4d_pair(sb + L::V + b * L::VBOX + lane * box * 128, &p.pages_map, 0,
+                                 (b >> 1) * 4 + rank * 2 + (b & 1), row, page, bar, keep);
           }
-          issued[g] = c + 1;
           __syncwarp();
         }
       }
     }
     if (!good && lane == 0) set_status(p.status, PA_DEV_TIMEOUT);
-    // every copy has landed, and every arrival that the MMAs send here, before
-    // the CTA ends
-    for (int g = 0; g < groups; ++g)
-      if (issued[g] > 0) {
-        mbar_wait_bounded_sleep(sb + (keys ? L::K_FULL : L::V_FULL) + 8 * g,
-                                (uint32_t)((issued[g] - 1) & 1), kDrainWaitNs);
-        wait_cluster(sb + (keys ? L::K_FREE : L::V_FREE) + 8 * g, (uint32_t)((issued[g] - 1) & 1),
-                     kDrainWaitNs);
-      }
-    if (keys && qc > 0) {
-      mbar_wait_bounded_sleep(sb + L::Q_FULL, (uint32_t)((qc - 1) & 1), kDrainWaitNs);
-      wait_cluster(sb + L::Q_FREE, (uint32_t)((qc - 1) & 1), kDrainWaitNs);
-    }
+    // every copy has been read, and with it every arrival that the MMAs send
+    // here has come, before the CTA ends
+    if (lane == 0 && c > 0)
+      for (int g = 0; g < groups; ++g)
+        mbar_wait_bounded_sleep(sb + (keys ? L::K_FREE : L::V_FREE) + 8 * g, (uint32_t)((c - 1) & 1),
+                                kDrainWaitNs);
+    if (lane == 0 && keys && qc > 0)
+      mbar_wait_bounded_sleep(sb + L::Q_FREE, (uint32_t)((qc - 1) & 1), kDrainWaitNs);
     __syncwarp();
   } else if (warp == 4) {
-    // ================= MMAs (first CTA), news of the buffers (second) =================
+    // ================= MMAs (first CTA) =================
+    // The second CTA's warp only clears value rows.
     const uint32_t idesc_s = tc5::instr_desc<T>(128, kPairTokens, false);
     const uint32_t idesc_o = tc5::instr_desc<T>(128, 256, true);
     bool good = true;
-    int c = 0, qc = 0;  // stages, segments
+    int c = 0, qc = 0;             // stages, segments
+    int cleared[L::NV] = {0, 0};   // uses of each value group with rows to clear
     auto wait = [&](int bar, int count) {
-      return __all_sync(kFull, wait_cluster(sb + bar, (uint32_t)(count & 1), p.wait_ns)) != 0;
+      return warp_wait(sb + bar, (uint32_t)(count & 1), p.wait_ns);
     };
-    // S of stage number cs: the group's buffers of both CTAs, then its MMAs
+    auto wait_peer = [&](int bar, int count) {
+      return warp_wait_cluster(sb + bar, (uint32_t)(count & 1), p.wait_ns);
+    };
+    // S of stage number cs
     auto scores = [&](int cs, bool last_of_segment) {
       for (int g = 0; g < L::NG; ++g) {
         if (!wait(L::K_FULL + 8 * g, cs)) return false;
-        if (rank != 0) {
-          if (lane == 0) arrive_first_cta(sb + L::K_PEER + 8 * g);
-          continue;
-        }
-        if (!wait(L::K_PEER + 8 * g, cs)) return false;
         if (lane == 0) {
           tc5::fence_after();
 #pragma unroll
@@ -325,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         __syncwarp();
       }
-      if (rank == 0 && lane == 0) {
+      if (lane == 0) {
         commit_pair(sb + L::S_DONE + 8 * (cs & 1));
         if (last_of_segment) commit_pair(sb + L::Q_FREE);
       }
@@ -336,47 +366,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (!usable(s)) continue;
       const int32_t* table = p.block_table + (int64_t)s.b * p.max_pages;
       const int n = stages_of(s);
-      good = wait(L::Q_FULL, qc);
-      if (good && rank != 0 && lane == 0) arrive_first_cta(sb + L::Q_PEER);
-      if (good && rank == 0) good = wait(L::Q_PEER, qc);
-      good = good && scores(c, n == 1);
+      if (rank == 0) good = wait(L::Q_FULL, qc) && scores(c, n == 1);
       for (int j = 0; j < n && good; ++j) {
         // lane u < 8: is the page of tokens 16 u .. of the stage bad?
         const int tok = s.tok0 + j * kPairTokens + lane * kLatentBlock;
         const int page = lane < 8 && tok < s.tok1 ? table[tok / p.page_size] : 0;
         const unsigned bad = __ballot_sync(kFull, page < 0 || page >= p.num_pages);
-        if (j + 1 < n) {
-          good = scores(c + j + 1, j + 2 == n);
-          if (!good) break;
-        }
-        if (rank == 0) {
-          good = wait(L::P_READY, c + j);
-          if (!good) break;
-        }
         const int valid = min(kPairTokens, s.tok1 - s.tok0 - j * kPairTokens);
+        if (rank == 0) {
+          if (j + 1 < n) good = scores(c + j + 1, j + 2 == n);
+          good = good && wait_peer(L::P_READY, c + j);
+          if (!good) break;
+        }
         for (int g = 0; g < L::NV; ++g) {
-          good = wait(L::V_FULL + 8 * g, c + j);
+          const bool clear =
+              (bad >> (4 * g) & 15) != 0 || (valid % kLatentBlock != 0 && (valid - 1) / 64 == g);
+          if (rank != 0 && !clear) continue;
+          good = rank == 0 ? wait(L::V_FULL + 8 * g, c + j) : wait(L::V_HERE + 8 * g, cleared[g]);
           if (!good) break;
-          // rows to clear: the rest of the last 16 tokens, and those of bad pages
-          for (int u = 4 * g; u < 4 * g + 4; ++u) {
-            if (u * 16 >= valid) break;
-            const int from = bad >> u & 1 ? 0 : valid - u * 16;
-            if (from < 16) {
-              for (int x = lane; x < (16 - from) * 8 * 4; x += 32) {
-                const int b = x / ((16 - from) * 8), k = x % ((16 - from) * 8);
-                *reinterpret_cast<uint4*>(base + L::V + b * L::VBOX + (u * 16 + from) * 128 + k * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+          if (clear) {  // the rest of the last 16 tokens, and the tokens of bad pages
+            for (int u = 4 * g; u < 4 * g + 4 && u * kLatentBlock < valid; ++u) {
+              const int from = bad >> u & 1 ? 0 : valid - u * kLatentBlock, rows = kLatentBlock - from;
+              for (int x = lane; x < rows * 8 * 4; x += 32) {
+                const int b = x / (rows * 8), k = x % (rows * 8);
+                *reinterpret_cast<uint4*>(base + L::V + b * L::VBOX + (u * kLatentBlock + from) * 128 +
+                                          k * 16) = make_uint4(0u, 0u, 0u, 0u);
               }
-              fence_proxy_async_smem();  // the tensor core reads them (async proxy)
             }
+            fence_proxy_async_smem();  // the tensor core reads them (async proxy)
+            __syncwarp();
+            if (rank != 0) {
+              if (lane == 0) arrive_first_cta(sb + L::V_PEER + 8 * g);
+            } else {
+              good = wait_peer(L::V_PEER + 8 * g, cleared[g]);
+            }
+            ++cleared[g];
+            if (!good) break;
           }
-          __syncwarp();
-          if (rank != 0) {
-            if (lane == 0) arrive_first_cta(sb + L::V_PEER + 8 * g);
-            continue;
-          }
-          good = wait(L::V_PEER + 8 * g, c + j);
-          if (!good) break;
+          if (rank != 0) continue;
           if (lane == 0) {
             tc5::fence_after();
             for (int k = 4 * g; k < 4 * g + 4 && k * 16 < valid; ++k) {
@@ -399,8 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (!good && lane == 0) set_status(p.status, PA_DEV_TIMEOUT);
     // every MMA issued has finished before either CTA goes on
     if (rank == 0 && lane == 0) commit_pair(sb + L::DRAIN);
-    wait_cluster(sb + L::DRAIN, 0u, kDrainWaitNs);
-    __syncwarp();
+    warp_wait(sb + L::DRAIN, 0u, kDrainWaitNs);
   } else {
     // ================= softmax and output =================
     const int row = (warp & 1) * 32 + lane;        // of the CTA's 64
@@ -411,7 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     bool good = true;  // after a wait that gave up, a warp only keeps its place in the pair barriers
     int c = 0;
     auto wait = [&](int bar, uint32_t parity) {
-      if (good) good = __all_sync(kFull, wait_cluster(sb + bar, parity, p.wait_ns));
+      if (good) good = warp_wait(sb + bar, parity, p.wait_ns);
     };
     for (int i = first; i < last; ++i) {
       const LatentSegment s = p.segments[i];

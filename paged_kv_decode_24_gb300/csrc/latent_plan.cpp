@@ -84,16 +84,17 @@ void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_
   }
   const int64_t by_work = std::max<int64_t>(1, total / (kMinRange + kPieceStages));
   const int64_t ranges = std::min<int64_t>(workers, by_work);
-  // each range gets an equal share of what is left when it is opened, the
-  // last one all of it
-  int64_t quota = (total + ranges - 1) / ranges;
+  // each range gets an equal share of what is left when it is opened, where
+  // every range but the last is expected to end in a cut, a piece more
+  auto share = [&](int64_t open) { return (total + kPieceStages * (open - 1) + open - 1) / open; };
+  int64_t quota = share(ranges);
   int64_t left = quota;  // of the range that is being filled
   w->ranges.push_back(0);
   auto close = [&] {
     if (w->ranges.back() != (int32_t)w->segments.size())
       w->ranges.push_back((int32_t)w->segments.size());
     const int64_t open = std::max<int64_t>(1, ranges - ((int64_t)w->ranges.size() - 1));
-    left = quota = (total + open - 1) / open;
+    left = quota = share(open);
   };
   for (const AbsorbedTile& t : tiles) {
     const int64_t n = stages_of(t.span);
