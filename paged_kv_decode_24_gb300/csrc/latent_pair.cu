@@ -36,7 +36,7 @@
 #include <math.h>
 
 #include "latent_segment.cuh"
-#include "prefill_tc5.cuh"
+#include "latent_tc5.cuh"
 #include "split_launch.cuh"
 
 namespace pa {
@@ -46,6 +46,7 @@ namespace {
 constexpr int kPairRows = 64;          // rows of one CTA
 constexpr int kPairTokens = 128;       // tokens of a stage
 constexpr int kPairThreads = 7 * 32;
+constexpr int kPrefetchStages = 2;     // how far ahead L2 is asked for rows
 constexpr float kPairLazyLog2 = 8.f;   // the maximum is raised when it grows by more than 2^8
 static_assert(kLatentRowsPair == 2 * kPairRows && kLatentStagePair == kPairTokens, "plan and kernel");
 
@@ -95,42 +96,17 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // Arrive on the first CTA's barrier at this offset of its shared memory.
+// What the arrival announces (weights, cleared values) lies in the arriving
+// CTA's shared memory and is read there by its own tensor core, so it is
+// fence.proxy.async before the arrival that makes it visible, and neither side
+// needs a cluster-wide fence (measured at 0.7 us each, on the path of every
+// stage).
 __device__ __forceinline__ void arrive_first_cta(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .b32 ra;\n\t"
       "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n\t}" ::"r"(bar)
+      "mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}" ::"r"(bar)
       : "memory");
-}
-
-// A bounded wait of the whole warp: one lane polls, so that waiting warps
-// leave shared memory and the issue slots to the copies and the others.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  bool ok = false;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait_bounded_sleep(bar, parity, limit_ns);
-  return __shfl_sync(kFull, ok, 0);
-}
-
-// The same for a barrier that the other CTA's threads arrive on: acquires
-// what they released.
-__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  bool good = false;
-  if ((threadIdx.x & 31) == 0) {
-    const uint64_t t0 = global_timer_ns();
-    for (;;) {
-      uint32_t ok;
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(bar), "r"(parity), "r"(limit_ns < kShortWaitNs ? 0u : kSuspendHintNs)
-          : "memory");
-      good = ok != 0;
-      if (good || global_timer_ns() - t0 > limit_ns) break;
-    }
-  }
-  return __shfl_sync(kFull, good, 0);
 }
 
 // The address of this offset of the first CTA's shared memory.
@@ -148,24 +124,6 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap
       ".cta_group::2.L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar),
       "l"(policy)
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// The barrier at this offset in both CTAs, once every MMA issued so far is done.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
       : "memory");
 }
 
@@ -253,7 +211,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (!usable(s)) continue;
       const int32_t* table = p.block_table + (int64_t)s.b * p.max_pages;
       if (keys) {  // q: the CTA's 64 rows
-        good = qc == 0 || warp_wait(sb + L::Q_FREE, (uint32_t)((qc - 1) & 1), p.wait_ns);
+        good = qc == 0 || tc5::warp_wait(sb + L::Q_FREE, (uint32_t)((qc - 1) & 1), p.wait_ns);
         if (!good) break;
         if (lane == 0) {
           if (rank == 0) mbar_arrive_expect_tx(sb + L::Q_FULL, 2 * 9 * L::QBOX);
@@ -274,10 +232,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (wanted && page < 0) set_status(p.status, PA_DEV_BAD_PAGE);
         const unsigned have = __ballot_sync(kFull, page >= 0);
         const unsigned missing = __ballot_sync(kFull, wanted && page < 0);
+        // The loads from HBM take longer than the buffers here can cover: ask L2
+        // for the rows of a later stage (each CTA for its half of the tokens)
+        if (keys) {
+          const int ahead = tok + kPrefetchStages * kPairTokens;
+          const int u = lane - rank * (copies / 2);
+          if (u >= 0 && u < copies / 2 && ahead < s.tok1) {
+            const int pg = table[ahead / p.page_size];
+            if (pg >= 0 && pg < p.num_pages)
+              prefetch_l2_bulk(static_cast<const T*>(p.pages) +
+                                   ((int64_t)pg * p.page_size + ahead % p.page_size) * kLatentRow,
+                               (uint32_t)(box * kLatentRow * 2));
+          }
+        }
         const int row = tok % p.page_size;
         const int valid = min(kPairTokens, s.tok1 - s.tok0 - j * kPairTokens);
         for (int g = 0; g < groups; ++g) {
-          good = c == 0 || warp_wait(sb + (keys ? L::K_FREE : L::V_FREE) + 8 * g,
+          good = c == 0 || tc5::warp_wait(sb + (keys ? L::K_FREE : L::V_FREE) + 8 * g,
                                      (uint32_t)((c - 1) & 1), p.wait_ns);
           if (!good) break;
           if (keys) {  // three boxes of the CTA's half of the tokens
@@ -330,34 +301,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // The second CTA's warp only clears value rows.
     const uint32_t idesc_s = tc5::instr_desc<T>(128, kPairTokens, false);
     const uint32_t idesc_o = tc5::instr_desc<T>(128, 256, true);
+    const uint64_t q_desc = tc5::smem_desc(sb + L::Q, 16, 1024), k_desc = tc5::smem_desc(sb + L::K, 16, 1024);
+    const uint64_t p_desc = tc5::smem_desc(sb + L::P, 16, 1024);
+    const uint64_t v_desc = tc5::smem_desc(sb + L::V, L::VBOX, 1024);
     bool good = true;
     int c = 0, qc = 0;             // stages, segments
     int cleared[L::NV] = {0, 0};   // uses of each value group with rows to clear
     auto wait = [&](int bar, int count) {
-      return warp_wait(sb + bar, (uint32_t)(count & 1), p.wait_ns);
-    };
-    auto wait_peer = [&](int bar, int count) {
-      return warp_wait_cluster(sb + bar, (uint32_t)(count & 1), p.wait_ns);
+      return tc5::warp_wait(sb + bar, (uint32_t)(count & 1), p.wait_ns);
     };
     // S of stage number cs
     auto scores = [&](int cs, bool last_of_segment) {
+#pragma unroll
       for (int g = 0; g < L::NG; ++g) {
         if (!wait(L::K_FULL + 8 * g, cs)) return false;
-        if (lane == 0) {
+        if (tc5::elect_one()) {
           tc5::fence_after();
 #pragma unroll
           for (int k = 12 * g; k < 12 * g + 12; ++k)
-            mma_pair(t_s + (uint32_t)(64 * (cs & 1)),
-                     tc5::smem_desc(sb + L::Q + (k >> 2) * L::QBOX + (k & 3) * 32, 16, 1024),
-                     tc5::smem_desc(sb + L::K + (k >> 2) * L::KBOX + (k & 3) * 32, 16, 1024),
-                     idesc_s, k > 0 ? 1u : 0u);
-          commit_pair(sb + L::K_FREE + 8 * g);
+            tc5::mma2(t_s + (uint32_t)(64 * (cs & 1)),
+                      tc5::desc_at(q_desc, (k >> 2) * L::QBOX + (k & 3) * 32),
+                      tc5::desc_at(k_desc, (k >> 2) * L::KBOX + (k & 3) * 32), idesc_s, k > 0 ? 1u : 0u);
+          tc5::commit2(sb + L::K_FREE + 8 * g);
+          if (g == L::NG - 1) {
+            tc5::commit2(sb + L::S_DONE + 8 * (cs & 1));
+            if (last_of_segment) tc5::commit2(sb + L::Q_FREE);
+          }
         }
         __syncwarp();
-      }
-      if (lane == 0) {
-        commit_pair(sb + L::S_DONE + 8 * (cs & 1));
-        if (last_of_segment) commit_pair(sb + L::Q_FREE);
       }
       return true;
     };
@@ -375,9 +346,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int valid = min(kPairTokens, s.tok1 - s.tok0 - j * kPairTokens);
         if (rank == 0) {
           if (j + 1 < n) good = scores(c + j + 1, j + 2 == n);
-          good = good && wait_peer(L::P_READY, c + j);
+          good = good && wait(L::P_READY, c + j);
           if (!good) break;
         }
+#pragma unroll
         for (int g = 0; g < L::NV; ++g) {
           const bool clear =
               (bad >> (4 * g) & 15) != 0 || (valid % kLatentBlock != 0 && (valid - 1) / 64 == g);
@@ -398,35 +370,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (rank != 0) {
               if (lane == 0) arrive_first_cta(sb + L::V_PEER + 8 * g);
             } else {
-              good = wait_peer(L::V_PEER + 8 * g, cleared[g]);
+              good = wait(L::V_PEER + 8 * g, cleared[g]);
             }
             ++cleared[g];
             if (!good) break;
           }
           if (rank != 0) continue;
-          if (lane == 0) {
+          if (tc5::elect_one()) {
             tc5::fence_after();
-            for (int k = 4 * g; k < 4 * g + 4 && k * 16 < valid; ++k) {
-              const uint64_t ad = tc5::smem_desc(sb + L::P + (k >> 2) * L::PBOX + (k & 3) * 32, 16, 1024);
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                mma_pair(t_o + (uint32_t)(128 * h), ad,
-                         tc5::smem_desc(sb + L::V + 2 * h * L::VBOX + k * 2048, L::VBOX, 1024), idesc_o,
-                         j > 0 || k > 0 ? 1u : 0u);
-            }
-            commit_pair(sb + L::V_FREE + 8 * g);
+            for (int k = 4 * g; k < 4 * g + 4; ++k)
+              if (k * 16 < valid) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  tc5::mma2(t_o + (uint32_t)(128 * h),
+                            tc5::desc_at(p_desc, (k >> 2) * L::PBOX + (k & 3) * 32),
+                            tc5::desc_at(v_desc, 2 * h * L::VBOX + k * 2048), idesc_o,
+                            j > 0 || k > 0 ? 1u : 0u);
+              }
+            tc5::commit2(sb + L::V_FREE + 8 * g);
+            if (g == L::NV - 1) tc5::commit2(sb + L::PV_DONE);
           }
           __syncwarp();
         }
-        if (good && rank == 0 && lane == 0) commit_pair(sb + L::PV_DONE);
       }
       c += n;
       ++qc;
     }
     if (!good && lane == 0) set_status(p.status, PA_DEV_TIMEOUT);
     // every MMA issued has finished before either CTA goes on
-    if (rank == 0 && lane == 0) commit_pair(sb + L::DRAIN);
-    warp_wait(sb + L::DRAIN, 0u, kDrainWaitNs);
+    if (rank == 0 && tc5::elect_one()) tc5::commit2(sb + L::DRAIN);
+    __syncwarp();
+    tc5::warp_wait(sb + L::DRAIN, 0u, kDrainWaitNs);
   } else {
     // ================= softmax and output =================
     const int row = (warp & 1) * 32 + lane;        // of the CTA's 64
@@ -437,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     bool good = true;  // after a wait that gave up, a warp only keeps its place in the pair barriers
     int c = 0;
     auto wait = [&](int bar, uint32_t parity) {
-      if (good) good = warp_wait(sb + bar, parity, p.wait_ns);
+      if (good) good = tc5::warp_wait(sb + bar, parity, p.wait_ns);
     };
     for (int i = first; i < last; ++i) {
       const LatentSegment s = p.segments[i];

@@ -35,29 +35,10 @@
 #include <math.h>
 
 #include "latent_params.h"
-#include "prefill_tc5.cuh"
+#include "latent_tc5.cuh"
 #include "split_launch.cuh"
 
 namespace pa {
-
-namespace tc5 {
-
-// 32 consecutive 32-bit columns of this thread's TMEM lane.
-__device__ __forceinline__ void ld32(uint32_t taddr, float* v) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-
-}  // namespace tc5
 
 namespace {
 
@@ -231,27 +212,29 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     if (n > 0) {
       const uint32_t idesc_s = tc5::instr_desc<T>(kRows, kTokens, false);
       const uint32_t idesc_o = tc5::instr_desc<T>(kRows, D, true);
+      const uint64_t q_desc = tc5::smem_desc(sb + L::Q, 16, 1024), k_desc = tc5::smem_desc(sb + L::K, 16, 1024);
+      const uint64_t v_desc = tc5::smem_desc(sb + L::V, L::BOX, 1024);
       auto issue_s = [&](int t, int j) {
-        if (lane == 0) {
+        if (tc5::elect_one()) {
           tc5::fence_after();
-          const uint32_t qb = sb + L::Q + t * L::QTILE, kb = sb + L::K + (j % L::NK) * L::KSTAGE;
+          const uint64_t qb = tc5::desc_at(q_desc, t * L::QTILE);
+          const uint64_t kb = tc5::desc_at(k_desc, (j % L::NK) * L::KSTAGE);
 #pragma unroll
           for (int k = 0; k < DK / 16; ++k)
-            tc5::mma(tmem + t * kTokens,
-                     tc5::smem_desc(qb + (k >> 2) * L::BOX + (k & 3) * 32, 16, 1024),
-                     tc5::smem_desc(kb + (k >> 2) * L::BOX + (k & 3) * 32, 16, 1024), idesc_s,
-                     k > 0 ? 1u : 0u);
+            tc5::mma1(tmem + t * kTokens, tc5::desc_at(qb, (k >> 2) * L::BOX + (k & 3) * 32),
+                      tc5::desc_at(kb, (k >> 2) * L::BOX + (k & 3) * 32), idesc_s, k > 0 ? 1u : 0u);
           tc5::commit(sb + L::S_DONE + 8 * t);
         }
+        __syncwarp();
       };
       auto wait = [&](int bar, uint32_t parity) {
-        return __all_sync(kFull, mbar_wait_bounded_sleep(sb + bar, parity, p.wait_ns)) != 0;
+        return tc5::warp_wait(sb + bar, parity, p.wait_ns);
       };
       bool good = wait(L::Q_FULL, 0u) && wait(L::K_FULL, 0u);
       if (good) {
         if (n0 > 0) issue_s(0, 0);
         if (n1 > 0) issue_s(1, 0);
-        if (lane == 0) tc5::commit(sb + L::K_FREE);
+        if (tc5::elect_one()) tc5::commit(sb + L::K_FREE);
       }
       for (int j = 0; j < n && good; ++j) {
         bool have_v = false;
@@ -276,16 +259,16 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
               }
             }
             if (!good) break;
-            if (lane == 0) {
+            if (tc5::elect_one()) {
               tc5::fence_after();
 #pragma unroll
               for (int k = 0; k < kTokens / 16; ++k)
-                tc5::mma_tmem_a(tmem + 2 * kTokens + t * D, tmem + t * kTokens + 8 * k,
-                                tc5::smem_desc(sb + L::V + k * 2048, L::BOX, 1024), idesc_o,
-                                j > 0 || k > 0 ? 1u : 0u);
+                tc5::mma1_tmem(tmem + 2 * kTokens + t * D, tmem + t * kTokens + 8 * k,
+                               tc5::desc_at(v_desc, k * 2048), idesc_o, j > 0 || k > 0 ? 1u : 0u);
               tc5::commit(sb + L::PV_DONE + 8 * t);
               if (t == (n1 > j ? 1 : 0)) tc5::commit(sb + L::V_FREE);
             }
+            __syncwarp();
           }
           if (j + 1 < nt) {
             if (!have_k) good = wait(L::K_FULL + 8 * ((j + 1) % L::NK), (uint32_t)(((j + 1) / L::NK) & 1));
@@ -296,14 +279,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             issue_s(t, j + 1);
           }
         }
-        if (good && next && lane == 0) tc5::commit(sb + L::K_FREE + 8 * ((j + 1) % L::NK));
+        if (good && next && tc5::elect_one()) tc5::commit(sb + L::K_FREE + 8 * ((j + 1) % L::NK));
       }
       if (!good && lane == 0) {
         set_status(p.status, PA_DEV_TIMEOUT);
         *flag = 1;
       }
       // every MMA issued finishes before TMEM is freed
-      if (lane == 0) {
+      __syncwarp();
+      if (tc5::elect_one()) {
         tc5::commit(sb + L::DRAIN);
         mbar_wait_bounded_sleep(sb + L::DRAIN, 0u, kDrainWaitNs);
       }
