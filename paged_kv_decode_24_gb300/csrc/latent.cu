@@ -245,7 +245,6 @@ extern "C" pa_status_t pa_latent_attention(const pa_latent_shape_t* shape,
                                        plan->num_slots);
   char* ws = static_cast<char*>(workspace);
   p.q = q;
-  p.pages = pages;
   p.out = out;
   p.block_table = block_table;
   p.ws = reinterpret_cast<const int32_t*>(ws);

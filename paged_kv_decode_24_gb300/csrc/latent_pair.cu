@@ -46,7 +46,6 @@ namespace {
 constexpr int kPairRows = 64;          // rows of one CTA
 constexpr int kPairTokens = 128;       // tokens of a stage
 constexpr int kPairThreads = 7 * 32;
-constexpr int kPrefetchStages = 2;     // how far ahead L2 is asked for rows
 constexpr float kPairLazyLog2 = 8.f;   // the maximum is raised when it grows by more than 2^8
 static_assert(kLatentRowsPair == 2 * kPairRows && kLatentStagePair == kPairTokens, "plan and kernel");
 
@@ -232,19 +231,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (wanted && page < 0) set_status(p.status, PA_DEV_BAD_PAGE);
         const unsigned have = __ballot_sync(kFull, page >= 0);
         const unsigned missing = __ballot_sync(kFull, wanted && page < 0);
-        // The loads from HBM take longer than the buffers here can cover: ask L2
-        // for the rows of a later stage (each CTA for its half of the tokens)
-        if (keys) {
-          const int ahead = tok + kPrefetchStages * kPairTokens;
-          const int u = lane - rank * (copies / 2);
-          if (u >= 0 && u < copies / 2 && ahead < s.tok1) {
-            const int pg = table[ahead / p.page_size];
-            if (pg >= 0 && pg < p.num_pages)
-              prefetch_l2_bulk(static_cast<const T*>(p.pages) +
-                                   ((int64_t)pg * p.page_size + ahead % p.page_size) * kLatentRow,
-                               (uint32_t)(box * kLatentRow * 2));
-          }
-        }
         const int row = tok % p.page_size;
         const int valid = min(kPairTokens, s.tok1 - s.tok0 - j * kPairTokens);
         for (int g = 0; g < groups; ++g) {

@@ -31,7 +31,6 @@ cudaError_t launch_latent_gather(const LatentRowsParams& p, cudaStream_t stream)
 struct LatentParams {
   CUtensorMap pages_map;  // the pool, in the boxes of the plan's kernel
   const void* q;
-  const void* pages;
   void* out;
   const int32_t* block_table;
   const int32_t* ws;

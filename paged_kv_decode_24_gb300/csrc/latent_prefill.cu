@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         __syncwarp();
       };
       auto wait = [&](int bar, uint32_t parity) {
-        return tc5::warp_wait(sb + bar, parity, p.wait_ns);
+        return __all_sync(kFull, mbar_wait_bounded(sb + bar, parity, p.wait_ns)) != 0;
       };
       bool good = wait(L::Q_FULL, 0u) && wait(L::K_FULL, 0u);
       if (good) {

@@ -78,12 +78,11 @@ __device__ __forceinline__ void ld32(uint32_t taddr, float* v) {
       : "r"(taddr));
 }
 
-// A bounded wait of the whole warp: one lane polls, so that waiting warps
-// leave shared memory and the issue slots to the copies and the others.
+// A bounded wait of the whole warp.  Every lane polls: with one lane polling
+// and a shuffle behind it the wake-up took longer (prompt 8192 x 32 heads 585
+// against 542 us, batch of 32 with 128 heads 68 against 60 us).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  bool ok = false;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait_bounded_sleep(bar, parity, limit_ns);
-  return __shfl_sync(kFull, ok, 0);
+  return __all_sync(kFull, mbar_wait_bounded_sleep(bar, parity, limit_ns)) != 0;
 }
 
 }  // namespace tc5
