@@ -248,8 +248,6 @@ extern "C" pa_status_t pa_latent_attention(const pa_latent_shape_t* shape,
   p.out = out;
   p.block_table = block_table;
   p.ws = reinterpret_cast<const int32_t*>(ws);
-  p.cu_q = reinterpret_cast<const int32_t*>(ws + l.cu_q);
-  p.cu_k = reinterpret_cast<const int32_t*>(ws + l.cu_k);
   p.ranges = reinterpret_cast<const int32_t*>(ws + l.ranges);
   p.segments = reinterpret_cast<const LatentSegment*>(ws + l.work);
   p.merges = reinterpret_cast<const LatentMerge*>(ws + l.merges);

@@ -22,10 +22,13 @@ constexpr int kLatentRowsExpanded = 256;      // query tokens of an expanded til
 constexpr uint32_t kLatentMagic = 0x564b414cu;  // "LAKV"
 
 // A piece of the absorbed work list: rows row0 .. row0 + nrows - 1 of
-// sequence b (row = query token x heads + head) over tokens [tok0, tok1).
-// slot < 0: writes out; else its partial result goes to that slot.
+// sequence b (row = query token x heads + head), packed rows packed0 .. of
+// [T * H], over tokens [tok0, tok1).  The sequence's first query token sits
+// at position pos0.  slot < 0: writes out; else its partial result goes to
+// that slot.  A piece holds all that a kernel has to know, so that it is one
+// load away from its work.
 struct LatentSegment {
-  int32_t b, row0, nrows, tok0, tok1, slot, pad0, pad1;
+  int32_t b, row0, nrows, tok0, tok1, slot, packed0, pos0;
 };
 
 // A tile cut into several pieces: its partials are in slots slot0 ..

@@ -37,6 +37,8 @@ namespace pa {
 namespace {
 
 constexpr int kWorkWarps = 8;
+constexpr int kManyMergeRows = 608;  // split rows from which the merge gives a row one warp
+                                     // (four a SM)
 constexpr int kMmaThreads = (kWorkWarps + 1) * 32;
 
 struct MmaLayout {
@@ -80,8 +82,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   volatile int* flag = reinterpret_cast<int*>(base + L::FLAG);
   volatile int* valid = reinterpret_cast<int*>(base + L::VALID);
 
+  int first, last;
+  const bool planned = latent_range(p, kLatentRowsMma, (int)blockIdx.x, first, last);
   if (threadIdx.x == 0) {
     *flag = 0;
+    if (!planned) set_status(p.status, PA_DEV_PLAN_MISMATCH);
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.pages_map)) : "memory");
     for (int s = 0; s < L::SLOTS; ++s) {
       mbar_init(sbase + L::FULL + 8 * s, 1);
@@ -89,21 +94,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
     fence_barrier_init();
   }
+  LatentSegment s{};
+  if (first < last) s = p.segments[first];
   __syncthreads();
   pdl_launch_dependents();
   pdl_wait_primary();
-
-  const int4 h0 = reinterpret_cast<const int4*>(p.ws)[0], h2 = reinterpret_cast<const int4*>(p.ws)[2];
-  int first = 0, last = 0;
-  if (h0.x == (int)kLatentMagic && h0.y == p.batch && h0.z == p.total_q && h2.x == p.num_ranges &&
-      h2.y == p.num_segments && h2.z == p.num_merges && h2.w == p.num_slots &&
-      p.ws[6] == PA_LATENT_ABSORBED && p.ws[7] == kLatentRowsMma) {
-    first = p.ranges[blockIdx.x];
-    last = min(p.ranges[blockIdx.x + 1], p.num_segments);
-    if (first < 0) first = last;
-  } else if (threadIdx.x == 0) {
-    set_status(p.status, PA_DEV_PLAN_MISMATCH);
-  }
 
   if (warp == kWorkWarps) {
     // ================= copies =================
@@ -111,7 +106,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     int k = 0;  // blocks issued
     bool good = true;
     for (int i = first; i < last && good; ++i) {
-      const LatentSegment s = p.segments[i];
+      if (i > first) s = p.segments[i];
       if (!latent_segment_ok(p, s, kLatentRowsMma)) continue;  // the working warps report it
       const int32_t* table = p.block_table + (int64_t)s.b * p.max_pages;
       const int blocks = (s.tok1 - s.tok0 + kLatentBlock - 1) / kLatentBlock;
@@ -166,14 +161,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   int k = 0;         // blocks consumed
   bool good = true;  // after a wait that gave up, a warp only keeps its place in the barriers
   for (int i = first; i < last; ++i) {
-    const LatentSegment s = p.segments[i];
+    if (i > first) s = p.segments[i];
     if (!latent_segment_ok(p, s, kLatentRowsMma)) {  // the same for every warp
       if (threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
       continue;
     }
-    const int cq = p.cu_q[s.b], qn = p.cu_q[s.b + 1] - cq;
-    const int len = p.cu_k[s.b + 1] - p.cu_k[s.b];
-    const int64_t grow = (int64_t)cq * p.heads + s.row0;  // packed row of tile row 0
+    const int64_t grow = s.packed0;  // packed row of tile row 0
 
     // this warp's quarter of q: nine A fragments of 16 dims
     uint32_t qa[9][4];
@@ -188,7 +181,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                                   : 0u;
       }
     // last token that this lane's softmax row sees
-    const int lim = srow < s.nrows ? len - qn + (s.row0 + srow) / p.heads : -1;
+    const int lim = srow < s.nrows ? s.pos0 + (s.row0 + srow) / p.heads : -1;
     float m_run = -INFINITY, l_run = 0.f;
     float o[8][4];
 #pragma unroll
@@ -198,19 +191,20 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 
     for (int t0 = s.tok0; t0 < s.tok1; t0 += kLatentStage) {
       const int blocks = min(kLatentStage / kLatentBlock, (s.tok1 - t0 + kLatentBlock - 1) / kLatentBlock);
-      unsigned ok_blocks = 0;  // blocks whose page was good
+      // lane u waits for block u; a block counts if its page was good
+      bool landed = true, usable = false;
+      if (lane < blocks) {
+        const int slot = (k + lane) % L::SLOTS;
+        landed = good && mbar_wait_bounded(sbase + L::FULL + 8 * slot,
+                                           (uint32_t)(((k + lane) / L::SLOTS) & 1), p.wait_ns);
+        usable = landed && valid[slot];
+      }
+      good = __all_sync(kFull, landed);
+      const unsigned ok_blocks = good ? __ballot_sync(kFull, usable) : 0u;
+      __syncwarp();
       uint32_t blk[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int slot = (k + u) % L::SLOTS;
-        blk[u] = sbase + slot * L::SLOT;
-        if (u < blocks) {
-          if (good)
-            good = __all_sync(kFull, mbar_wait_bounded(sbase + L::FULL + 8 * slot,
-                                                       (uint32_t)(((k + u) / L::SLOTS) & 1), p.wait_ns));
-          if (good && valid[slot]) ok_blocks |= 1u << u;
-        }
-      }
+      for (int u = 0; u < 4; ++u) blk[u] = sbase + (uint32_t)((k + u) % L::SLOTS) * L::SLOT;
       if (!good) *flag = 1;
 
       // ---- scores of 32 tokens over a quarter of the dims
@@ -365,45 +359,79 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 // w_s = 2^(lse_s - max lse).  Pieces in their order, so the sum is the same
 // on every call.  A piece whose waits gave up left an lse of +infinity, which
 // no piece that completed has: its rows stay unwritten.
-template <typename T>
+// WARPS warps share a row's pieces, each covering all 512 values: one where
+// many rows were split (each warp then has its few pieces' loads in flight at
+// once), four where few rows were split into many pieces (two sequences in 38
+// pieces each: 10 against 21 us; 29 tiles of 128 rows in 3 pieces: with four
+// warps a row 23 us).
+template <typename T, int WARPS>
 __global__ void __launch_bounds__(128) latent_merge_kernel(const __grid_constant__ LatentParams p) {
+  constexpr int ROWS = 4 / WARPS;  // rows of a block
+  __shared__ float4 acc_s[4][kLatent / 4];
+  __shared__ float sum_s[4];
+  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+  const int4 h0 = reinterpret_cast<const int4*>(p.ws)[0], h2 = reinterpret_cast<const int4*>(p.ws)[2];
+  const int which = (int)blockIdx.x * ROWS + warp / WARPS;  // row of all tiles' rows
+  const LatentMerge m = p.merges[which / p.rows];           // p.rows is a multiple of ROWS
+  const int row = which % p.rows;
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int4 h2 = reinterpret_cast<const int4*>(p.ws)[2];
-  if (p.ws[0] != (int)kLatentMagic || h2.z != p.num_merges || h2.w != p.num_slots) return;  // reported already
-  const LatentMerge m = p.merges[blockIdx.x / p.rows];
-  const int row = (int)(blockIdx.x % p.rows);
-  if (row >= m.nrows || m.slot0 < 0 || m.n < 1 || m.slot0 + m.n > p.num_slots || m.row0 < 0 ||
+  if (h0.x != (int)kLatentMagic || h2.z != p.num_merges || h2.w != p.num_slots) return;  // reported already
+  if (row >= m.nrows || m.slot0 < 0 || m.n < 1 || (int64_t)m.slot0 + m.n > p.num_slots || m.row0 < 0 ||
       (int64_t)m.row0 + m.nrows > (int64_t)p.total_q * p.heads)
     return;
-  const int lane = threadIdx.x & 31;
   const float* lse = p.part_lse + (int64_t)m.slot0 * p.rows + row;
   float mx = -INFINITY;
   for (int s = lane; s < m.n; s += 32) mx = fmaxf(mx, __ldcg(lse + (int64_t)s * p.rows));
 #pragma unroll
   for (int w = 16; w >= 1; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, w));
-  if (mx == INFINITY) return;
+  if (mx == INFINITY) return;  // the same in every warp of the row
   const float ref = mx == -INFINITY ? 0.f : mx;
-  const float4* o = reinterpret_cast<const float4*>(p.part_o + ((int64_t)m.slot0 * p.rows + row) * kLatent) +
-                    threadIdx.x;
+  const float4* o =
+      reinterpret_cast<const float4*>(p.part_o + ((int64_t)m.slot0 * p.rows + row) * kLatent) + lane;
   const int64_t step = (int64_t)p.rows * (kLatent / 4);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-#pragma unroll 8
-  for (int s = 0; s < m.n; ++s) {
+#pragma unroll 4
+  for (int s = warp % WARPS; s < m.n; s += WARPS) {
     const float w = ex2(__ldcg(lse + (int64_t)s * p.rows) - ref);
-    const float4 v = __ldcg(o + s * step);
     sum += w;
-    acc.x += w * v.x;
-    acc.y += w * v.y;
-    acc.z += w * v.z;
-    acc.w += w * v.w;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float4 v = __ldcg(o + s * step + 32 * c);
+      acc[c].x += w * v.x;
+      acc[c].y += w * v.y;
+      acc[c].z += w * v.z;
+      acc[c].w += w * v.w;
+    }
+  }
+  if (WARPS > 1) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc_s[warp][lane + 32 * c] = acc[c];
+    if (lane == 0) sum_s[warp] = sum;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int g = 1; g < WARPS; ++g) {
+      sum += sum_s[g];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 v = acc_s[g][lane + 32 * c];
+        acc[c].x += v.x;
+        acc[c].y += v.y;
+        acc[c].z += v.z;
+        acc[c].w += v.w;
+      }
+    }
   }
   const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-  uint2 r;
-  r.x = Elem<T>::from_f2(acc.x * inv, acc.y * inv);
-  r.y = Elem<T>::from_f2(acc.z * inv, acc.w * inv);
-  reinterpret_cast<uint2*>(static_cast<T*>(p.out) + ((int64_t)m.row0 + row) * kLatent)[threadIdx.x] = r;
+  uint2* out = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + ((int64_t)m.row0 + row) * kLatent) + lane;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    out[32 * c] = make_uint2(Elem<T>::from_f2(acc[c].x * inv, acc[c].y * inv),
+                             Elem<T>::from_f2(acc[c].z * inv, acc[c].w * inv));
 }
 
 template <typename T>
@@ -415,8 +443,11 @@ cudaError_t launch_mma_t(const LatentParams& p, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t launch_merge_t(const LatentParams& p, cudaStream_t stream) {
-  static std::atomic<unsigned long long> configured{0};
-  return launch_pdl(latent_merge_kernel<T>, 0, configured, p, p.num_merges * p.rows, 128, stream);
+  static std::atomic<unsigned long long> one{0}, four{0};
+  const int64_t rows = (int64_t)p.num_merges * p.rows;
+  if (rows >= kManyMergeRows)
+    return launch_pdl(latent_merge_kernel<T, 1>, 0, one, p, (int)(rows / 4), 128, stream);
+  return launch_pdl(latent_merge_kernel<T, 4>, 0, four, p, (int)rows, 128, stream);
 }
 
 }  // namespace

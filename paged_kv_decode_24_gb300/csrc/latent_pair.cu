@@ -135,6 +135,26 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// The page of token tok, -1 from `end` on.  A volatile load, which stays where
+// it is written: a stage ahead of its use.
+__device__ __forceinline__ int table_entry(const int32_t* table, int page_size, int tok, int end) {
+  int page = -1;
+  if (tok < end) asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(page) : "l"(table + tok / page_size));
+  return page;
+}
+
+// 32 bytes to a 16-byte aligned address; `whole`: it is 32-byte aligned.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* w, bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 __device__ __forceinline__ void row_pair_barrier(int warp) {  // the two warps that share 32 rows
   asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 1)) : "memory");
 }
@@ -150,8 +170,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t sb = smem_u32(base);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cta_rank();
+  int first, last;
+  const bool planned = latent_range(p, kLatentRowsPair, (int)(blockIdx.x >> 1), first, last);
 
   if (threadIdx.x == 0) {
+    if (!planned) set_status(p.status, PA_DEV_PLAN_MISMATCH);
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.pages_map)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&q_map)) : "memory");
     for (int b = L::Q_FREE; b < L::P_READY; b += 8) mbar_init(sb + b, 1);
@@ -164,6 +187,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  LatentSegment s{};
+  if (first < last) s = p.segments[first];
   tc5::fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before either is arrived on
@@ -173,18 +198,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   pdl_launch_dependents();
   pdl_wait_primary();
 
-  const int4 h0 = reinterpret_cast<const int4*>(p.ws)[0], h2 = reinterpret_cast<const int4*>(p.ws)[2];
-  int first = 0, last = 0;
-  if (h0.x == (int)kLatentMagic && h0.y == p.batch && h0.z == p.total_q && h2.x == p.num_ranges &&
-      h2.y == p.num_segments && h2.z == p.num_merges && h2.w == p.num_slots &&
-      p.ws[6] == PA_LATENT_ABSORBED && p.ws[7] == kLatentRowsPair) {
-    const int range = (int)(blockIdx.x >> 1);
-    first = p.ranges[range];
-    last = min(p.ranges[range + 1], p.num_segments);
-    if (first < 0) first = last;
-  } else if (threadIdx.x == 0) {
-    set_status(p.status, PA_DEV_PLAN_MISMATCH);
-  }
   auto usable = [&](const LatentSegment& s) {  // the same answer in every warp of both CTAs
     return latent_segment_ok(p, s, kLatentRowsPair);
   };
@@ -206,7 +219,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int groups = keys ? L::NG : L::NV;
     const uint32_t full0 = in_first_cta(sb + (keys ? L::K_FULL : L::V_FULL));
     for (int i = first; i < last && good; ++i) {
-      const LatentSegment s = p.segments[i];
+      if (i > first) s = p.segments[i];
       if (!usable(s)) continue;
       const int32_t* table = p.block_table + (int64_t)s.b * p.max_pages;
       if (keys) {  // q: the CTA's 64 rows
@@ -214,7 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (!good) break;
         if (lane == 0) {
           if (rank == 0) mbar_arrive_expect_tx(sb + L::Q_FULL, 2 * 9 * L::QBOX);
-          const int row = (int)((int64_t)p.cu_q[s.b] * p.heads + s.row0) + rank * kPairRows;
+          const int row = s.packed0 + rank * kPairRows;
           const uint32_t bar = in_first_cta(sb + L::Q_FULL);
           for (int b = 0; b < 9; ++b)
             tma_load_2d_pair(sb + L::Q + b * L::QBOX, &q_map, b * 64, row, bar, once);
@@ -222,11 +235,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         ++qc;
       }
       const int n = stages_of(s);
+      // lane u: the page of tokens u * box .. of a stage, a stage ahead of its use
+      int next = table_entry(table, p.page_size, s.tok0 + lane * box, lane < copies ? s.tok1 : 0);
       for (int j = 0; j < n && good; ++j, ++c) {
-        // lane u: the page of tokens u * box .. of the stage
         const int tok = s.tok0 + j * kPairTokens + lane * box;
         const bool wanted = lane < copies && tok < s.tok1;
-        int page = wanted ? table[tok / p.page_size] : -1;
+        int page = next;
+        next = table_entry(table, p.page_size, tok + kPairTokens, lane < copies ? s.tok1 : 0);
         if (page >= p.num_pages) page = -1;
         if (wanted && page < 0) set_status(p.status, PA_DEV_BAD_PAGE);
         const unsigned have = __ballot_sync(kFull, page >= 0);
@@ -319,16 +334,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       return true;
     };
     for (int i = first; i < last && good; ++i) {
-      const LatentSegment s = p.segments[i];
+      if (i > first) s = p.segments[i];
       if (!usable(s)) continue;
       const int32_t* table = p.block_table + (int64_t)s.b * p.max_pages;
       const int n = stages_of(s);
       if (rank == 0) good = wait(L::Q_FULL, qc) && scores(c, n == 1);
+      // lane u < 8: the page of tokens 16 u .. of a stage, a stage ahead of its use
+      const int lane_end = lane < 8 ? s.tok1 : 0;
+      int next = table_entry(table, p.page_size, s.tok0 + lane * kLatentBlock, lane_end);
       for (int j = 0; j < n && good; ++j) {
-        // lane u < 8: is the page of tokens 16 u .. of the stage bad?
         const int tok = s.tok0 + j * kPairTokens + lane * kLatentBlock;
-        const int page = lane < 8 && tok < s.tok1 ? table[tok / p.page_size] : 0;
-        const unsigned bad = __ballot_sync(kFull, page < 0 || page >= p.num_pages);
+        const unsigned bad = __ballot_sync(kFull, tok < lane_end && (next < 0 || next >= p.num_pages));
+        next = table_entry(table, p.page_size, tok + kPairTokens, lane_end);
         const int valid = min(kPairTokens, s.tok1 - s.tok0 - j * kPairTokens);
         if (rank == 0) {
           if (j + 1 < n) good = scores(c + j + 1, j + 2 == n);
@@ -401,16 +418,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (good) good = tc5::warp_wait(sb + bar, parity, p.wait_ns);
     };
     for (int i = first; i < last; ++i) {
-      const LatentSegment s = p.segments[i];
+      if (i > first) s = p.segments[i];
       if (!usable(s)) {
         if (threadIdx.x == 0 && rank == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
         continue;
       }
       const int32_t* table = p.block_table + (int64_t)s.b * p.max_pages;
       const int n = stages_of(s);
-      const int cq = p.cu_q[s.b], qn = p.cu_q[s.b + 1] - cq, len = p.cu_k[s.b + 1] - p.cu_k[s.b];
       const int trow = rank * kPairRows + row;     // of the tile
-      const int lim0 = trow < s.nrows ? len - qn + (s.row0 + trow) / p.heads : -1;  // last visible token
+      const int lim0 = trow < s.nrows ? s.pos0 + (s.row0 + trow) / p.heads : -1;  // last visible token
       const bool idle = rank * kPairRows + (warp & 1) * 32 >= s.nrows;  // no row of the warp's is real
       float m_run = -INFINITY, l_run = 0.f;
       int nph[4];  // pages of the thread's 64 tokens, a stage ahead
@@ -418,9 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int tok = s.tok0 + j * kPairTokens + half * 64 + u * 16;
-          nph[u] = -1;
-          if (!idle && tok < s.tok1)
-            asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(nph[u]) : "l"(table + tok / p.page_size));
+          nph[u] = table_entry(table, p.page_size, tok, idle ? 0 : s.tok1);
         }
       };
       load_pages(0);
@@ -517,8 +531,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const float l = l_run + other;
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a NaN sum stays NaN
         const bool mine = trow < s.nrows;
-        const int64_t grow = (int64_t)cq * p.heads + s.row0 + trow;
+        const int64_t grow = (int64_t)s.packed0 + trow;
         const int64_t at = (int64_t)s.slot * p.rows + trow;
+        const bool whole32 = ((reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.part_o)) & 31) == 0;
         if (whole) {
           tc5::fence_after();
 #pragma unroll 2
@@ -528,23 +543,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             tc5::ld16(t_o + (uint32_t)x + 16u + lane_off, ov + 16);
             tc5::wait_ld();
             const int dim = (x >> 7) * 256 + half * 128 + (x & 127);
+            // a thread's row is its own: 32 bytes a store, a whole sector each
             if (mine && s.slot < 0) {
               T* out = static_cast<T*>(p.out) + grow * kLatent + dim;
 #pragma unroll
-              for (int y = 0; y < 32; y += 8) {
-                uint4 w;
-                w.x = Elem<T>::from_f2(ov[y] * inv, ov[y + 1] * inv);
-                w.y = Elem<T>::from_f2(ov[y + 2] * inv, ov[y + 3] * inv);
-                w.z = Elem<T>::from_f2(ov[y + 4] * inv, ov[y + 5] * inv);
-                w.w = Elem<T>::from_f2(ov[y + 6] * inv, ov[y + 7] * inv);
-                *reinterpret_cast<uint4*>(out + y) = w;
+              for (int y = 0; y < 32; y += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int z = 0; z < 8; ++z)
+                  w[z] = Elem<T>::from_f2(ov[y + 2 * z] * inv, ov[y + 2 * z + 1] * inv);
+                store32(out + y, w, whole32);
               }
             } else if (mine) {
               float* po = p.part_o + at * kLatent + dim;
 #pragma unroll
-              for (int y = 0; y < 32; y += 4)
-                *reinterpret_cast<float4*>(po + y) =
-                    make_float4(ov[y] * inv, ov[y + 1] * inv, ov[y + 2] * inv, ov[y + 3] * inv);
+              for (int y = 0; y < 32; y += 8) {
+                uint32_t w[8];
+#pragma unroll
+                for (int z = 0; z < 8; ++z) w[z] = __float_as_uint(ov[y + z] * inv);
+                store32(po + y, w, whole32);
+              }
             }
           }
         }

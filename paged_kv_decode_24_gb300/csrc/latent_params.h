@@ -34,8 +34,6 @@ struct LatentParams {
   void* out;
   const int32_t* block_table;
   const int32_t* ws;
-  const int32_t* cu_q;
-  const int32_t* cu_k;
   const int32_t* ranges;
   const LatentSegment* segments;
   const LatentMerge* merges;

@@ -116,7 +116,9 @@ void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_
         if (n - at - take < kMinPiece) take = n - at;
       }
       const int32_t tok1 = (int32_t)std::min<int64_t>((at + take) * stage, t.span);
-      w->segments.push_back({t.b, t.row0, t.nrows, (int32_t)(at * stage), tok1, -1, 0, 0});
+      w->segments.push_back({t.b, t.row0, t.nrows, (int32_t)(at * stage), tok1, -1,
+                             (int32_t)((int64_t)cu_q[(size_t)t.b] * s.num_heads + t.row0),
+                             lens[t.b] - qs[t.b]});
       at += take;
       left -= take + kPieceStages;
       total -= take + (at == n ? kPieceStages : 0);
@@ -124,8 +126,7 @@ void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_
     }
     const size_t pieces = w->segments.size() - first;
     if (pieces > 1) {
-      w->merges.push_back({(int32_t)w->slots, (int32_t)pieces,
-                           (int32_t)((int64_t)cu_q[(size_t)t.b] * s.num_heads + t.row0), t.nrows});
+      w->merges.push_back({(int32_t)w->slots, (int32_t)pieces, w->segments[first].packed0, t.nrows});
       for (size_t i = first; i < w->segments.size(); ++i)
         w->segments[i].slot = (int32_t)w->slots++;
     }

@@ -5,16 +5,30 @@
 
 namespace pa {
 
-// A segment of this call's plan whose rows and tokens are its sequence's.
+// A piece whose rows and tokens lie within this call's tensors.
 __device__ __forceinline__ bool latent_segment_ok(const LatentParams& p, const LatentSegment& s,
                                                   int rows) {
-  if (s.b < 0 || s.b >= p.batch || s.nrows < 1 || s.nrows > rows || s.row0 < 0 ||
-      s.slot >= p.num_slots || s.tok0 < 0 || s.tok0 % kLatentStage != 0 || s.tok1 <= s.tok0)
-    return false;
-  const int cq = p.cu_q[s.b], qn = p.cu_q[s.b + 1] - cq, len = p.cu_k[s.b + 1] - p.cu_k[s.b];
-  return cq >= 0 && p.cu_q[s.b + 1] <= p.total_q &&
-         (int64_t)s.row0 + s.nrows <= (int64_t)qn * p.heads && qn <= len && s.tok1 <= len &&
-         (int64_t)len <= (int64_t)p.max_pages * p.page_size;
+  return s.b >= 0 && s.b < p.batch && s.nrows >= 1 && s.nrows <= rows && s.row0 >= 0 &&
+         s.packed0 >= 0 && (int64_t)s.packed0 + s.nrows <= (int64_t)p.total_q * p.heads &&
+         s.slot < p.num_slots && s.tok0 >= 0 && s.tok0 % kLatentStage == 0 && s.tok1 > s.tok0 &&
+         (int64_t)s.tok1 <= (int64_t)p.max_pages * p.page_size && s.pos0 >= 0;
+}
+
+// The pieces [first, last) of one range, or none where the workspace does
+// not hold this call's plan.  The plan is written by the upload alone, which
+// the programmatic launch does not overlap: it may be read before the wait
+// for the kernel ahead.
+__device__ __forceinline__ bool latent_range(const LatentParams& p, int rows, int range, int& first,
+                                             int& last) {
+  const int4 h0 = reinterpret_cast<const int4*>(p.ws)[0], h1 = reinterpret_cast<const int4*>(p.ws)[1];
+  const int4 h2 = reinterpret_cast<const int4*>(p.ws)[2];
+  first = p.ranges[range];
+  last = min(p.ranges[range + 1], p.num_segments);
+  const bool ok = h0.x == (int)kLatentMagic && h0.y == p.batch && h0.z == p.total_q &&
+                  h1.z == PA_LATENT_ABSORBED && h1.w == rows && h2.x == p.num_ranges &&
+                  h2.y == p.num_segments && h2.z == p.num_merges && h2.w == p.num_slots && first >= 0;
+  if (!ok) first = last = 0;
+  return ok;
 }
 
 }  // namespace pa

@@ -177,6 +177,27 @@ def test_absorbed_offsets_past_32_bits(rows):
     assert_latent_close(out.double().cpu().numpy(), want, 300, "fp16")
 
 
+@both_kernels
+@pytest.mark.parametrize("splits", [1, 2])
+def test_absorbed_buffers_aligned_to_16_bytes_only(splits, rows):
+    c = Case([300, 70], [2, 1], heads=12, page=16, seed=23)
+    d = Device(c, forced_splits=splits, rows_per_tile=rows)
+
+    def shifted(t):   # the same contents 16 bytes off a 256-byte boundary
+        n = 16 // t.element_size()
+        big = torch.empty(t.numel() + n, dtype=t.dtype, device="cuda")
+        big[n:] = t.flatten()
+        return big[n:].view(t.shape)
+
+    d.q, d.pages, d.ws = shifted(d.q), shifted(d.pages), shifted(d.ws)
+    assert all(t.data_ptr() % 32 == 16 for t in (d.q, d.pages, d.ws))
+    out = shifted(torch.full((c.T, 12, LATENT), float("nan"), dtype=DT["fp16"], device="cuda"))
+    d.attention(out)
+    assert d.done() == 0
+    want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), c.lens, c.qs, c.scale)
+    assert_latent_close(out.double().cpu().numpy(), want, 300, "fp16")
+
+
 # ---- expanded attention
 
 EXPANDED = [
