@@ -153,24 +153,6 @@ LatentRowsParams rows_params(const pa_latent_shape_t* s, const int32_t* block_ta
   return p;
 }
 
-// The pool [P][S][576] with boxes of `cols` column blocks (64 elements each)
-// by `tokens` tokens, 128-byte swizzle.
-bool encode_latent_map(CUtensorMap* map, const void* pages, const pa_latent_shape_t& s, int cols,
-                       int tokens) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (!enc) return false;
-  const cuuint64_t row = kLatentRow * 2;
-  cuuint64_t dims[4] = {64, kLatentRow / 64, (cuuint64_t)s.page_size, (cuuint64_t)s.num_pages};
-  cuuint64_t strides[3] = {128, row, row * s.page_size};
-  cuuint32_t box[4] = {64, (cuuint32_t)cols, (cuuint32_t)tokens, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUtensorMapDataType ty = s.dtype == PA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  return enc(map, ty, 4, const_cast<void*>(pages), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 }  // namespace pa
 
@@ -268,13 +250,8 @@ extern "C" pa_status_t pa_latent_attention(const pa_latent_shape_t* shape,
   p.total_q = plan->total_q;
   p.rows = plan->rows_per_tile;
   cudaStream_t s = (cudaStream_t)stream;
-  const bool pair = plan->rows_per_tile == kLatentRowsPair;
-  const int box = shape->page_size < 64 ? shape->page_size : 64;
-  if (!encode_latent_map(&p.pages_map, pages, *shape, pair ? 1 : kLatentRow / 64,
-                         pair ? box : kLatentBlock))
-    return PA_ERR_CUDA;
-  cudaError_t e = pair ? launch_latent_pair(p, shape->dtype, s)
-                       : launch_latent_mma(p, shape->dtype, s);
+  cudaError_t e = plan->rows_per_tile == kLatentRowsPair ? launch_latent_pair(p, *shape, pages, s)
+                                                         : launch_latent_mma(p, *shape, pages, s);
   if (e == cudaSuccess && p.num_merges > 0) e = launch_latent_merge(p, shape->dtype, s);
   return cuda_status(e);
 }

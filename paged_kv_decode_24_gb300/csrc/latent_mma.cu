@@ -39,6 +39,7 @@ namespace {
 constexpr int kWorkWarps = 8;
 constexpr int kManyMergeRows = 608;  // split rows from which the merge gives a row one warp
                                      // (four a SM)
+PA_HD constexpr int kMergeWarps(int warps_per_row) { return warps_per_row < 4 ? 4 : warps_per_row; }
 constexpr int kMmaThreads = (kWorkWarps + 1) * 32;
 
 struct MmaLayout {
@@ -361,14 +362,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 // no piece that completed has: its rows stay unwritten.
 // WARPS warps share a row's pieces, each covering all 512 values: one where
 // many rows were split (each warp then has its few pieces' loads in flight at
-// once), four where few rows were split into many pieces (two sequences in 38
-// pieces each: 10 against 21 us; 29 tiles of 128 rows in 3 pieces: with four
-// warps a row 23 us).
+// once), eight where few rows were split into many pieces.
 template <typename T, int WARPS>
-__global__ void __launch_bounds__(128) latent_merge_kernel(const __grid_constant__ LatentParams p) {
-  constexpr int ROWS = 4 / WARPS;  // rows of a block
-  __shared__ float4 acc_s[4][kLatent / 4];
-  __shared__ float sum_s[4];
+__global__ void __launch_bounds__(kMergeWarps(WARPS) * 32)
+    latent_merge_kernel(const __grid_constant__ LatentParams p) {
+  constexpr int ROWS = kMergeWarps(WARPS) / WARPS;  // rows of a block
+  constexpr int BATCH = 4;                          // pieces in flight
+  __shared__ float4 acc_s[WARPS > 1 ? WARPS : 1][kLatent / 4];
+  __shared__ float sum_s[WARPS];
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
   const int4 h0 = reinterpret_cast<const int4*>(p.ws)[0], h2 = reinterpret_cast<const int4*>(p.ws)[2];
   const int which = (int)blockIdx.x * ROWS + warp / WARPS;  // row of all tiles' rows
@@ -381,30 +382,44 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(const __grid_constant
       (int64_t)m.row0 + m.nrows > (int64_t)p.total_q * p.heads)
     return;
   const float* lse = p.part_lse + (int64_t)m.slot0 * p.rows + row;
+  const float4* o =
+      reinterpret_cast<const float4*>(p.part_o + ((int64_t)m.slot0 * p.rows + row) * kLatent) + lane;
+  const int64_t step = (int64_t)p.rows * (kLatent / 4);
+  float4 v[BATCH][4];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        v[b][c] = s0 + b * WARPS < m.n ? __ldcg(o + (int64_t)(s0 + b * WARPS) * step + 32 * c)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  load(warp % WARPS);  // in flight while the weights are found
   float mx = -INFINITY;
   for (int s = lane; s < m.n; s += 32) mx = fmaxf(mx, __ldcg(lse + (int64_t)s * p.rows));
 #pragma unroll
   for (int w = 16; w >= 1; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, w));
   if (mx == INFINITY) return;  // the same in every warp of the row
   const float ref = mx == -INFINITY ? 0.f : mx;
-  const float4* o =
-      reinterpret_cast<const float4*>(p.part_o + ((int64_t)m.slot0 * p.rows + row) * kLatent) + lane;
-  const int64_t step = (int64_t)p.rows * (kLatent / 4);
   float4 acc[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-#pragma unroll 4
-  for (int s = warp % WARPS; s < m.n; s += WARPS) {
-    const float w = ex2(__ldcg(lse + (int64_t)s * p.rows) - ref);
-    sum += w;
+  for (int s0 = warp % WARPS; s0 < m.n; s0 += BATCH * WARPS) {
+    if (s0 >= WARPS) load(s0);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float4 v = __ldcg(o + s * step + 32 * c);
-      acc[c].x += w * v.x;
-      acc[c].y += w * v.y;
-      acc[c].z += w * v.z;
-      acc[c].w += w * v.w;
+    for (int b = 0; b < BATCH; ++b) {
+      const int s = s0 + b * WARPS;
+      if (s >= m.n) break;
+      const float w = ex2(__ldcg(lse + (int64_t)s * p.rows) - ref);
+      sum += w;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        acc[c].x += w * v[b][c].x;
+        acc[c].y += w * v[b][c].y;
+        acc[c].z += w * v[b][c].z;
+        acc[c].w += w * v[b][c].w;
+      }
     }
   }
   if (WARPS > 1) {
@@ -413,16 +428,16 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(const __grid_constant
     if (lane == 0) sum_s[warp] = sum;
     __syncthreads();
     if (warp > 0) return;
-#pragma unroll
+#pragma unroll 1
     for (int g = 1; g < WARPS; ++g) {
       sum += sum_s[g];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const float4 v = acc_s[g][lane + 32 * c];
-        acc[c].x += v.x;
-        acc[c].y += v.y;
-        acc[c].z += v.z;
-        acc[c].w += v.w;
+        const float4 x = acc_s[g][lane + 32 * c];
+        acc[c].x += x.x;
+        acc[c].y += x.y;
+        acc[c].z += x.z;
+        acc[c].w += x.w;
       }
     }
   }
@@ -434,6 +449,23 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(const __grid_constant
                              Elem<T>::from_f2(acc[c].z * inv, acc[c].w * inv));
 }
 
+// The pool [P][S][576] with boxes of 16 whole rows, 128-byte swizzle over
+// their 128-byte lines.
+bool encode_latent_map(CUtensorMap* map, const void* pages, const pa_latent_shape_t& s) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t row = kLatentRow * 2;
+  cuuint64_t dims[4] = {64, kLatentRow / 64, (cuuint64_t)s.page_size, (cuuint64_t)s.num_pages};
+  cuuint64_t strides[3] = {128, row, row * s.page_size};
+  cuuint32_t box[4] = {64, kLatentRow / 64, kLatentBlock, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUtensorMapDataType ty = s.dtype == PA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(map, ty, 4, const_cast<void*>(pages), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T>
 cudaError_t launch_mma_t(const LatentParams& p, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
@@ -443,17 +475,20 @@ cudaError_t launch_mma_t(const LatentParams& p, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t launch_merge_t(const LatentParams& p, cudaStream_t stream) {
-  static std::atomic<unsigned long long> one{0}, four{0};
+  static std::atomic<unsigned long long> one{0}, several{0};
   const int64_t rows = (int64_t)p.num_merges * p.rows;
   if (rows >= kManyMergeRows)
     return launch_pdl(latent_merge_kernel<T, 1>, 0, one, p, (int)(rows / 4), 128, stream);
-  return launch_pdl(latent_merge_kernel<T, 4>, 0, four, p, (int)rows, 128, stream);
+  return launch_pdl(latent_merge_kernel<T, 8>, 0, several, p, (int)rows, 256, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_mma(const LatentParams& p, int dtype, cudaStream_t stream) {
-  if (dtype == PA_DTYPE_BF16) return launch_mma_t<__nv_bfloat16>(p, stream);
+cudaError_t launch_latent_mma(const LatentParams& params, const pa_latent_shape_t& shape,
+                              const void* pages, cudaStream_t stream) {
+  LatentParams p = params;
+  if (!encode_latent_map(&p.pages_map, pages, shape)) return cudaErrorInvalidValue;
+  if (shape.dtype == PA_DTYPE_BF16) return launch_mma_t<__nv_bfloat16>(p, stream);
   return launch_mma_t<__half>(p, stream);
 }
 

@@ -13,7 +13,7 @@
 // reads half of its B operand from either SM.  Per stage of 128 tokens a CTA
 // holds
 //   K [9 boxes of 64 dims][64 tokens][128 B]   its half of the stage's tokens
-//   V [4 boxes][128 tokens][128 B]             its half of the 512 values
+//   V [2 groups of 64 tokens][4 boxes][64 tokens][128 B]   its half of the 512 values
 // of which K is refilled in three groups of boxes and V in two groups of
 // tokens, each as soon as the MMAs that read it are done.
 //   warps 0-3: softmax and output.  Thread (warp, lane) owns row
@@ -22,7 +22,7 @@
 //              exchange their maxima through shared memory.
 //   warp 4:    in the pair's first CTA issues the MMAs of both; in either
 //              clears value rows
-//   warp 5:    copies q and K;  warp 6: copies V
+//   warp 5:    copies K;  warp 6: copies q and V
 // Per stage j: S(j+1) = q K^T into one of two TMEM buffers; softmax(j);
 // O += P(j) V(j), P from shared memory [2 boxes of 64 tokens][64 rows][128 B].
 // The weights are rounded to the element type once (fp16: times 2^7, so that
@@ -52,12 +52,14 @@ static_assert(kLatentRowsPair == 2 * kPairRows && kLatentStagePair == kPairToken
 struct PLayout {
   static constexpr int QBOX = kPairRows * 128;            // 8 KB
   static constexpr int KBOX = kPairTokens / 2 * 128;      // 8 KB
-  static constexpr int VBOX = kPairTokens * 128;          // 16 KB
+  static constexpr int VBOX = 64 * 128;                   // 8 KB
+  static constexpr int VGROUP = 4 * VBOX;                 // 64 tokens of the CTA's 256 values
   static constexpr int NG = 3, NV = 2;                    // groups of K boxes, of V tokens
+  static constexpr int BPG = 9 / NG;                      // boxes of a K group
   static constexpr int Q = 0;
   static constexpr int K = Q + 9 * QBOX;
   static constexpr int V = K + 9 * KBOX;
-  static constexpr int P = V + 4 * VBOX;
+  static constexpr int P = V + NV * VGROUP;
   static constexpr int PBOX = kPairRows * 128;
   static constexpr int BARS = P + 2 * PBOX;
   // mbarriers that the MMAs arrive on, in both CTAs
@@ -116,13 +118,12 @@ __device__ __forceinline__ uint32_t in_first_cta(uint32_t addr) {
 }
 
 // TMA copies into this CTA whose barrier may be the other CTA's.
-__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1,
-                                                 int c2, int c3, uint32_t bar, uint64_t policy) {
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                                 int c2, uint32_t bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".cta_group::2.L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar),
-      "l"(policy)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
       : "memory");
 }
 
@@ -216,22 +217,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint64_t once = l2_evict_first_policy(), keep = tc5::l2_evict_normal_policy();
     const int box = p.page_size < 64 ? p.page_size : 64;  // tokens of one copy
     const int copies = kPairTokens / box;                 // of a stage
+    const int per = 64 / box;                             // of a group
     const int groups = keys ? L::NG : L::NV;
     const uint32_t full0 = in_first_cta(sb + (keys ? L::K_FULL : L::V_FULL));
     for (int i = first; i < last && good; ++i) {
       if (i > first) s = p.segments[i];
       if (!usable(s)) continue;
       const int32_t* table = p.block_table + (int64_t)s.b * p.max_pages;
-      if (keys) {  // q: the CTA's 64 rows
+      if (!keys) {  // q: the CTA's 64 rows, by the warp whose own copies are needed later
         good = qc == 0 || tc5::warp_wait(sb + L::Q_FREE, (uint32_t)((qc - 1) & 1), p.wait_ns);
         if (!good) break;
-        if (lane == 0) {
-          if (rank == 0) mbar_arrive_expect_tx(sb + L::Q_FULL, 2 * 9 * L::QBOX);
-          const int row = s.packed0 + rank * kPairRows;
-          const uint32_t bar = in_first_cta(sb + L::Q_FULL);
-          for (int b = 0; b < 9; ++b)
-            tma_load_2d_pair(sb + L::Q + b * L::QBOX, &q_map, b * 64, row, bar, once);
-        }
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(sb + L::Q_FULL, 2 * 9 * L::QBOX);
+        if (lane < 9)
+          tma_load_2d_pair(sb + L::Q + lane * L::QBOX, &q_map, lane * 64, s.packed0 + rank * kPairRows,
+                           in_first_cta(sb + L::Q_FULL), once);
         ++qc;
       }
       const int n = stages_of(s);
@@ -252,36 +251,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           good = c == 0 || tc5::warp_wait(sb + (keys ? L::K_FREE : L::V_FREE) + 8 * g,
                                      (uint32_t)((c - 1) & 1), p.wait_ns);
           if (!good) break;
-          if (keys) {  // three boxes of the CTA's half of the tokens
+          // One lane a copy
+          if (keys) {  // boxes of the CTA's half of the tokens
             if (rank == 0 && lane == 0) {
-              const uint32_t bytes = (uint32_t)(__popc(have) * box * 128 * 3);
+              const uint32_t bytes = (uint32_t)(__popc(have) * box * 128 * L::BPG);
               if (bytes) mbar_arrive_expect_tx(sb + L::K_FULL + 8 * g, bytes);
               else mbar_arrive(sb + L::K_FULL + 8 * g);
             }
-            const int u = lane - rank * (copies / 2);  // of the half
-            if (page >= 0 && u >= 0 && u < copies / 2)
+            const int u = lane - rank * per;
+            if (page >= 0 && u >= 0 && u < per)
 #pragma unroll
-              for (int b = 0; b < 3; ++b)
-                tma_load_4d_pair(sb + L::K + (3 * g + b) * L::KBOX + u * box * 128, &p.pages_map, 0,
-                                 3 * g + b, row, page, full0 + 8 * g, keep);
+              for (int b = L::BPG * g; b < L::BPG * (g + 1); ++b)
+                tma_load_3d_pair(sb + L::K + b * L::KBOX + u * box * 128, &p.pages_map, b * 64, row, page,
+                                 full0 + 8 * g, keep);
           } else {     // four boxes, the CTA's half of the values, of 64 tokens
-            const int per = copies / L::NV;
             const unsigned mask = ((1u << per) - 1u) << (g * per);
             // rows to clear: the second CTA's copies complete on its own barrier
             const bool clear = (missing & mask) != 0 || (valid % kLatentBlock != 0 && (valid - 1) / 64 == g);
             const uint32_t bytes = (uint32_t)(__popc(have & mask) * box * 128 * 4);
+            const bool here = rank != 0 && clear;
             if (lane == 0 && (rank == 0 || clear)) {
-              const uint32_t bar = sb + (rank == 0 ? L::V_FULL : L::V_HERE) + 8 * g;
+              const uint32_t bar = sb + (here ? L::V_HERE : L::V_FULL) + 8 * g;
               if (bytes) mbar_arrive_expect_tx(bar, rank == 0 && !clear ? 2 * bytes : bytes);
               else mbar_arrive(bar);
             }
-            const uint32_t bar = rank != 0 && clear ? sb + L::V_HERE + 8 * g : full0 + 8 * g;
             __syncwarp();
-            if (page >= 0 && (mask >> lane & 1))
+            const int u = lane - g * per;
+            const uint32_t bar = here ? sb + L::V_HERE + 8 * g : full0 + 8 * g;
+            if (page >= 0 && u >= 0 && u < per)
 #pragma unroll
               for (int b = 0; b < 4; ++b)
-                tma_load_4d_pair(sb + L::V + b * L::VBOX + lane * box * 128, &p.pages_map, 0,
-                                 (b >> 1) * 4 + rank * 2 + (b & 1), row, page, bar, keep);
+                tma_load_3d_pair(sb + L::V + g * L::VGROUP + b * L::VBOX + u * box * 128, &p.pages_map,
+                                 ((b >> 1) * 4 + rank * 2 + (b & 1)) * 64, row, page, bar, keep);
           }
           __syncwarp();
         }
@@ -294,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int g = 0; g < groups; ++g)
         mbar_wait_bounded_sleep(sb + (keys ? L::K_FREE : L::V_FREE) + 8 * g, (uint32_t)((c - 1) & 1),
                                 kDrainWaitNs);
-    if (lane == 0 && keys && qc > 0)
+    if (lane == 0 && qc > 0)
       mbar_wait_bounded_sleep(sb + L::Q_FREE, (uint32_t)((qc - 1) & 1), kDrainWaitNs);
     __syncwarp();
   } else if (warp == 4) {
@@ -319,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (tc5::elect_one()) {
           tc5::fence_after();
 #pragma unroll
-          for (int k = 12 * g; k < 12 * g + 12; ++k)
+          for (int k = 4 * L::BPG * g; k < 4 * L::BPG * (g + 1); ++k)
             tc5::mma2(t_s + (uint32_t)(64 * (cs & 1)),
                       tc5::desc_at(q_desc, (k >> 2) * L::QBOX + (k & 3) * 32),
                       tc5::desc_at(k_desc, (k >> 2) * L::KBOX + (k & 3) * 32), idesc_s, k > 0 ? 1u : 0u);
@@ -364,8 +365,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               const int from = bad >> u & 1 ? 0 : valid - u * kLatentBlock, rows = kLatentBlock - from;
               for (int x = lane; x < rows * 8 * 4; x += 32) {
                 const int b = x / (rows * 8), k = x % (rows * 8);
-                *reinterpret_cast<uint4*>(base + L::V + b * L::VBOX + (u * kLatentBlock + from) * 128 +
-                                          k * 16) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(base + L::V + g * L::VGROUP + b * L::VBOX +
+                                          ((u & 3) * kLatentBlock + from) * 128 + k * 16) = make_uint4(0u, 0u, 0u, 0u);
               }
             }
             fence_proxy_async_smem();  // the tensor core reads them (async proxy)
@@ -388,7 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 for (int h = 0; h < 2; ++h)
                   tc5::mma2(t_o + (uint32_t)(128 * h),
                             tc5::desc_at(p_desc, (k >> 2) * L::PBOX + (k & 3) * 32),
-                            tc5::desc_at(v_desc, 2 * h * L::VBOX + k * 2048), idesc_o,
+                            tc5::desc_at(v_desc, g * L::VGROUP + 2 * h * L::VBOX + (k & 3) * 2048), idesc_o,
                             j > 0 || k > 0 ? 1u : 0u);
               }
             tc5::commit2(sb + L::V_FREE + 8 * g);
@@ -601,6 +602,23 @@ bool encode_q(CUtensorMap* map, const LatentParams& p, int dtype) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The pool [P][S][576] with boxes of `tokens` tokens by 64 dims.  (With the
+// row split into a dimension of nine boxes the copies run 12 % slower.)
+bool encode_boxes(CUtensorMap* map, const void* pages, const pa_latent_shape_t& s, int tokens) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t row = kLatentRow * 2;
+  cuuint64_t dims[3] = {kLatentRow, (cuuint64_t)s.page_size, (cuuint64_t)s.num_pages};
+  cuuint64_t strides[2] = {row, row * s.page_size};
+  cuuint32_t box[3] = {64, (cuuint32_t)tokens, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType ty = s.dtype == PA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(map, ty, 3, const_cast<void*>(pages), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T>
 cudaError_t launch_t(const LatentParams& p, const CUtensorMap& q_map, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
@@ -610,10 +628,14 @@ cudaError_t launch_t(const LatentParams& p, const CUtensorMap& q_map, cudaStream
 
 }  // namespace
 
-cudaError_t launch_latent_pair(const LatentParams& p, int dtype, cudaStream_t stream) {
+cudaError_t launch_latent_pair(const LatentParams& params, const pa_latent_shape_t& shape,
+                               const void* pages, cudaStream_t stream) {
+  LatentParams p = params;
   CUtensorMap q_map;
-  if (!encode_q(&q_map, p, dtype)) return cudaErrorInvalidValue;
-  if (dtype == PA_DTYPE_BF16) return launch_t<__nv_bfloat16>(p, q_map, stream);
+  if (!encode_q(&q_map, p, shape.dtype) ||
+      !encode_boxes(&p.pages_map, pages, shape, shape.page_size < 64 ? shape.page_size : 64))
+    return cudaErrorInvalidValue;
+  if (shape.dtype == PA_DTYPE_BF16) return launch_t<__nv_bfloat16>(p, q_map, stream);
   return launch_t<__half>(p, q_map, stream);
 }
 

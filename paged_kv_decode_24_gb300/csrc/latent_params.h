@@ -46,8 +46,11 @@ struct LatentParams {
   int32_t num_ranges, num_segments, num_merges, num_slots, total_q, rows;
 };
 
-cudaError_t launch_latent_mma(const LatentParams& p, int dtype, cudaStream_t stream);
-cudaError_t launch_latent_pair(const LatentParams& p, int dtype, cudaStream_t stream);
+// pages_map is the launchers' to fill: each kernel has boxes of its own.
+cudaError_t launch_latent_mma(const LatentParams& p, const pa_latent_shape_t& shape, const void* pages,
+                              cudaStream_t stream);
+cudaError_t launch_latent_pair(const LatentParams& p, const pa_latent_shape_t& shape,
+                               const void* pages, cudaStream_t stream);
 cudaError_t launch_latent_merge(const LatentParams& p, int dtype, cudaStream_t stream);
 
 // Expanded attention.
