@@ -286,8 +286,6 @@ extern "C" pa_status_t pa_latent_prefill(const pa_latent_shape_t* shape,
   p.v = v;
   p.out = out;
   p.ws = reinterpret_cast<const int32_t*>(ws);
-  p.cu_q = reinterpret_cast<const int32_t*>(ws + l.cu_q);
-  p.cu_k = reinterpret_cast<const int32_t*>(ws + l.cu_k);
   p.tiles = reinterpret_cast<const LatentTile*>(ws + l.work);
   p.status = dev_status;
   p.k_token = k_token_stride;

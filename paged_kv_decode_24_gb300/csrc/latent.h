@@ -37,9 +37,11 @@ struct LatentMerge {
   int32_t slot0, n, row0, nrows;
 };
 
-// An expanded tile: query tokens tok0 .. tok0 + ntok - 1 of one head.
+// An expanded tile: ntok query tokens of one head, from packed row q0; the
+// first sits at position pos0 of its sequence, whose tokens are packed from
+// k0.
 struct LatentTile {
-  int32_t b, head, tok0, ntok;
+  int32_t head, ntok, q0, pos0, k0, pad0, pad1, pad2;
 };
 
 // Blob = header (16 x int32) | cu_q [B+1] | cu_k [B+1] | then for

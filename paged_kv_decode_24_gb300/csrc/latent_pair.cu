@@ -20,9 +20,8 @@
 //              32 (warp % 2) + lane of the CTA's 64: tokens 0-63 of the stage
 //              in warps 0-1, 64-127 in warps 2-3; the two threads of a row
 //              exchange their maxima through shared memory.
-//   warp 4:    in the pair's first CTA issues the MMAs of both; in either
-//              clears value rows
-//   warp 5:    copies K;  warp 6: copies q and V
+//   warp 4:    in the pair's first CTA one thread issues the MMAs of both
+//   warp 5:    copies K;  warp 6: copies q and V, clears value rows
 // Per stage j: S(j+1) = q K^T into one of two TMEM buffers; softmax(j);
 // O += P(j) V(j), P from shared memory [2 boxes of 64 tokens][64 rows][128 B].
 // The weights are rounded to the element type once (fp16: times 2^7, so that
@@ -64,9 +63,9 @@ struct PLayout {
   static constexpr int BARS = P + 2 * PBOX;
   // mbarriers that the MMAs arrive on, in both CTAs
   static constexpr int Q_FREE = BARS;
-  static constexpr int K_FREE = Q_FREE + 8;               // NG
-  static constexpr int V_FREE = K_FREE + 8 * NG;          // NV
-  static constexpr int S_DONE = V_FREE + 8 * NV;          // 2
+  static constexpr int K_FREE = Q_FREE + 8;               // NG - 1 (S_DONE frees the last group)
+  static constexpr int V_FREE = K_FREE + 8 * (NG - 1);    // NV - 1 (PV_DONE frees the last group)
+  static constexpr int S_DONE = V_FREE + 8 * (NV - 1);    // 2
   static constexpr int PV_DONE = S_DONE + 16;
   static constexpr int DRAIN = PV_DONE + 8;
   // in the first CTA: the copies of both have landed
@@ -74,12 +73,13 @@ struct PLayout {
   static constexpr int K_FULL = Q_FULL + 8;               // NG
   static constexpr int V_FULL = K_FULL + 8 * NG;          // NV
   // values with rows to clear: landed in the second CTA (there), cleared in
-  // it (in the first CTA)
+  // both (in the first CTA)
   static constexpr int V_HERE = V_FULL + 8 * NV;          // NV
-  static constexpr int V_PEER = V_HERE + 8 * NV;          // NV
+  static constexpr int V_CLEAR = V_HERE + 8 * NV;         // NV
   // in the first CTA: the weights of both are written
-  static constexpr int P_READY = V_PEER + 8 * NV;
-  static constexpr int TMEM_SLOT = P_READY + 8;
+  static constexpr int P_READY = V_CLEAR + 8 * NV;
+  static constexpr int CLEAR = P_READY + 8;               // NV flags: this use has rows to clear
+  static constexpr int TMEM_SLOT = CLEAR + 4 * NV;
   static constexpr int XMAX = align_up(TMEM_SLOT + 8, 16);  // [2][128] floats: row maxima, sums
   static constexpr int BYTES = XMAX + 2 * 128 * 4 + 1024;
 };
@@ -178,7 +178,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (!planned) set_status(p.status, PA_DEV_PLAN_MISMATCH);
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.pages_map)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&q_map)) : "memory");
-    for (int b = L::Q_FREE; b < L::P_READY; b += 8) mbar_init(sb + b, 1);
+    for (int b = L::Q_FREE; b < L::V_CLEAR; b += 8) mbar_init(sb + b, 1);
+    for (int b = L::V_CLEAR; b < L::P_READY; b += 8) mbar_init(sb + b, 2);
     mbar_init(sb + L::P_READY, 8);
     fence_barrier_init();
   }
@@ -219,6 +220,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int copies = kPairTokens / box;                 // of a stage
     const int per = 64 / box;                             // of a group
     const int groups = keys ? L::NG : L::NV;
+    int clears = 0;                                       // uses of V_HERE, a bit a group: parities
+    // use c of group g has been read
+    auto wait_free = [&](int g, int c, uint64_t limit) {
+      if (g < groups - 1)
+        return tc5::warp_wait(sb + (keys ? L::K_FREE : L::V_FREE) + 8 * g, (uint32_t)(c & 1), limit);
+      return keys ? tc5::warp_wait(sb + L::S_DONE + 8 * (c & 1), (uint32_t)((c >> 1) & 1), limit)
+                  : tc5::warp_wait(sb + L::PV_DONE, (uint32_t)(c & 1), limit);
+    };
     const uint32_t full0 = in_first_cta(sb + (keys ? L::K_FULL : L::V_FULL));
     for (int i = first; i < last && good; ++i) {
       if (i > first) s = p.segments[i];
@@ -248,8 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int row = tok % p.page_size;
         const int valid = min(kPairTokens, s.tok1 - s.tok0 - j * kPairTokens);
         for (int g = 0; g < groups; ++g) {
-          good = c == 0 || tc5::warp_wait(sb + (keys ? L::K_FREE : L::V_FREE) + 8 * g,
-                                     (uint32_t)((c - 1) & 1), p.wait_ns);
+          good = c == 0 || wait_free(g, c - 1, p.wait_ns);
           if (!good) break;
           // One lane a copy
           if (keys) {  // boxes of the CTA's half of the tokens
@@ -272,6 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const bool here = rank != 0 && clear;
             if (lane == 0 && (rank == 0 || clear)) {
               const uint32_t bar = sb + (here ? L::V_HERE : L::V_FULL) + 8 * g;
+              *reinterpret_cast<volatile int*>(base + L::CLEAR + 4 * g) = clear;
               if (bytes) mbar_arrive_expect_tx(bar, rank == 0 && !clear ? 2 * bytes : bytes);
               else mbar_arrive(bar);
             }
@@ -283,6 +292,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               for (int b = 0; b < 4; ++b)
                 tma_load_3d_pair(sb + L::V + g * L::VGROUP + b * L::VBOX + u * box * 128, &p.pages_map,
                                  ((b >> 1) * 4 + rank * 2 + (b & 1)) * 64, row, page, bar, keep);
+            if (clear) {  // the rest of the last 16 tokens, and the tokens of bad pages
+              good = rank == 0 ? tc5::warp_wait(sb + L::V_FULL + 8 * g, (uint32_t)(c & 1), p.wait_ns)
+                               : tc5::warp_wait(sb + L::V_HERE + 8 * g, (uint32_t)(clears >> g & 1), p.wait_ns);
+              clears ^= 1 << g;
+              if (!good) break;
+              __syncwarp();
+              for (int v = 0; v < 4; ++v) {
+                const int at = g * 64 + v * kLatentBlock;  // first token of the block
+                if (at >= valid) break;
+                const int from = missing >> (at / box) & 1 ? 0 : valid - at, rows = kLatentBlock - from;
+                for (int x = lane; x < rows * 8 * 4; x += 32) {
+                  const int b = x / (rows * 8), k = x % (rows * 8);
+                  *reinterpret_cast<uint4*>(base + L::V + g * L::VGROUP + b * L::VBOX +
+                                            (v * kLatentBlock + from) * 128 + k * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+              }
+              fence_proxy_async_smem();  // the tensor core reads them (async proxy)
+              __syncwarp();
+              if (lane == 0) arrive_first_cta(sb + L::V_CLEAR + 8 * g);
+            }
           }
           __syncwarp();
         }
@@ -291,96 +320,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (!good && lane == 0) set_status(p.status, PA_DEV_TIMEOUT);
     // every copy has been read, and with it every arrival that the MMAs send
     // here has come, before the CTA ends
-    if (lane == 0 && c > 0)
-      for (int g = 0; g < groups; ++g)
-        mbar_wait_bounded_sleep(sb + (keys ? L::K_FREE : L::V_FREE) + 8 * g, (uint32_t)((c - 1) & 1),
-                                kDrainWaitNs);
-    if (lane == 0 && qc > 0)
-      mbar_wait_bounded_sleep(sb + L::Q_FREE, (uint32_t)((qc - 1) & 1), kDrainWaitNs);
+    if (c > 0)
+      for (int g = 0; g < groups; ++g) wait_free(g, c - 1, kDrainWaitNs);
+    if (qc > 0) tc5::warp_wait(sb + L::Q_FREE, (uint32_t)((qc - 1) & 1), kDrainWaitNs);
     __syncwarp();
   } else if (warp == 4) {
-    // ================= MMAs (first CTA) =================
-    // The second CTA's warp only clears value rows.
-    const uint32_t idesc_s = tc5::instr_desc<T>(128, kPairTokens, false);
-    const uint32_t idesc_o = tc5::instr_desc<T>(128, 256, true);
-    const uint64_t q_desc = tc5::smem_desc(sb + L::Q, 16, 1024), k_desc = tc5::smem_desc(sb + L::K, 16, 1024);
-    const uint64_t p_desc = tc5::smem_desc(sb + L::P, 16, 1024);
-    const uint64_t v_desc = tc5::smem_desc(sb + L::V, L::VBOX, 1024);
-    bool good = true;
-    int c = 0, qc = 0;             // stages, segments
-    int cleared[L::NV] = {0, 0};   // uses of each value group with rows to clear
-    auto wait = [&](int bar, int count) {
-      return tc5::warp_wait(sb + bar, (uint32_t)(count & 1), p.wait_ns);
-    };
-    // S of stage number cs
-    auto scores = [&](int cs, bool last_of_segment) {
+    // ================= MMAs (one thread of the first CTA) =================
+    if (rank == 0 && tc5::elect_one()) {
+      const uint32_t idesc_s = tc5::instr_desc<T>(128, kPairTokens, false);
+      const uint32_t idesc_o = tc5::instr_desc<T>(128, 256, true);
+      const uint64_t q_desc = tc5::smem_desc(sb + L::Q, 16, 1024), k_desc = tc5::smem_desc(sb + L::K, 16, 1024);
+      const uint64_t p_desc = tc5::smem_desc(sb + L::P, 16, 1024);
+      const uint64_t v_desc = tc5::smem_desc(sb + L::V, L::VBOX, 1024);
+      bool good = true;
+      int c = 0, qc = 0;             // stages, segments
+      int cleared[L::NV] = {0, 0};   // uses of each value group with rows to clear
+      auto wait = [&](int bar, int count) {
+        return mbar_wait_bounded(sb + bar, (uint32_t)(count & 1), p.wait_ns);
+      };
+      // S of stage number cs
+      auto scores = [&](int cs, bool last_of_segment) {
 #pragma unroll
-      for (int g = 0; g < L::NG; ++g) {
-        if (!wait(L::K_FULL + 8 * g, cs)) return false;
-        if (tc5::elect_one()) {
+        for (int g = 0; g < L::NG; ++g) {
+          if (!wait(L::K_FULL + 8 * g, cs)) return false;
           tc5::fence_after();
 #pragma unroll
           for (int k = 4 * L::BPG * g; k < 4 * L::BPG * (g + 1); ++k)
             tc5::mma2(t_s + (uint32_t)(64 * (cs & 1)),
                       tc5::desc_at(q_desc, (k >> 2) * L::QBOX + (k & 3) * 32),
                       tc5::desc_at(k_desc, (k >> 2) * L::KBOX + (k & 3) * 32), idesc_s, k > 0 ? 1u : 0u);
-          tc5::commit2(sb + L::K_FREE + 8 * g);
-          if (g == L::NG - 1) {
-            tc5::commit2(sb + L::S_DONE + 8 * (cs & 1));
-            if (last_of_segment) tc5::commit2(sb + L::Q_FREE);
-          }
+          if (g < L::NG - 1) tc5::commit2(sb + L::K_FREE + 8 * g);
         }
-        __syncwarp();
-      }
-      return true;
-    };
-    for (int i = first; i < last && good; ++i) {
-      if (i > first) s = p.segments[i];
-      if (!usable(s)) continue;
-      const int32_t* table = p.block_table + (int64_t)s.b * p.max_pages;
-      const int n = stages_of(s);
-      if (rank == 0) good = wait(L::Q_FULL, qc) && scores(c, n == 1);
-      // lane u < 8: the page of tokens 16 u .. of a stage, a stage ahead of its use
-      const int lane_end = lane < 8 ? s.tok1 : 0;
-      int next = table_entry(table, p.page_size, s.tok0 + lane * kLatentBlock, lane_end);
-      for (int j = 0; j < n && good; ++j) {
-        const int tok = s.tok0 + j * kPairTokens + lane * kLatentBlock;
-        const unsigned bad = __ballot_sync(kFull, tok < lane_end && (next < 0 || next >= p.num_pages));
-        next = table_entry(table, p.page_size, tok + kPairTokens, lane_end);
-        const int valid = min(kPairTokens, s.tok1 - s.tok0 - j * kPairTokens);
-        if (rank == 0) {
+        tc5::commit2(sb + L::S_DONE + 8 * (cs & 1));
+        if (last_of_segment) tc5::commit2(sb + L::Q_FREE);
+        return true;
+      };
+      for (int i = first; i < last && good; ++i) {
+        if (i > first) s = p.segments[i];
+        if (!usable(s)) continue;
+        const int n = stages_of(s);
+        good = wait(L::Q_FULL, qc) && scores(c, n == 1);
+        for (int j = 0; j < n && good; ++j) {
+          const int valid = min(kPairTokens, s.tok1 - s.tok0 - j * kPairTokens);
           if (j + 1 < n) good = scores(c + j + 1, j + 2 == n);
           good = good && wait(L::P_READY, c + j);
           if (!good) break;
-        }
 #pragma unroll
-        for (int g = 0; g < L::NV; ++g) {
-          const bool clear =
-              (bad >> (4 * g) & 15) != 0 || (valid % kLatentBlock != 0 && (valid - 1) / 64 == g);
-          if (rank != 0 && !clear) continue;
-          good = rank == 0 ? wait(L::V_FULL + 8 * g, c + j) : wait(L::V_HERE + 8 * g, cleared[g]);
-          if (!good) break;
-          if (clear) {  // the rest of the last 16 tokens, and the tokens of bad pages
-            for (int u = 4 * g; u < 4 * g + 4 && u * kLatentBlock < valid; ++u) {
-              const int from = bad >> u & 1 ? 0 : valid - u * kLatentBlock, rows = kLatentBlock - from;
-              for (int x = lane; x < rows * 8 * 4; x += 32) {
-                const int b = x / (rows * 8), k = x % (rows * 8);
-                *reinterpret_cast<uint4*>(base + L::V + g * L::VGROUP + b * L::VBOX +
-                                          ((u & 3) * kLatentBlock + from) * 128 + k * 16) = make_uint4(0u, 0u, 0u, 0u);
-              }
-            }
-            fence_proxy_async_smem();  // the tensor core reads them (async proxy)
-            __syncwarp();
-            if (rank != 0) {
-              if (lane == 0) arrive_first_cta(sb + L::V_PEER + 8 * g);
-            } else {
-              good = wait(L::V_PEER + 8 * g, cleared[g]);
-            }
-            ++cleared[g];
+          for (int g = 0; g < L::NV; ++g) {
+            good = wait(L::V_FULL + 8 * g, c + j);
+            if (good && *reinterpret_cast<volatile int*>(base + L::CLEAR + 4 * g))
+              good = wait(L::V_CLEAR + 8 * g, cleared[g]++);
             if (!good) break;
-          }
-          if (rank != 0) continue;
-          if (tc5::elect_one()) {
             tc5::fence_after();
 #pragma unroll
             for (int k = 4 * g; k < 4 * g + 4; ++k)
@@ -392,18 +382,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                             tc5::desc_at(v_desc, g * L::VGROUP + 2 * h * L::VBOX + (k & 3) * 2048), idesc_o,
                             j > 0 || k > 0 ? 1u : 0u);
               }
-            tc5::commit2(sb + L::V_FREE + 8 * g);
-            if (g == L::NV - 1) tc5::commit2(sb + L::PV_DONE);
+            if (g < L::NV - 1) tc5::commit2(sb + L::V_FREE + 8 * g);
           }
-          __syncwarp();
+          if (good) tc5::commit2(sb + L::PV_DONE);
         }
+        c += n;
+        ++qc;
       }
-      c += n;
-      ++qc;
+      if (!good) set_status(p.status, PA_DEV_TIMEOUT);
+      // every MMA issued has finished before either CTA goes on
+      tc5::commit2(sb + L::DRAIN);
     }
-    if (!good && lane == 0) set_status(p.status, PA_DEV_TIMEOUT);
-    // every MMA issued has finished before either CTA goes on
-    if (rank == 0 && tc5::elect_one()) tc5::commit2(sb + L::DRAIN);
     __syncwarp();
     tc5::warp_wait(sb + L::DRAIN, 0u, kDrainWaitNs);
   } else {

@@ -61,8 +61,6 @@ struct LatentPrefillParams {
   const void* v;
   void* out;
   const int32_t* ws;
-  const int32_t* cu_q;
-  const int32_t* cu_k;
   const LatentTile* tiles;
   int32_t* status;
   int64_t k_token, k_head, kr_token, v_token, v_head;  // strides, elements

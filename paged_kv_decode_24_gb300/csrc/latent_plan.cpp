@@ -12,7 +12,7 @@
 // kMinPiece stages is moved to the tile's edge.
 //
 // Expanded form.  A tile is up to kLatentRowsExpanded query tokens of one
-// head, longest first, so that the short ones fill the tail of the grid.
+// head, the costliest first, so that the cheap ones fill the tail of the grid.
 #include <stdlib.h>
 #include <string.h>
 
@@ -135,22 +135,23 @@ void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_
     w->ranges.push_back((int32_t)w->segments.size());
 }
 
-void expanded_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_t* qs, int rows,
+void expanded_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_t* qs,
+                   const std::vector<int32_t>& cu_q, const std::vector<int32_t>& cu_k, int rows,
                    Work* w) {
   struct Sized {
     LatentTile t;
-    int32_t span;
+    int64_t cost;
   };
   std::vector<Sized> all;
   for (int b = 0; b < s.batch; ++b)
     for (int32_t t0 = 0; t0 < qs[b]; t0 += rows) {
-      const int32_t n = std::min(rows, qs[b] - t0);
-      const int32_t span = lens[b] - qs[b] + t0 + n;
-      for (int h = 0; h < s.num_heads; ++h) all.push_back({{b, h, t0, n}, span});
+      const int32_t n = std::min(rows, qs[b] - t0), pos0 = lens[b] - qs[b] + t0;
+      const int64_t cost = ((int64_t)pos0 + n + 127) / 128;  // stages
+      for (int h = 0; h < s.num_heads; ++h)
+        all.push_back({{h, n, cu_q[(size_t)b] + t0, pos0, cu_k[(size_t)b], 0, 0, 0}, cost});
     }
-  std::stable_sort(all.begin(), all.end(), [](const Sized& x, const Sized& y) {
-    return x.span != y.span ? x.span > y.span : x.t.ntok > y.t.ntok;
-  });
+  std::stable_sort(all.begin(), all.end(),
+                   [](const Sized& x, const Sized& y) { return x.cost > y.cost; });
   for (const Sized& x : all) w->tiles.push_back(x.t);
 }
 
@@ -202,7 +203,7 @@ extern "C" pa_status_t pa_latent_plan(const pa_latent_shape_t* shape, const int3
     absorbed_work(*shape, seq_lens_host, q_lens_host, cu_q, rows,
                   rows == kLatentRowsPair ? std::max(1, num_sms / 2) : num_sms, o.forced_splits, &w);
   else
-    expanded_work(*shape, seq_lens_host, q_lens_host, rows, &w);
+    expanded_work(*shape, seq_lens_host, q_lens_host, cu_q, cu_k, rows, &w);
   const size_t ranges = absorbed ? w.ranges.size() - 1 : w.tiles.size();
   if (ranges > (size_t)INT32_MAX || w.segments.size() > (size_t)INT32_MAX ||
       w.slots > INT32_MAX / rows)

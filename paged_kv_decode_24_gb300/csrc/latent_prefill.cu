@@ -10,19 +10,22 @@
 // cores work on the other.
 //   warps 0-3: softmax and output of tile 0 (thread = row = TMEM lane)
 //   warps 4-7: the same of tile 1
-//   warp 8:    issues the MMAs
-//   warp 9:    copies q, then stages of 128 tokens' keys and values
+//   warp 8:    issues the MMAs;  warp 9: copies q and keys;  warp 10: copies values
 // TMEM (512 columns): S0, S1 (128 each), O0, O1 (128 each).  The weights
 // P_t take S_t's place, two 16-bit weights a column: the A operand of P V.
-// Shared memory (128-byte swizzle): q 2 x [DK/64][128 rows][128 B], two key
-// stages [DK/64][128 tokens][128 B], one value stage [D/64][128 tokens][128 B].
+// Shared memory (128-byte swizzle): q 2 x [DK/64][128 rows][128 B] takes
+// almost half.  The rest is two rings of four 16 KB units each:
+// keys [128 tokens][128 B] of 64 dims, DK/64 of them a stage, and values
+// [D/64][64 tokens][128 B] of half a stage.  That is two stages of values and
+// one and a third of keys at D = 128 (with two of keys and one of values each
+// product waited 0.5 us of a stage's 2.1 for the values).
 //
-// Per stage j and tile t:
+// Per stage j of 128 tokens and tile t:
 //   S_t(j) = q_t K(j)^T             DK/16 MMAs, M = N = 128
-//   softmax in registers, P_t(j) over S_t(j)
-//   O_t += P_t(j) V(j)              8 MMAs, N = D
+//   softmax in registers, P_t(j) over S_t(j), in two halves of 64 tokens
+//   O_t += P_t(j) V(j)              4 MMAs, N = D, as each half is written
 //   S_t(j+1) once P V(j) of the tile is done, which reads the same columns
-// in the order PV_0, S_0, PV_1, S_1.  The weights are rounded to the element
+// in the order PV_0, PV_1, S_0, S_1.  The weights are rounded to the element
 // type once: the product's time is what a second part of them would cost
 // again, and the error stays below that of rounding the result.  For fp16
 // they carry a factor 2^7, so that small weights stay normal numbers.  The
@@ -44,32 +47,33 @@ namespace {
 
 constexpr int kRows = 128;                  // query rows of a tile (TMEM lanes)
 constexpr int kTokens = 128;                // tokens of a stage
-constexpr int kPrefillThreads = 10 * 32;
+constexpr int kPrefillThreads = 11 * 32;
 constexpr float kLazyLog2 = 8.f;            // the maximum is raised when it grows by more than 2^8
 static_assert(kLatentRowsExpanded == 2 * kRows, "a CTA has two tiles");
 
 template <int D>
 struct XLayout {
   static constexpr int DK = D + kRope;
+  static constexpr int KB = DK / 64;                    // key units of a stage
   static constexpr int BOX = kTokens * 128;             // 16 KB: 64 dims of 128 rows
-  static constexpr int QTILE = DK / 64 * BOX;
-  static constexpr int KSTAGE = DK / 64 * BOX;
-  static constexpr int VSTAGE = D / 64 * BOX;
-  static constexpr int NK = 2;
+  static constexpr int QTILE = KB * BOX;
+  static constexpr int VBOX = kTokens / 2 * 128;        // 8 KB: 64 dims of 64 tokens
+  static constexpr int VUNIT = D / 64 * VBOX;
+  static constexpr int NK = 4;                          // units of the key ring
+  static constexpr int NV = 4;                          // units of the value ring
   static constexpr int Q = 0;
   static constexpr int K = Q + 2 * QTILE;
-  static constexpr int V = K + NK * KSTAGE;
-  static constexpr int BARS = V + VSTAGE;
+  static constexpr int V = K + NK * BOX;
+  static constexpr int BARS = V + NV * VUNIT;
   // mbarriers
   static constexpr int Q_FULL = BARS;
-  static constexpr int K_FULL = Q_FULL + 8;             // NK
-  static constexpr int K_FREE = K_FULL + 8 * NK;        // NK
-  static constexpr int V_FULL = K_FREE + 8 * NK;
-  static constexpr int V_FREE = V_FULL + 8;
-  static constexpr int S_DONE = V_FREE + 8;             // one per tile, as the next two
-  static constexpr int P_READY = S_DONE + 16;
-  static constexpr int PV_DONE = P_READY + 16;
-  static constexpr int DRAIN = PV_DONE + 16;
+  static constexpr int K_FULL = Q_FULL + 8;             // stages j & 1
+  static constexpr int V_FULL = K_FULL + 16;            // stages j & 1
+  static constexpr int S_DONE = V_FULL + 16;            // one per tile, as PV_DONE
+  static constexpr int PV_DONE = S_DONE + 16;
+  static constexpr int V_CLEAR = PV_DONE + 16;          // the last stage's rows
+  static constexpr int P_READY = V_CLEAR + 8;           // two halves per tile
+  static constexpr int DRAIN = P_READY + 32;
   static constexpr int TMEM_SLOT = DRAIN + 8;
   static constexpr int FLAG = TMEM_SLOT + 8;
   static constexpr int BYTES = FLAG + 8 + 1024;
@@ -94,7 +98,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     latent_prefill_kernel(const __grid_constant__ LatentPrefillParams p,
                           const __grid_constant__ XMaps maps) {
   using L = XLayout<D>;
-  constexpr int DK = L::DK;
   extern __shared__ unsigned char smem_dyn[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -102,24 +105,31 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* flag = reinterpret_cast<int*>(base + L::FLAG);
 
+  // The plan is written by the upload alone, which the programmatic launch
+  // does not overlap: it may be read before the wait for the kernel ahead.
+  const int4 h0 = reinterpret_cast<const int4*>(p.ws)[0], h1 = reinterpret_cast<const int4*>(p.ws)[1];
+  const LatentTile tile = p.tiles[blockIdx.x];
+  const int pos0 = tile.pos0;  // position of the first row
+  const int span = pos0 + tile.ntok;
+  const bool bad = h0.x != (int)kLatentMagic || h0.y != p.batch || h0.z != p.total_q ||
+                   h0.w != p.total_k || h1.z != PA_LATENT_EXPANDED || h1.w != kLatentRowsExpanded ||
+                   p.ws[8] != p.num_tiles || tile.head < 0 || tile.head >= p.heads || tile.ntok < 1 ||
+                   tile.ntok > kLatentRowsExpanded || tile.q0 < 0 || tile.q0 > p.total_q - tile.ntok ||
+                   pos0 < 0 || tile.k0 < 0 || (int64_t)tile.k0 + pos0 + tile.ntok > p.total_k;
+  // stages of each tile (0: it has no rows)
+  const int n0 = bad ? 0 : (pos0 + min(tile.ntok, kRows) + kTokens - 1) / kTokens;
+  const int n1 = bad || tile.ntok <= kRows ? 0 : (span + kTokens - 1) / kTokens;
+  const int n = max(n0, n1);
+  if (bad && threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
+
   if (threadIdx.x == 0) {
     *flag = 0;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.q)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.kr)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
-    mbar_init(sb + L::Q_FULL, 1);
-    for (int s = 0; s < L::NK; ++s) {
-      mbar_init(sb + L::K_FULL + 8 * s, 1);
-      mbar_init(sb + L::K_FREE + 8 * s, 1);
-    }
-    mbar_init(sb + L::V_FULL, 1);
-    mbar_init(sb + L::V_FREE, 1);
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(sb + L::S_DONE + 8 * t, 1);
-      mbar_init(sb + L::P_READY + 8 * t, 4);
-      mbar_init(sb + L::PV_DONE + 8 * t, 1);
-    }
+    for (int b = L::Q_FULL; b < L::P_READY; b += 8) mbar_init(sb + b, 1);
+    for (int b = L::P_READY; b < L::DRAIN; b += 8) mbar_init(sb + b, 4);
     mbar_init(sb + L::DRAIN, 1);
     fence_barrier_init();
   }
@@ -136,163 +146,144 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   pdl_launch_dependents();
   pdl_wait_primary();
 
-  const int4 h0 = reinterpret_cast<const int4*>(p.ws)[0];
-  bool bad = h0.x != (int)kLatentMagic || h0.y != p.batch || h0.z != p.total_q || h0.w != p.total_k ||
-             p.ws[6] != PA_LATENT_EXPANDED || p.ws[7] != kLatentRowsExpanded || p.ws[8] != p.num_tiles;
-  LatentTile tile{};
-  int cq = 0, qn = 0, ck = 0, len = 0;
-  if (!bad) {
-    tile = p.tiles[blockIdx.x];
-    bad = tile.b < 0 || tile.b >= p.batch || tile.head < 0 || tile.head >= p.heads || tile.tok0 < 0 ||
-          tile.ntok < 1 || tile.ntok > kLatentRowsExpanded;
-  }
-  if (!bad) {
-    cq = p.cu_q[tile.b];
-    qn = p.cu_q[tile.b + 1] - cq;
-    ck = p.cu_k[tile.b];
-    len = p.cu_k[tile.b + 1] - ck;
-    bad = cq < 0 || ck < 0 || qn > len || tile.tok0 + tile.ntok > qn || cq + qn > p.total_q ||
-          ck + len > p.total_k;
-  }
-  if (bad && threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
-  const int pos0 = len - qn + tile.tok0;  // position of the first row
-  // stages of each tile (0: it has no rows)
-  const int n0 = bad ? 0 : (pos0 + min(tile.ntok, kRows) + kTokens - 1) / kTokens;
-  const int n1 = bad || tile.ntok <= kRows ? 0 : (pos0 + tile.ntok + kTokens - 1) / kTokens;
-  const int n = max(n0, n1);
-  const int span = pos0 + tile.ntok;
-
-  if (warp == 9) {
+  if (warp == 9 || warp == 10) {
     // ================= copies =================
     if (lane == 0 && n > 0) {
+      const bool keys = warp == 9;
       const uint64_t keep = tc5::l2_evict_normal_policy(), once = l2_evict_first_policy();
-      const int tiles = n1 > 0 ? 2 : 1;
-      mbar_arrive_expect_tx(sb + L::Q_FULL, (uint32_t)(tiles * L::QTILE));
-      for (int t = 0; t < tiles; ++t)
-        for (int b = 0; b < DK / 64; ++b)
-          tma_load_3d(sb + L::Q + t * L::QTILE + b * L::BOX, &maps.q, b * 64, tile.head,
-                      cq + tile.tok0 + t * kRows, sb + L::Q_FULL, once);
-      int j = 0, jv = 0;
+      const int per = keys ? L::KB : 2, ring = keys ? L::NK : L::NV;  // units of a stage, of the ring
+      // The last tile of a stage has read its keys once its scores are done, and
+      // its values once its product is: no barriers of their own for the free units.
+      const uint32_t done = sb + (keys ? L::S_DONE : L::PV_DONE);
+      const uint32_t full = sb + (keys ? L::K_FULL : L::V_FULL);
+      if (keys) {
+        const int tiles = n1 > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(sb + L::Q_FULL, (uint32_t)(tiles * L::QTILE));
+        for (int t = 0; t < tiles; ++t)
+          for (int b = 0; b < L::KB; ++b)
+            tma_load_3d(sb + L::Q + t * L::QTILE + b * L::BOX, &maps.q, b * 64, tile.head,
+                        tile.q0 + t * kRows, sb + L::Q_FULL, once);
+      }
       bool good = true;
-      for (; j < n; ++j) {
-        const int s = j % L::NK, tok = ck + j * kTokens;
-        good = j < L::NK || mbar_wait_bounded_sleep(sb + L::K_FREE + 8 * s,
-                                                    (uint32_t)((j / L::NK - 1) & 1), p.wait_ns);
-        if (!good) break;
-        const uint32_t kb = sb + L::K + s * L::KSTAGE, kf = sb + L::K_FULL + 8 * s;
-        mbar_arrive_expect_tx(kf, L::KSTAGE);
-        for (int b = 0; b < D / 64; ++b)
-          tma_load_3d(kb + b * L::BOX, &maps.k, b * 64, p.k_token_major ? tile.head : tok,
-                      p.k_token_major ? tok : tile.head, kf, keep);
-        tma_load_3d(kb + D / 64 * L::BOX, &maps.kr, 0, tok, 0, kf, keep);
-        good = j < 1 || mbar_wait_bounded_sleep(sb + L::V_FREE, (uint32_t)((j - 1) & 1), p.wait_ns);
-        if (!good) break;
-        mbar_arrive_expect_tx(sb + L::V_FULL, L::VSTAGE);
-        for (int b = 0; b < D / 64; ++b)
-          tma_load_3d(sb + L::V + b * L::BOX, &maps.v, b * 64, p.v_token_major ? tile.head : tok,
-                      p.v_token_major ? tok : tile.head, sb + L::V_FULL, keep);
-        ++jv;
+      int j = 0, freed = 0;  // stages issued, stages known to be free
+      for (int u = 0; j < n && good; ++j) {
+        const uint32_t bar = full + 8 * (j & 1);
+        for (int x = 0; x < per; ++x, ++u) {
+          // the unit's slot was last used by unit u - ring, of stage (u - ring) / per
+          for (; good && freed * per < u - ring + 1; ++freed)
+            good = mbar_wait_bounded_sleep(done + (n1 > freed ? 8 : 0), (uint32_t)(freed & 1), p.wait_ns);
+          if (!good) break;
+          const int slot = u % ring, tok = tile.k0 + j * kTokens + (keys ? 0 : x * (kTokens / 2));
+          if (x == 0) mbar_arrive_expect_tx(bar, (uint32_t)(keys ? L::KB * L::BOX : 2 * L::VUNIT));
+          if (keys) {
+            if (x < D / 64)
+              tma_load_3d(sb + L::K + slot * L::BOX, &maps.k, x * 64, p.k_token_major ? tile.head : tok,
+                          p.k_token_major ? tok : tile.head, bar, keep);
+            else
+              tma_load_3d(sb + L::K + slot * L::BOX, &maps.kr, 0, tok, 0, bar, keep);
+          } else {
+            for (int b = 0; b < D / 64; ++b)
+              tma_load_3d(sb + L::V + slot * L::VUNIT + b * L::VBOX, &maps.v, b * 64,
+                          p.v_token_major ? tile.head : tok, p.v_token_major ? tok : tile.head, bar, keep);
+          }
+        }
       }
       if (!good) {
         set_status(p.status, PA_DEV_TIMEOUT);
         *flag = 1;
-        ++j;  // the stage whose keys were issued (or an older phase, complete already)
       }
       // copies in flight land before the CTA exits
-      mbar_wait_bounded_sleep(sb + L::Q_FULL, 0u, kDrainWaitNs);
-      for (int i = j < L::NK ? 0 : j - L::NK; i < j && i < n; ++i)
-        if (i < jv || !good)
-          mbar_wait_bounded_sleep(sb + L::K_FULL + 8 * (i % L::NK), (uint32_t)((i / L::NK) & 1),
-                                  kDrainWaitNs);
-      if (jv > 0) mbar_wait_bounded_sleep(sb + L::V_FULL, (uint32_t)((jv - 1) & 1), kDrainWaitNs);
+      if (keys) mbar_wait_bounded_sleep(sb + L::Q_FULL, 0u, kDrainWaitNs);
+      for (int i = j < 2 ? 0 : j - 2; i < j; ++i)
+        mbar_wait_bounded_sleep(full + 8 * (i & 1), (uint32_t)((i >> 1) & 1), kDrainWaitNs);
     }
     __syncwarp();
+    // Rows of the last stage that no row of the tile sees become zeros (the
+    // copies have landed, and no product reads them before).
+    const int valid = span - (n - 1) * kTokens;
+    if (warp == 10 && n > 0 && *flag == 0 && valid < kTokens) {
+      for (int h = 0; h < 2; ++h) {
+        const int v0 = min(64, max(0, valid - h * 64)), chunks = (64 - v0) * 8;
+        unsigned char* unit = base + L::V + (2 * (n - 1) + h) % L::NV * L::VUNIT;
+        for (int i = lane; i < chunks * (D / 64); i += 32)
+          *reinterpret_cast<uint4*>(unit + (i / chunks) * L::VBOX + v0 * 128 + (i % chunks) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();  // the tensor core reads them (async proxy)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sb + L::V_CLEAR);
+    }
   } else if (warp == 8) {
-    // ================= MMAs =================
-    if (n > 0) {
+    // ================= MMAs (one thread) =================
+    if (n > 0 && tc5::elect_one()) {
       const uint32_t idesc_s = tc5::instr_desc<T>(kRows, kTokens, false);
       const uint32_t idesc_o = tc5::instr_desc<T>(kRows, D, true);
       const uint64_t q_desc = tc5::smem_desc(sb + L::Q, 16, 1024), k_desc = tc5::smem_desc(sb + L::K, 16, 1024);
-      const uint64_t v_desc = tc5::smem_desc(sb + L::V, L::BOX, 1024);
-      auto issue_s = [&](int t, int j) {
-        if (tc5::elect_one()) {
-          tc5::fence_after();
-          const uint64_t qb = tc5::desc_at(q_desc, t * L::QTILE);
-          const uint64_t kb = tc5::desc_at(k_desc, (j % L::NK) * L::KSTAGE);
+      const uint64_t v_desc = tc5::smem_desc(sb + L::V, L::VBOX, 1024);
+      auto wait = [&](int bar, uint32_t parity) { return mbar_wait_bounded(sb + bar, parity, p.wait_ns); };
+      auto scores = [&](int t, int j) {  // S_t(j)
+        tc5::fence_after();
+        const uint64_t qb = tc5::desc_at(q_desc, t * L::QTILE);
 #pragma unroll
-          for (int k = 0; k < DK / 16; ++k)
-            tc5::mma1(tmem + t * kTokens, tc5::desc_at(qb, (k >> 2) * L::BOX + (k & 3) * 32),
-                      tc5::desc_at(kb, (k >> 2) * L::BOX + (k & 3) * 32), idesc_s, k > 0 ? 1u : 0u);
-          tc5::commit(sb + L::S_DONE + 8 * t);
+        for (int b = 0; b < L::KB; ++b) {
+          const uint64_t kb = tc5::desc_at(k_desc, (j * L::KB + b) % L::NK * L::BOX);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc5::mma1(tmem + t * kTokens, tc5::desc_at(qb, b * L::BOX + k * 32), tc5::desc_at(kb, k * 32),
+                      idesc_s, b > 0 || k > 0 ? 1u : 0u);
         }
-        __syncwarp();
-      };
-      auto wait = [&](int bar, uint32_t parity) {
-        return __all_sync(kFull, mbar_wait_bounded(sb + bar, parity, p.wait_ns)) != 0;
+        tc5::commit(sb + L::S_DONE + 8 * t);
       };
       bool good = wait(L::Q_FULL, 0u) && wait(L::K_FULL, 0u);
-      if (good) {
-        if (n0 > 0) issue_s(0, 0);
-        if (n1 > 0) issue_s(1, 0);
-        if (tc5::elect_one()) tc5::commit(sb + L::K_FREE);
-      }
+      if (good && n0 > 0) scores(0, 0);
+      if (good && n1 > 0) scores(1, 0);
       for (int j = 0; j < n && good; ++j) {
-        bool have_v = false;
-        const bool next = j + 1 < n;
-        bool have_k = false;
+        const int valid = span - j * kTokens;  // rows of the stage that some row sees
+        bool have_v = false, have_k = false;
+        // both products first: with S_0(j+1) between them each product waited for
+        // the tile's other one (prompt of 8192: 552 against 522 us)
         for (int t = 0; t < 2 && good; ++t) {
           const int nt = t ? n1 : n0;
           if (j < nt) {
-            good = wait(L::P_READY + 8 * t, (uint32_t)(j & 1));
-            if (good && !have_v) {
-              good = wait(L::V_FULL, (uint32_t)(j & 1));
-              have_v = true;
-              const int valid = span - j * kTokens;  // rows of the stage that some row sees
-              if (good && valid < kTokens) {
-                for (int i = lane; i < (kTokens - valid) * 8 * (D / 64); i += 32) {
-                  const int b = i / ((kTokens - valid) * 8), c = i % ((kTokens - valid) * 8);
-                  *reinterpret_cast<uint4*>(base + L::V + b * L::BOX + valid * 128 + c * 16) =
-                      make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();  // the tensor core reads them (async proxy)
-                __syncwarp();
-              }
+            if (!have_v)
+              good = wait(L::V_FULL + 8 * (j & 1), (uint32_t)((j >> 1) & 1)) &&
+                     (valid >= kTokens || wait(L::V_CLEAR, 0u));  // rows to clear: once they are
+            have_v = true;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // halves of 64 tokens
+              good = good && wait(L::P_READY + 16 * t + 8 * h, (uint32_t)(j & 1));
+              if (!good) break;
+              tc5::fence_after();
+              const uint64_t vb = tc5::desc_at(v_desc, (2 * j + h) % L::NV * L::VUNIT);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc5::mma1_tmem(tmem + 2 * kTokens + t * D, tmem + t * kTokens + 32 * h + 8 * k,
+                               tc5::desc_at(vb, k * 2048), idesc_o, j > 0 || h > 0 || k > 0 ? 1u : 0u);
             }
             if (!good) break;
-            if (tc5::elect_one()) {
-              tc5::fence_after();
-#pragma unroll
-              for (int k = 0; k < kTokens / 16; ++k)
-                tc5::mma1_tmem(tmem + 2 * kTokens + t * D, tmem + t * kTokens + 8 * k,
-                               tc5::desc_at(v_desc, k * 2048), idesc_o, j > 0 || k > 0 ? 1u : 0u);
-              tc5::commit(sb + L::PV_DONE + 8 * t);
-              if (t == (n1 > j ? 1 : 0)) tc5::commit(sb + L::V_FREE);
-            }
-            __syncwarp();
+            tc5::commit(sb + L::PV_DONE + 8 * t);
           }
+        }
+        for (int t = 0; t < 2 && good; ++t) {
+          const int nt = t ? n1 : n0;
           if (j + 1 < nt) {
-            if (!have_k) good = wait(L::K_FULL + 8 * ((j + 1) % L::NK), (uint32_t)(((j + 1) / L::NK) & 1));
+            if (!have_k) good = wait(L::K_FULL + 8 * ((j + 1) & 1), (uint32_t)(((j + 1) >> 1) & 1));
             have_k = true;
             // P V(j) reads P_t from the columns that S_t(j + 1) overwrites
             good = good && wait(L::PV_DONE + 8 * t, (uint32_t)(j & 1));
-            if (!good) break;
-            issue_s(t, j + 1);
+            if (good) scores(t, j + 1);
           }
         }
-        if (good && next && tc5::elect_one()) tc5::commit(sb + L::K_FREE + 8 * ((j + 1) % L::NK));
       }
-      if (!good && lane == 0) {
+      if (!good) {
         set_status(p.status, PA_DEV_TIMEOUT);
         *flag = 1;
       }
       // every MMA issued finishes before TMEM is freed
-      __syncwarp();
-      if (tc5::elect_one()) {
-        tc5::commit(sb + L::DRAIN);
-        mbar_wait_bounded_sleep(sb + L::DRAIN, 0u, kDrainWaitNs);
-      }
-      __syncwarp();
+      tc5::commit(sb + L::DRAIN);
+      mbar_wait_bounded_sleep(sb + L::DRAIN, 0u, kDrainWaitNs);
     }
+    __syncwarp();
   } else {
     // ================= softmax and output =================
     const int t = warp >> 2;
@@ -329,27 +320,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         resc = m_run != -INFINITY;
         m_run = mx;
       }
-      const float nm = m_run == -INFINITY ? -INFINITY : kBias - m_run;  // no token yet: weights 0
-      const float2 qs2 = make_float2(p.qscale, p.qscale), nm2 = make_float2(nm, nm);
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int c0 = 0; c0 < kTokens; c0 += 32) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const float2 x = ffma2(make_float2(sv[c0 + c], sv[c0 + c + 1]), qs2, nm2);
-          const float2 w = make_float2(ex2(x.x), ex2(x.y));
-          sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], w);
-          pk[c >> 1] = Elem<T>::from_f2(w.x, w.y);
-        }
-        tc5::st16u(t_s + (uint32_t)(c0 / 2), pk);
-      }
-      const float2 s2 = fadd2(sum[0], sum[1]);
-      l_run = l_run * al + (s2.x + s2.y);
       // S(j) was issued after P V(j - 1) was done, so O may be rescaled now
       if (j > 0 && __any_sync(kFull, resc)) {
         const float f = resc ? al : 1.f;
-#pragma unroll
+#pragma unroll 2
         for (int c = 0; c < D; c += 16) {
           float ov[16];
           tc5::ld16(t_o + (uint32_t)c, ov);
@@ -359,10 +333,30 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           tc5::st16(t_o + (uint32_t)c, ov);
         }
       }
-      tc5::wait_st();
-      tc5::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sb + L::P_READY + 8 * t);
+      const float nm = m_run == -INFINITY ? -INFINITY : kBias - m_run;  // no token yet: weights 0
+      const float2 qs2 = make_float2(p.qscale, p.qscale), nm2 = make_float2(nm, nm);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int c0 = 64 * h; c0 < 64 * h + 64; c0 += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float2 x = ffma2(make_float2(sv[c0 + c], sv[c0 + c + 1]), qs2, nm2);
+            const float2 w = make_float2(ex2(x.x), ex2(x.y));
+            sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], w);
+            pk[c >> 1] = Elem<T>::from_f2(w.x, w.y);
+          }
+          tc5::st16u(t_s + (uint32_t)(c0 / 2), pk);
+        }
+        tc5::wait_st();
+        tc5::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sb + L::P_READY + 16 * t + 8 * h);
+      }
+      const float2 s2 = fadd2(sum[0], sum[1]);
+      l_run = l_run * al + (s2.x + s2.y);
     }
     if (nt > 0 && good) {
       good = __all_sync(kFull, mbar_wait_bounded_sleep(sb + L::PV_DONE + 8 * t, (uint32_t)((nt - 1) & 1),
@@ -371,7 +365,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         tc5::fence_after();
         const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
         T* out = static_cast<T*>(p.out) +
-                 ((int64_t)(cq + tile.tok0 + t * kRows + row) * p.heads + tile.head) * D;
+                 ((int64_t)(tile.q0 + t * kRows + row) * p.heads + tile.head) * D;
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           float ov[32];
@@ -403,17 +397,19 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
 }
 
 // Rows [outer][inner] of `width` dense elements, as a 3-D map with boxes of
-// 64 elements by 128 tokens of one head.  token_major: tokens are the outer
-// dimension.
-bool encode_rows(CUtensorMap* map, const void* ptr, int dtype, int width, int64_t tokens,
-                 int64_t token_stride, int64_t heads, int64_t head_stride, bool token_major) {
+// 64 elements by `box_tokens` tokens of one head.  token_major: tokens are
+// the outer dimension.
+bool encode_rows(CUtensorMap* map, const void* ptr, int dtype, int box_tokens, int width,
+                 int64_t tokens, int64_t token_stride, int64_t heads, int64_t head_stride,
+                 bool token_major) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t nt = (cuuint64_t)tokens, nh = (cuuint64_t)heads;
   cuuint64_t dims[3] = {(cuuint64_t)width, token_major ? nh : nt, token_major ? nt : nh};
   cuuint64_t strides[2] = {(cuuint64_t)(token_major ? head_stride : token_stride) * 2,
                            (cuuint64_t)(token_major ? token_stride : head_stride) * 2};
-  cuuint32_t box[3] = {64, token_major ? 1u : (cuuint32_t)kTokens, token_major ? (cuuint32_t)kTokens : 1u};
+  cuuint32_t box[3] = {64, token_major ? 1u : (cuuint32_t)box_tokens,
+                       token_major ? (cuuint32_t)box_tokens : 1u};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType ty = dtype == PA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -439,12 +435,12 @@ cudaError_t launch_latent_prefill(const LatentPrefillParams& params, int head_di
   p.k_token_major = p.k_token >= p.k_head;
   p.v_token_major = p.v_token >= p.v_head;
   XMaps maps{};
-  if (!encode_rows(&maps.q, p.q, dtype, (int)dk, p.total_q, p.heads * dk, p.heads, dk, true) ||
-      !encode_rows(&maps.k, p.k, dtype, head_dim, p.total_k, p.k_token, p.heads, p.k_head,
+  if (!encode_rows(&maps.q, p.q, dtype, kRows, (int)dk, p.total_q, p.heads * dk, p.heads, dk, true) ||
+      !encode_rows(&maps.k, p.k, dtype, kTokens, head_dim, p.total_k, p.k_token, p.heads, p.k_head,
                    p.k_token_major) ||
-      !encode_rows(&maps.kr, p.k_rope, dtype, kRope, p.total_k, p.kr_token, 1,
+      !encode_rows(&maps.kr, p.k_rope, dtype, kTokens, kRope, p.total_k, p.kr_token, 1,
                    p.kr_token * p.total_k, false) ||
-      !encode_rows(&maps.v, p.v, dtype, head_dim, p.total_k, p.v_token, p.heads, p.v_head,
+      !encode_rows(&maps.v, p.v, dtype, kTokens / 2, head_dim, p.total_k, p.v_token, p.heads, p.v_head,
                    p.v_token_major))
     return cudaErrorInvalidValue;
   const bool bf = dtype == PA_DTYPE_BF16;
