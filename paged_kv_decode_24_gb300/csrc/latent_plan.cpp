@@ -8,7 +8,7 @@
 // wherever that falls, so that the CTAs end together whatever the lengths.
 // A tile that a cut falls into becomes several pieces, whose partial results
 // are merged.  A piece costs its stages and a fixed part (queries in, output
-// out), kPieceStages; a cut that would leave a piece of less than
+// out), kPieceStages16 or 128; a cut that would leave a piece of less than
 // kMinPiece stages is moved to the tile's edge.
 //
 // Expanded form.  A tile is up to kLatentRowsExpanded query tokens of one
@@ -44,7 +44,9 @@ namespace {
 
 std::atomic<uint64_t> g_latent_ids{1};
 
-constexpr int kPieceStages = 2;  // fixed cost of a piece, in stages
+// fixed cost of a piece, in stages: measured 2 to 2.8 of the 128-row kernel's
+// 2 us, about 1 of the 16-row kernel's 1.7 us
+constexpr int kPieceStages16 = 1, kPieceStages128 = 2;
 constexpr int kMinPiece = 2;     // stages of the shortest piece a cut leaves
 constexpr int kMinRange = 4;     // stages a range is worth launching a CTA for
 
@@ -65,6 +67,7 @@ struct AbsorbedTile {
 void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_t* qs,
                    const std::vector<int32_t>& cu_q, int rows, int workers, int forced, Work* w) {
   const int64_t stage = rows == kLatentRowsPair ? kLatentStagePair : kLatentStage;
+  const int64_t piece_cost = rows == kLatentRowsPair ? kPieceStages128 : kPieceStages16;
   auto stages_of = [&](int64_t tokens) { return (tokens + stage - 1) / stage; };
   std::vector<AbsorbedTile> tiles;
   int64_t total = 0;
@@ -75,18 +78,18 @@ void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_
       const int32_t last = (int32_t)((r + n - 1) / s.num_heads);  // query token of its last row
       const int32_t span = lens[b] - qs[b] + last + 1;
       tiles.push_back({b, (int32_t)r, n, span});
-      total += stages_of(span) + kPieceStages;
+      total += stages_of(span) + piece_cost;
     }
   }
   if (tiles.empty()) {
     w->ranges.push_back(0);
     return;
   }
-  const int64_t by_work = std::max<int64_t>(1, total / (kMinRange + kPieceStages));
+  const int64_t by_work = std::max<int64_t>(1, total / (kMinRange + piece_cost));
   const int64_t ranges = std::min<int64_t>(workers, by_work);
   // each range gets an equal share of what is left when it is opened, where
   // every range but the last is expected to end in a cut, a piece more
-  auto share = [&](int64_t open) { return (total + kPieceStages * (open - 1) + open - 1) / open; };
+  auto share = [&](int64_t open) { return (total + piece_cost * (open - 1) + open - 1) / open; };
   int64_t quota = share(ranges);
   int64_t left = quota;  // of the range that is being filled
   w->ranges.push_back(0);
@@ -107,12 +110,12 @@ void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_
         ++piece;
         take = n * piece / parts - at;
         close();
-      } else if (take + kPieceStages > left) {
-        if (left < kMinPiece + kPieceStages && left < quota) {  // nothing worth starting
+      } else if (take + piece_cost > left) {
+        if (left < kMinPiece + piece_cost && left < quota) {  // nothing worth starting
           close();
           continue;
         }
-        take = std::min<int64_t>(take, std::max<int64_t>(left - kPieceStages, kMinPiece));
+        take = std::min<int64_t>(take, std::max<int64_t>(left - piece_cost, kMinPiece));
         if (n - at - take < kMinPiece) take = n - at;
       }
       const int32_t tok1 = (int32_t)std::min<int64_t>((at + take) * stage, t.span);
@@ -120,8 +123,8 @@ void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_
                              (int32_t)((int64_t)cu_q[(size_t)t.b] * s.num_heads + t.row0),
                              lens[t.b] - qs[t.b]});
       at += take;
-      left -= take + kPieceStages;
-      total -= take + (at == n ? kPieceStages : 0);
+      left -= take + piece_cost;
+      total -= take + (at == n ? piece_cost : 0);
       if (forced == 0 && left <= 0) close();
     }
     const size_t pieces = w->segments.size() - first;
