@@ -547,9 +547,11 @@ pa_status_t pa_prefill_attention(const pa_shape_t* shape, const pa_prefill_plan_
  *   block_table [batch][max_pages_per_seq], int32, dense
  *   packed rows T = sum of q_lens, Tk = sum of seq_lens, in sequence order
  * The lengths are those of the plan, which every call reads from the
- * workspace the plan was uploaded to.  The calls on one plan and workspace
- * may share it in stream order; absorbed calls in flight at once each need
- * their own (their split partials live there).
+ * workspace the plan was uploaded to.  A call may read it while the kernel
+ * ahead in the stream still runs, so nothing but pa_latent_plan_upload may
+ * write that part of the workspace.  Calls on one plan and workspace may
+ * share it in stream order; absorbed calls in flight at once each need their
+ * own (their split partials live there).
  */
 typedef struct {
   int32_t batch;             /* B, >= 0 */
@@ -637,7 +639,9 @@ pa_status_t pa_latent_gather(const pa_latent_shape_t* shape, const pa_latent_pla
 /* Absorbed attention.  q: [T][H][576] dense; out: [T][H][512] dense.  fp32
  * accumulation and softmax.  Tokens of a page whose index is out of range
  * are left out and set PA_DEV_BAD_PAGE; a row left without any token gets
- * zeros.  Long sequences are cut into pieces over their tokens, whose
+ * zeros.  The cached rows of a sequence's own tokens have to be finite (a
+ * query's weight of a later token is 0, but its product may be formed); what
+ * no sequence owns may hold anything.  Long sequences are cut into pieces over their tokens, whose
  * partial results a second kernel merges (one launch when nothing was cut).
  * The same bits on every call.  The plan's form must be PA_LATENT_ABSORBED. */
 pa_status_t pa_latent_attention(const pa_latent_shape_t* shape, const pa_latent_plan_t* plan,
@@ -650,8 +654,12 @@ pa_status_t pa_latent_attention(const pa_latent_shape_t* shape, const pa_latent_
  * with its token and head stride in elements (k and v may be halves of one
  * projection's output); k_rope: Tk rows of 64 values, kr_stride elements
  * apart (the tail of pa_latent_gather's rows, kr_stride = 576).  Values
- * dense within a head; pointers 16-byte aligned, strides positive multiples of 8
- * elements.  The plan's form must be PA_LATENT_EXPANDED. */
+ * dense within a head; pointers 16-byte aligned; strides multiples of 8
+ * elements that keep tokens and heads apart (either may be the outer one).
+ * Weights of later tokens are 0, but their values are read up to the next
+ * multiple of 128 tokens that some query sees: values of a sequence's own
+ * tokens have to be finite.  Rows of other sequences may hold anything.
+ * The plan's form must be PA_LATENT_EXPANDED. */
 pa_status_t pa_latent_prefill(const pa_latent_shape_t* shape, const pa_latent_plan_t* plan,
                               const void* q, const void* k, int64_t k_token_stride,
                               int64_t k_head_stride, const void* k_rope, int64_t kr_stride,

@@ -710,9 +710,11 @@ def _latent_rows(t, dtype, size, name):
     if t.numel() and t.stride(-1) != 1:
         raise ValueError(f"{name} must be dense in its last dimension")
     _on_current_device(t, name)
-    # a dimension of one entry has no stride of its own: any valid one will do
-    strides = [t.stride(i) if t.shape[i] > 1 else -(-max(t.stride(i), size[-1]) // 8) * 8
-               for i in range(t.dim() - 1)]
+    # a dimension of one entry has no stride of its own: the dense one will do
+    strides, dense = [], size[-1]
+    for i in reversed(range(t.dim() - 1)):
+        strides.insert(0, t.stride(i) if t.shape[i] > 1 else dense)
+        dense *= max(1, t.shape[i])
     return ctypes.c_void_p(t.data_ptr()), strides
 
 

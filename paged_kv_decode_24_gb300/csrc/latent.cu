@@ -28,48 +28,74 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int batch, int r, 
   return lo;
 }
 
-// One warp per row: a row is 72 chunks of 16 bytes, two or three per lane.
-// Both directions only move bytes, so they run at the copy bandwidth once
-// enough rows are in flight.
+// Two consecutive packed rows per warp and turn: 144 chunks of 16 bytes, up to
+// five a lane, in flight at once behind one look-up of the rows' places (lane
+// u looks up row u).  Both directions only move bytes.  Measured against the
+// copy bandwidth: contexts of 292 MB read back at 93 %, prompts of 125 MB
+// written at 85 % (one row per warp 83 and 85 %, four 89 and 67 %: the lanes'
+// registers then leave too few warps), with up to 16 blocks an SM (8: 90 and
+// 83 %).
+constexpr int kWarpRows = 2;
+constexpr int kRowBlocks = 152 * 16;
+
 template <bool APPEND>
 __global__ void __launch_bounds__(256) latent_rows_kernel(const LatentRowsParams p) {
+  constexpr int CHUNKS = (kWarpRows * kRowChunks + 31) / 32;  // of a lane
   pdl_launch_dependents();
-  pdl_wait_primary();
   const int lane = threadIdx.x & 31;
-  const int32_t* cu = p.ws + 16 + (APPEND ? 0 : p.batch + 1);
   const int32_t* cu_q = p.ws + 16;
   const int32_t* cu_k = cu_q + p.batch + 1;
-  if (p.ws[0] != (int)kLatentMagic || p.ws[1] != p.batch || p.ws[APPEND ? 2 : 3] != p.total) {
+  const int32_t* cu = APPEND ? cu_q : cu_k;
+  // the plan is written by the upload alone: it may be read before the wait
+  const bool planned = p.ws[0] == (int)kLatentMagic && p.ws[1] == p.batch && p.ws[APPEND ? 2 : 3] == p.total;
+  const int64_t turns = ((int64_t)p.total + kWarpRows - 1) / kWarpRows;
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
+  int64_t turn = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  pdl_wait_primary();
+  if (!planned) {
     if (threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
     return;
   }
-  const int warps = (int)(gridDim.x * (blockDim.x >> 5));
-  for (int64_t r64 = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r64 < p.total;
-       r64 += warps) {
-    const int r = (int)r64;
-    const int b = sequence_of(cu, p.batch, r, lane);
-    int t = r - cu[b];
-    if (APPEND) t += cu_k[b + 1] - cu_k[b] - (cu_q[b + 1] - cu_q[b]);
-    const int j = t / p.page_size;
-    const int page = j < p.max_pages ? p.block_table[(int64_t)b * p.max_pages + j] : -1;
-    const bool bad = page < 0 || page >= p.num_pages;
-    if (bad && lane == 0) set_status(p.status, PA_DEV_BAD_PAGE);
-    uint4* cached = static_cast<uint4*>(p.pages) +
-                    ((int64_t)(bad ? 0 : page) * p.page_size + t % p.page_size) * kRowChunks;
-    if (APPEND) {
-      if (bad) continue;
-      const uint4* c = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.c) + r * p.c_stride);
-      const uint4* rr = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.r) + r * p.r_stride);
-      const uint4 v0 = c[lane], v1 = c[lane + 32];
-      if (lane < kRowChunks - kCChunks) cached[kCChunks + lane] = rr[lane];
-      cached[lane] = v0;
-      cached[lane + 32] = v1;
-    } else {
-      uint4* row = static_cast<uint4*>(p.rows) + (int64_t)r * kRowChunks;
+  for (; turn < turns; turn += step) {
+    const int r0 = (int)(turn * kWarpRows);
+    int b = sequence_of(cu, p.batch, r0, lane);
+    // lane u: where row r0 + u is cached, -1 for a bad page or past the end
+    int64_t at = -1;
+    if (lane < kWarpRows && r0 + lane < p.total) {
+      const int r = r0 + lane;
+      while (r >= cu[b + 1]) ++b;
+      int t = r - cu[b];
+      if (APPEND) t += cu_k[b + 1] - cu_k[b] - (cu_q[b + 1] - cu_q[b]);
+      const int j = t / p.page_size;
+      const int page = j < p.max_pages ? p.block_table[(int64_t)b * p.max_pages + j] : -1;
+      if (page >= 0 && page < p.num_pages)
+        at = ((int64_t)page * p.page_size + t % p.page_size) * kRowChunks;
+      else
+        set_status(p.status, PA_DEV_BAD_PAGE);
+    }
+    uint4 v[CHUNKS];
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const int ch = lane + 32 * i;
-        if (ch < kRowChunks) row[ch] = bad ? make_uint4(0u, 0u, 0u, 0u) : cached[ch];
+    for (int i = 0; i < CHUNKS; ++i) {
+      const int c = lane + 32 * i, u = c / kRowChunks, ch = c % kRowChunks;
+      const int64_t cached = __shfl_sync(kFull, at, u);
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (cached < 0 || u >= kWarpRows) continue;
+      if (!APPEND)
+        v[i] = static_cast<const uint4*>(p.pages)[cached + ch];
+      else if (ch < kCChunks)
+        v[i] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.c) + (r0 + u) * p.c_stride)[ch];
+      else
+        v[i] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.r) + (r0 + u) * p.r_stride)[ch - kCChunks];
+    }
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) {
+      const int c = lane + 32 * i, u = c / kRowChunks, ch = c % kRowChunks;
+      const int64_t cached = __shfl_sync(kFull, at, u);
+      if (u >= kWarpRows) continue;
+      if (APPEND) {
+        if (cached >= 0) static_cast<uint4*>(p.pages)[cached + ch] = v[i];
+      } else if (r0 + u < p.total) {
+        static_cast<uint4*>(p.rows)[(int64_t)(r0 + u) * kRowChunks + ch] = v[i];
       }
     }
   }
@@ -78,8 +104,8 @@ __global__ void __launch_bounds__(256) latent_rows_kernel(const LatentRowsParams
 template <bool APPEND>
 cudaError_t launch_rows(const LatentRowsParams& p, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
-  const int64_t blocks = ((int64_t)p.total + 7) / 8;
-  const int grid = (int)(blocks < 152 * 8 ? blocks : 152 * 8);
+  const int64_t blocks = ((int64_t)p.total + 8 * kWarpRows - 1) / (8 * kWarpRows);
+  const int grid = (int)(blocks < kRowBlocks ? blocks : kRowBlocks);
   return launch_pdl(latent_rows_kernel<APPEND>, 0, configured, p, grid, 256, stream);
 }
 
@@ -133,8 +159,21 @@ pa_status_t check_latent_call(const pa_latent_shape_t* s, const pa_latent_plan_t
   return PA_OK;
 }
 
+// Strides in elements: multiples of 16 bytes below 2^40 bytes.
 bool stride_ok(int64_t stride, int width) {
-  return stride >= width && stride % 8 == 0 && stride < (int64_t)1 << 38;
+  return stride >= width && stride % 8 == 0 && stride < (int64_t)1 << 39;
+}
+
+// Tokens and heads of D values whose strides keep them apart, tokens outside
+// heads or heads outside tokens.
+bool planes_ok(int64_t token, int64_t head, int64_t tokens, int64_t heads, int d) {
+  if (!stride_ok(token, 8) || !stride_ok(head, 8)) return false;
+  const bool token_major = token >= head;
+  const int64_t inner = token_major ? head : token, outer = token_major ? token : head;
+  const int64_t n_inner = token_major ? heads : tokens, n_outer = token_major ? tokens : heads;
+  // inner < 2^39 and n_inner < 2^31: compared by division
+  if (n_inner > 1 && inner < d) return false;
+  return n_outer <= 1 || (outer >= d && (n_inner <= 1 || (outer - d) / inner >= n_inner - 1));
 }
 
 LatentRowsParams rows_params(const pa_latent_shape_t* s, const int32_t* block_table,
@@ -273,8 +312,9 @@ extern "C" pa_status_t pa_latent_prefill(const pa_latent_shape_t* shape,
       !aligned(out, 16) || !aligned(dev_status, 4))
     return PA_ERR_INVALID_ARG;
   if (!isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
-  if (!stride_ok(k_token_stride, 8) || !stride_ok(k_head_stride, 8) ||
-      !stride_ok(kr_stride, 8) || !stride_ok(v_token_stride, 8) || !stride_ok(v_head_stride, 8))
+  if (!planes_ok(k_token_stride, k_head_stride, plan->total_k, shape->num_heads, shape->head_dim) ||
+      !planes_ok(v_token_stride, v_head_stride, plan->total_k, shape->num_heads, shape->head_dim) ||
+      !stride_ok(kr_stride, kRope))
     return PA_ERR_INVALID_ARG;
   LatentPrefillParams p{};
   const LatentLayout l = latent_layout(shape->batch, plan->form, plan->rows_per_tile,

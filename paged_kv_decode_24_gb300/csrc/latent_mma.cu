@@ -87,7 +87,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   const bool planned = latent_range(p, kLatentRowsMma, (int)blockIdx.x, first, last);
   if (threadIdx.x == 0) {
     *flag = 0;
-    if (!planned) set_status(p.status, PA_DEV_PLAN_MISMATCH);
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.pages_map)) : "memory");
     for (int s = 0; s < L::SLOTS; ++s) {
       mbar_init(sbase + L::FULL + 8 * s, 1);
@@ -100,6 +99,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   __syncthreads();
   pdl_launch_dependents();
   pdl_wait_primary();
+  if (!planned && threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
 
   if (warp == kWorkWarps) {
     // ================= copies =================

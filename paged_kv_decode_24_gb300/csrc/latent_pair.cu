@@ -175,7 +175,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const bool planned = latent_range(p, kLatentRowsPair, (int)(blockIdx.x >> 1), first, last);
 
   if (threadIdx.x == 0) {
-    if (!planned) set_status(p.status, PA_DEV_PLAN_MISMATCH);
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.pages_map)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&q_map)) : "memory");
     for (int b = L::Q_FREE; b < L::V_CLEAR; b += 8) mbar_init(sb + b, 1);
@@ -199,6 +198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t t_o = tmem, t_s = tmem + 256;  // O 256 columns, S two buffers of 64
   pdl_launch_dependents();
   pdl_wait_primary();
+  if (!planned && threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
 
   auto usable = [&](const LatentSegment& s) {  // the same answer in every warp of both CTAs
     return latent_segment_ok(p, s, kLatentRowsPair);

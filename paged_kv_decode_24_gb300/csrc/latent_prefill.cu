@@ -120,8 +120,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   const int n0 = bad ? 0 : (pos0 + min(tile.ntok, kRows) + kTokens - 1) / kTokens;
   const int n1 = bad || tile.ntok <= kRows ? 0 : (span + kTokens - 1) / kTokens;
   const int n = max(n0, n1);
-  if (bad && threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
-
   if (threadIdx.x == 0) {
     *flag = 0;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.q)) : "memory");
@@ -145,6 +143,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + L::TMEM_SLOT);
   pdl_launch_dependents();
   pdl_wait_primary();
+  if (bad && threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
 
   if (warp == 9 || warp == 10) {
     // ================= copies =================

@@ -1,0 +1,315 @@
+"""Host-side checks of the latent attention calls that need no GPU: the
+planner's work lists, the oracle against its own definition, and every refusal
+(each before any CUDA call)."""
+
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+import pytest
+
+import oracle
+from paged_kv_decode_24_gb300 import binding
+
+PTR = ctypes.c_void_p(0x10000)   # 16-byte aligned, never touched
+ODD = ctypes.c_void_p(0x10008)
+
+
+def shape(batch=3, heads=16, head_dim=128, page=16, max_pages=64, num_pages=100, dtype="bf16"):
+    return binding.make_latent_shape(batch, heads, head_dim, page, max_pages, num_pages, dtype)
+
+
+def parts(plan):
+    """header, cu_q, cu_k, ranges, segments, merges (absorbed) or tiles (expanded)."""
+    b = plan.blob()
+    B, form, rows, nr, ns, nm = b[1], b[6], b[7], b[8], b[9], b[10]
+    at = 16
+    cu_q, cu_k = b[at:at + B + 1], b[at + B + 1:at + 2 * (B + 1)]
+    at = (at + 2 * (B + 1) + 3) // 4 * 4
+    if form == 1:
+        return b[:16], cu_q, cu_k, b[at:at + 8 * nr].reshape(nr, 8)
+    ranges = b[at:at + nr + 1]
+    at = (at + nr + 1 + 3) // 4 * 4
+    segments = b[at:at + 8 * ns].reshape(ns, 8)
+    merges = b[at + 8 * ns:at + 8 * ns + 4 * nm].reshape(nm, 4)
+    return b[:16], cu_q, cu_k, ranges, segments, merges
+
+
+BATCHES = [
+    ([1], [1], 1), ([5, 0, 77], [1, 0, 1], 16), ([1000, 33, 2000], [1, 1, 1], 16),
+    ([100, 64, 500], [5, 3, 7], 3), ([40000, 10, 3], [1, 1, 1], 128), ([300] * 40, [1] * 40, 128),
+    ([64, 65, 63, 128, 129], [64, 1, 2, 128, 5], 20), ([2000] * 200, [1] * 200, 16),
+    ([0, 0], [0, 0], 4),
+]
+
+
+@pytest.mark.parametrize("rows", [0, 16, 128])
+@pytest.mark.parametrize("splits", [0, 1, 3])
+@pytest.mark.parametrize("case", BATCHES, ids=lambda c: f"B{len(c[0])}_H{c[2]}_L{max(c[0])}")
+def test_absorbed_plan_covers_every_row_and_token_once(lib, case, splits, rows):
+    lens, qs, heads = case
+    s = shape(len(lens), heads, max_pages=3000)
+    p = binding.LatentPlan(s, lens, qs, 152, rows_per_tile=rows, forced_splits=splits)
+    head, cu_q, cu_k, ranges, seg, merges = parts(p)
+    most = max(q * heads for q in qs)
+    R = head[7]
+    assert R == (rows or (16 if most <= 16 else 128)) == p.c.rows_per_tile
+    assert list(cu_q) == [0, *np.cumsum(qs)] and list(cu_k) == [0, *np.cumsum(lens)]
+    stage = 128 if R == 128 else 64
+    # ranges split the list of pieces, none is empty
+    assert ranges[0] == 0 and ranges[-1] == len(seg) and np.all(np.diff(ranges) > 0)
+    workers = 76 if R == 128 else 152
+    if splits == 0:
+        assert len(ranges) - 1 <= workers
+    tiles = {}
+    for b, row0, nrows, t0, t1, slot, packed0, pos0 in seg.tolist():
+        assert 1 <= nrows <= R and row0 % R == 0
+        assert packed0 == cu_q[b] * heads + row0 and pos0 == lens[b] - qs[b]
+        assert t0 % stage == 0 and t0 < t1
+        tiles.setdefault((b, row0), []).append((t0, t1, slot, nrows))
+    want = {(b, r) for b in range(len(lens)) for r in range(0, qs[b] * heads, R)}
+    assert set(tiles) == want
+    slots, cut = [], []
+    for (b, row0), pieces in tiles.items():
+        n = pieces[0][3]
+        assert n == min(R, qs[b] * heads - row0) and all(x[3] == n for x in pieces)
+        span = lens[b] - qs[b] + (row0 + n - 1) // heads + 1     # tokens its last row sees
+        assert [x[0] for x in pieces] == [0, *[x[1] for x in pieces[:-1]]] and pieces[-1][1] == span
+        if len(pieces) == 1:
+            assert pieces[0][2] == -1
+        else:
+            ids = [x[2] for x in pieces]
+            assert ids == list(range(ids[0], ids[0] + len(ids)))
+            slots += ids
+            cut.append((ids[0], len(ids), cu_q[b] * heads + row0, n))
+        if splits:
+            assert len(pieces) == min(splits, -(-span // stage))
+    assert sorted(slots) == list(range(head[11])) and sorted(cut) == sorted(map(tuple, merges.tolist()))
+
+
+def test_absorbed_ranges_have_equal_work(lib):
+    """No range has more than a stage, a piece's fixed cost and the shortest
+    piece above the mean, whatever the lengths."""
+    rng = np.random.default_rng(5)
+    for heads, unit, fixed in ((16, 64, 1), (128, 128, 2)):
+        lens = rng.integers(3000, 9000, 64).tolist()
+        s = shape(64, heads, max_pages=1000)
+        _, _, _, ranges, seg, _ = parts(binding.LatentPlan(s, lens, [1] * 64, 152))
+        cost = -(-(seg[:, 4] - seg[:, 3]) // unit) + fixed
+        per = np.add.reduceat(cost, ranges[:-1])
+        assert per.max() <= per.mean() + 2 + fixed + 2, (heads, per.max(), per.mean())
+
+
+@pytest.mark.parametrize("case", BATCHES, ids=lambda c: f"B{len(c[0])}_H{c[2]}_L{max(c[0])}")
+def test_expanded_plan_covers_every_token_and_head_once(lib, case):
+    lens, qs, heads = case
+    p = binding.LatentPlan(shape(len(lens), heads, max_pages=3000), lens, qs, 152, form="expanded")
+    head, cu_q, cu_k, tiles = parts(p)
+    assert p.c.num_ranges == len(tiles) and p.c.workspace_bytes >= p.c.blob_bytes
+    seen = set()
+    for h, n, q0, pos0, k0 in tiles[:, :5].tolist():
+        b = int(np.searchsorted(cu_q, q0, side="right")) - 1
+        while qs[b] == 0:
+            b -= 1
+        assert 1 <= n <= 256 and k0 == cu_k[b] and pos0 == lens[b] - qs[b] + q0 - cu_q[b]
+        assert q0 + n <= cu_q[b + 1]
+        seen |= {(q0 + i, h) for i in range(n)}
+    assert len(seen) == sum(qs) * heads == int(tiles[:, 1].sum())
+    stages = -(-(tiles[:, 3] + tiles[:, 1]) // 128)
+    assert np.all(np.diff(stages) <= 0)          # the longest first
+
+
+def plan_code(s, lens, qs, sms=152, form=0, **opts):
+    o = binding.PaLatentOptions(opts.get("rows", 0), opts.get("splits", 0), 0)
+    out = binding.PaLatentPlan()
+    a, b = np.asarray(lens, np.int32), np.asarray(qs, np.int32)
+    code = binding.load().pa_latent_plan(ctypes.byref(s), a.ctypes.data if a.size else None,
+                                         b.ctypes.data if b.size else None, sms, form,
+                                         ctypes.byref(o), ctypes.byref(out))
+    if code == 0:
+        binding.load().pa_latent_plan_free(ctypes.byref(out))
+    return code
+
+
+INVALID, UNSUPPORTED, WORKSPACE, PLAN = 1, 2, 3, 8
+
+
+def test_plan_refusals(lib):
+    good = shape(2)
+    assert plan_code(good, [5, 3], [1, 3]) == 0
+    for lens, qs in (([5, -1], [1, 0]), ([5, 3], [1, 4]), ([5, 3], [-1, 0]), ([64 * 16 + 1, 3], [1, 1])):
+        assert plan_code(good, lens, qs) == INVALID
+    assert plan_code(good, [5, 3], [1, 1], sms=0) == INVALID
+    assert plan_code(good, [5, 3], [1, 1], form=2) == INVALID
+    assert plan_code(good, [5, 3], [1, 1], rows=64) == INVALID
+    assert plan_code(good, [5, 3], [1, 1], splits=-1) == INVALID
+    assert plan_code(good, [5, 3], [1, 1], form=1, rows=128) == INVALID
+    assert plan_code(good, [5, 3], [1, 1], form=1, splits=2) == INVALID
+    for k, v, want in (("num_heads", 129, UNSUPPORTED), ("num_heads", 0, INVALID),
+                       ("head_dim", 96, UNSUPPORTED), ("latent_dim", 256, UNSUPPORTED),
+                       ("rope_dim", 32, UNSUPPORTED), ("page_size", 8, UNSUPPORTED),
+                       ("page_size", 48, UNSUPPORTED), ("page_size", 0, INVALID),
+                       ("dtype", 2, UNSUPPORTED), ("batch", -1, INVALID), ("num_pages", 0, INVALID),
+                       ("max_pages_per_seq", 0, INVALID), ("max_pages_per_seq", 2**30, INVALID)):
+        s = shape(2)
+        setattr(s, k, v)
+        assert plan_code(s, [5, 3], [1, 1]) == want, (k, v)
+    big = shape(1, max_pages=2**27 - 1)       # packed rows times heads past 32 bits
+    assert plan_code(big, [2**31 - 32], [2**31 - 32]) == INVALID
+    assert lib.pa_latent_plan(ctypes.byref(good), None, None, 152, 0, None,
+                              ctypes.byref(binding.PaLatentPlan())) == INVALID
+    lib.pa_latent_plan_free(None)
+
+
+class Call:
+    """The four device calls with fake pointers: every refusal comes before a
+    CUDA call, so these run without a GPU."""
+
+    def __init__(self, lib, form="absorbed", **sh):
+        self.lib, self.s = lib, shape(2, **sh)
+        self.p = binding.LatentPlan(self.s, [500, 3], [1, 3], 152, form=form)
+
+    def args(self, **kw):
+        return kw.get("s", self.s), kw.get("plan", self.p.c), kw.get("n", self.p.workspace_bytes)
+
+    def append(self, **kw):
+        s, plan, n = self.args(**kw)
+        return self.lib.pa_latent_append(
+            ctypes.byref(s), ctypes.byref(plan), kw.get("c", PTR), kw.get("cs", 512),
+            kw.get("r", PTR), kw.get("rs", 64), kw.get("pages", PTR), kw.get("table", PTR),
+            kw.get("ws", PTR), n, kw.get("status", PTR), None)
+
+    def gather(self, **kw):
+        s, plan, n = self.args(**kw)
+        return self.lib.pa_latent_gather(
+            ctypes.byref(s), ctypes.byref(plan), kw.get("pages", PTR), kw.get("table", PTR),
+            kw.get("rows", PTR), kw.get("ws", PTR), n, kw.get("status", PTR), None)
+
+    def attention(self, **kw):
+        s, plan, n = self.args(**kw)
+        return self.lib.pa_latent_attention(
+            ctypes.byref(s), ctypes.byref(plan), kw.get("q", PTR), kw.get("pages", PTR),
+            kw.get("table", PTR), ctypes.c_float(kw.get("scale", 0.1)), kw.get("out", PTR),
+            kw.get("ws", PTR), n, kw.get("status", PTR), None)
+
+    def prefill(self, **kw):
+        s, plan, n = self.args(**kw)
+        return self.lib.pa_latent_prefill(
+            ctypes.byref(s), ctypes.byref(plan), kw.get("q", PTR), kw.get("k", PTR),
+            kw.get("kt", 2048), kw.get("kh", 128), kw.get("kr", PTR), kw.get("krs", 576),
+            kw.get("v", PTR), kw.get("vt", 2048), kw.get("vh", 128),
+            ctypes.c_float(kw.get("scale", 0.1)), kw.get("out", PTR), kw.get("ws", PTR), n,
+            kw.get("status", PTR), None)
+
+
+NAMES = {"append": ["c", "r", "pages"], "gather": ["pages", "rows"],
+         "attention": ["q", "pages", "out"], "prefill": ["q", "k", "kr", "v", "out"]}
+
+
+@pytest.mark.parametrize("op", list(NAMES))
+def test_call_refusals(lib, op):
+    c = Call(lib, "expanded" if op == "prefill" else "absorbed")
+    call = getattr(c, op)
+    for name in NAMES[op] + ["ws"]:
+        assert call(**{name: None}) == INVALID and call(**{name: ODD}) == INVALID, name
+    for name in ["status"] + (["table"] if op != "prefill" else []):
+        assert call(**{name: None}) == INVALID
+        assert call(**{name: ctypes.c_void_p(0x10002)}) == INVALID
+    assert call(n=c.p.workspace_bytes - 1) == WORKSPACE
+    for k, v in (("batch", 3), ("num_heads", 8), ("head_dim", 64), ("page_size", 32),
+                 ("max_pages_per_seq", 65)):
+        s = shape(2)
+        setattr(s, k, v)
+        assert call(s=s) == PLAN, k
+    s = shape(2)
+    s.num_heads = 200
+    assert call(s=s) == UNSUPPORTED
+    for k, v in (("num_segments", 7), ("num_slots", -1), ("rows_per_tile", 32), ("form", 9),
+                 ("workspace_bytes", 0)):
+        plan = binding.PaLatentPlan.from_buffer_copy(c.p.c)
+        setattr(plan, k, v)
+        if op == "prefill" and k == "num_segments":
+            continue    # the expanded plan has none: the field is not read
+        assert call(plan=plan) == PLAN, k
+
+
+def test_scale_stride_and_form_refusals(lib):
+    a, e = Call(lib), Call(lib, "expanded")
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert a.attention(scale=scale) == INVALID and e.prefill(scale=scale) == INVALID
+    assert a.attention(plan=e.p.c, n=10**6) == PLAN and e.prefill(plan=a.p.c, n=10**6) == PLAN
+    for kw in ({"cs": 511}, {"cs": 504}, {"cs": 516}, {"rs": 63}, {"rs": 0}, {"cs": -512}):
+        assert a.append(**kw) == INVALID, kw
+    for kw in ({"kt": 0}, {"kh": 0}, {"vt": 7}, {"vh": 4}, {"krs": -64}, {"krs": 56},
+               {"kt": 1 << 40}, {"kt": 128, "kh": 128}, {"kh": 120}, {"vt": 2040}):
+        assert e.prefill(**kw) == INVALID, kw
+
+
+def test_empty_batches_launch_nothing(lib):
+    s = shape(0)
+    for form in ("absorbed", "expanded"):
+        p = binding.LatentPlan(s, [], [], 152, form=form)
+        none = ctypes.c_void_p(None)
+        f = ctypes.c_float(1.0)
+        if form == "absorbed":
+            assert lib.pa_latent_append(ctypes.byref(s), ctypes.byref(p.c), none, 512, none, 64, none,
+                                        none, none, 0, none, None) == 0
+            assert lib.pa_latent_gather(ctypes.byref(s), ctypes.byref(p.c), none, none, none, none, 0,
+                                        none, None) == 0
+            assert lib.pa_latent_attention(ctypes.byref(s), ctypes.byref(p.c), none, none, none, f,
+                                           none, none, 0, none, None) == 0
+        else:
+            assert lib.pa_latent_prefill(ctypes.byref(s), ctypes.byref(p.c), none, none, 8, 8, none,
+                                         64, none, 8, 8, f, none, none, 0, none, None) == 0
+
+
+def test_binding_checks_sizes_before_the_call(lib):
+    torch = pytest.importorskip("torch")
+    s = shape(2)
+    p = binding.LatentPlan(s, [5, 3], [1, 3], 152)
+    cpu = torch.zeros(4, 512, dtype=torch.bfloat16)
+    with pytest.raises((TypeError, ValueError)):
+        binding._latent_rows(cpu, torch.bfloat16, (4, 512), "c_new")
+    with pytest.raises(ValueError):
+        binding.LatentPlan(s, [5, 3, 2], [1, 3], 152)
+    with pytest.raises(KeyError):
+        binding.LatentPlan(s, [5, 3], [1, 3], 152, form="other")
+    with pytest.raises(binding.PagedAttnError):
+        binding.LatentPlan(s, [5, 3], [1, 4], 152)
+    del p
+
+
+# ---- the oracle
+
+def test_oracle_forms_agree_in_64_bits():
+    """Absorbed and expanded attention of the same cache and maps are equal."""
+    rng = np.random.default_rng(0)
+    lens, qs, H, D, S = [21, 40], [21, 3], 3, 64, 16
+    table = np.array([[4, 1, 0], [2, 5, 3]])
+    pages = rng.standard_normal((6, S, 576))
+    W, U = rng.standard_normal((2, H, D, 512)) * 0.05
+    q = rng.standard_normal((24, H, D + 64))
+    rows = oracle.latent_gather(pages, table, lens)
+    k = np.einsum("tc,hdc->thd", rows[:, :512], W)
+    v = np.einsum("tc,hdc->thd", rows[:, :512], U)
+    x = oracle.latent_prefill(q, k, rows[:, 512:], v, lens, qs, 0.09)[0]
+    qa = np.concatenate([np.einsum("thd,hdc->thc", q[..., :D], W), q[..., D:]], 2)
+    y = oracle.latent_attention(qa, pages, table, lens, qs, 0.09)[0]
+    assert np.abs(x - np.einsum("thc,hdc->thd", y, U)).max() < 1e-12
+
+
+def test_oracle_closed_forms():
+    """One visible token: its own latent; equal scores: the mean; a sequence
+    whose pages are all bad: zeros."""
+    rng = np.random.default_rng(1)
+    pages = rng.standard_normal((3, 16, 576))
+    table = np.array([[1, 2]])
+    q = rng.standard_normal((1, 2, 576))
+    out = oracle.latent_attention(q, pages, table, [1], [1], 1.0)[0]
+    assert np.allclose(out, pages[1, 0, :512][None, None], atol=0)
+    out = oracle.latent_attention(q * 0, pages, table, [20], [1], 1.0)[0]
+    mean = np.concatenate([pages[1], pages[2, :4]])[:, :512].mean(0)
+    assert np.allclose(out[0], mean[None], atol=1e-14)
+    out = oracle.latent_attention(q, pages, table, [20], [1], 1.0, bad_pages=[(0, 0), (0, 1)])[0]
+    assert np.all(out == 0)
