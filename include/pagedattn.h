@@ -592,7 +592,7 @@ typedef struct {
 
 /* Options of a latent plan; a zeroed struct or NULL gives the defaults. */
 typedef struct {
-  int32_t rows_per_tile;    /* absorbed: 16 or 128 (0: the planner's choice by the rows of a
+  int32_t rows_per_tile;    /* absorbed: 16, 64 or 128 (0: the planner's choice by the rows of a
                                sequence); expanded: 0 */
   int32_t forced_splits;    /* absorbed: cut every tile's tokens into this many pieces, as far
                                as it has stages of 64 tokens (0: the planner's choice) */

@@ -27,7 +27,7 @@ SOURCES = ["api.cu", "plan.cpp", "aux_kernels.cu", "decode_d64.cu", "decode_d128
            "decode_f8_d64.cu", "decode_f8_d128.cu",
            "static_workspace.cu", "blocks.cpp", "prefill_plan.cpp", "prefill_d64.cu",
            "prefill_d128.cu", "prefill_tc5_d64.cu", "prefill_tc5_d128.cu",
-           "latent.cu", "latent_plan.cpp", "latent_mma.cu", "latent_pair.cu",
+           "latent.cu", "latent_plan.cpp", "latent_mma.cu", "latent_solo.cu", "latent_pair.cu",
            "latent_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

@@ -144,7 +144,7 @@ pa_status_t check_latent_call(const pa_latent_shape_t* s, const pa_latent_plan_t
       (form >= 0 && plan->form != form))
     return PA_ERR_PLAN;
   const int rows = plan->rows_per_tile;
-  if (plan->form == PA_LATENT_ABSORBED ? rows != kLatentRowsMma && rows != kLatentRowsPair
+  if (plan->form == PA_LATENT_ABSORBED ? rows != kLatentRowsMma && rows != kLatentRowsSolo && rows != kLatentRowsPair
                                        : rows != kLatentRowsExpanded)
     return PA_ERR_PLAN;
   if (plan->num_ranges < 0 || plan->num_segments < 0 || plan->num_merges < 0 ||
@@ -289,8 +289,9 @@ extern "C" pa_status_t pa_latent_attention(const pa_latent_shape_t* shape,
   p.total_q = plan->total_q;
   p.rows = plan->rows_per_tile;
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = plan->rows_per_tile == kLatentRowsPair ? launch_latent_pair(p, *shape, pages, s)
-                                                         : launch_latent_mma(p, *shape, pages, s);
+  cudaError_t e = plan->rows_per_tile == kLatentRowsPair   ? launch_latent_pair(p, *shape, pages, s)
+                  : plan->rows_per_tile == kLatentRowsSolo ? launch_latent_solo(p, *shape, pages, s)
+                                                           : launch_latent_mma(p, *shape, pages, s);
   if (e == cudaSuccess && p.num_merges > 0) e = launch_latent_merge(p, shape->dtype, s);
   return cuda_status(e);
 }

@@ -12,11 +12,12 @@ namespace pa {
 constexpr int kLatent = 512;                  // latent values of a cached row (also the values)
 constexpr int kRope = 64;                     // rotary key values
 constexpr int kLatentRow = kLatent + kRope;   // elements of a cached row
-constexpr int kLatentStage = 64;              // tokens of a stage of 16-row tiles: their pieces
-                                              // are cut at its multiples
+constexpr int kLatentStage = 64;              // tokens of a stage of 16- and 64-row tiles:
+                                              // their pieces are cut at its multiples
 constexpr int kLatentStagePair = 128;         // the same of 128-row tiles
 constexpr int kLatentBlock = 16;              // tokens of one page copy (divides every page size)
 constexpr int kLatentRowsMma = 16;            // rows of a tile: the mma.sync kernel
+constexpr int kLatentRowsSolo = 64;           // rows of a tile: the tcgen05 kernel on one SM
 constexpr int kLatentRowsPair = 128;          // rows of a tile: the tcgen05 kernel on SM pairs
 constexpr int kLatentRowsExpanded = 256;      // query tokens of an expanded tile
 constexpr uint32_t kLatentMagic = 0x564b414cu;  // "LAKV"

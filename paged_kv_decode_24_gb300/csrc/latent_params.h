@@ -49,6 +49,8 @@ struct LatentParams {
 // pages_map is the launchers' to fill: each kernel has boxes of its own.
 cudaError_t launch_latent_mma(const LatentParams& p, const pa_latent_shape_t& shape, const void* pages,
                               cudaStream_t stream);
+cudaError_t launch_latent_solo(const LatentParams& p, const pa_latent_shape_t& shape,
+                               const void* pages, cudaStream_t stream);
 cudaError_t launch_latent_pair(const LatentParams& p, const pa_latent_shape_t& shape,
                                const void* pages, cudaStream_t stream);
 cudaError_t launch_latent_merge(const LatentParams& p, int dtype, cudaStream_t stream);

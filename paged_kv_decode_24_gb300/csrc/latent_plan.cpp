@@ -176,7 +176,7 @@ extern "C" pa_status_t pa_latent_plan(const pa_latent_shape_t* shape, const int3
       o.rows_per_tile < 0)
     return PA_ERR_INVALID_ARG;
   if (absorbed ? (o.rows_per_tile != 0 && o.rows_per_tile != kLatentRowsMma &&
-                  o.rows_per_tile != kLatentRowsPair)
+                  o.rows_per_tile != kLatentRowsSolo && o.rows_per_tile != kLatentRowsPair)
                : (o.rows_per_tile != 0 || o.forced_splits != 0))
     return PA_ERR_INVALID_ARG;
   const int B = shape->batch;
@@ -200,7 +200,10 @@ extern "C" pa_status_t pa_latent_plan(const pa_latent_shape_t* shape, const int3
     int64_t most = 0;  // query rows of one sequence
     for (int b = 0; b < B; ++b)
       most = std::max(most, (int64_t)q_lens_host[b] * shape->num_heads);
-    rows = o.rows_per_tile ? o.rows_per_tile : most <= kLatentRowsMma ? kLatentRowsMma : kLatentRowsPair;
+    rows = o.rows_per_tile             ? o.rows_per_tile
+           : most <= kLatentRowsMma  ? kLatentRowsMma
+           : most <= kLatentRowsSolo ? kLatentRowsSolo
+                                     : kLatentRowsPair;
   }
   if (absorbed)
     absorbed_work(*shape, seq_lens_host, q_lens_host, cu_q, rows,

@@ -5,6 +5,7 @@
 // registers; descriptors are a base plus constants.
 #pragma once
 
+#include "latent_params.h"
 #include "prefill_tc5.cuh"
 
 namespace pa {
@@ -86,4 +87,61 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
 }
 
 }  // namespace tc5
+
+// The page of token tok, -1 from `end` on.  A volatile load, which stays where
+// it is written: a stage ahead of its use.
+__device__ __forceinline__ int table_entry(const int32_t* table, int page_size, int tok, int end) {
+  int page = -1;
+  if (tok < end) asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(page) : "l"(table + tok / page_size));
+  return page;
+}
+
+// 32 bytes to a 16-byte aligned address; `whole`: it is 32-byte aligned.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* w, bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+__device__ __forceinline__ void row_pair_barrier(int warp) {  // the two warps that share 32 rows
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 1)) : "memory");
+}
+
+// q as [T * H][576], with boxes of 64 rows by 64 dims.
+inline bool encode_latent_q(CUtensorMap* map, const LatentParams& p, int dtype) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {kLatentRow, (cuuint64_t)p.total_q * (cuuint64_t)p.heads};
+  cuuint64_t strides[1] = {kLatentRow * 2};
+  cuuint32_t box[2] = {64, kLatentRowsSolo};
+  cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType ty = dtype == PA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(map, ty, 2, const_cast<void*>(p.q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The pool [P][S][576] with boxes of `tokens` tokens by 64 dims.  (With the
+// row split into a dimension of nine boxes the copies run 12 % slower.)
+inline bool encode_latent_boxes(CUtensorMap* map, const void* pages, const pa_latent_shape_t& s, int tokens) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t row = kLatentRow * 2;
+  cuuint64_t dims[3] = {kLatentRow, (cuuint64_t)s.page_size, (cuuint64_t)s.num_pages};
+  cuuint64_t strides[2] = {row, row * s.page_size};
+  cuuint32_t box[3] = {64, (cuuint32_t)tokens, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType ty = s.dtype == PA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(map, ty, 3, const_cast<void*>(pages), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace pa

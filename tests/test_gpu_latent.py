@@ -95,11 +95,11 @@ ABSORBED = [
 ]
 
 
-# the two kernels: 16-row tiles (mma.sync), 128-row tiles on SM pairs (tcgen05)
-both_kernels = pytest.mark.parametrize("rows", [16, 128], ids=["mma_sync", "tcgen05"])
+# the kernels: 16-row tiles (mma.sync), 64-row tiles (tcgen05), 128-row tiles on SM pairs (tcgen05)
+all_kernels = pytest.mark.parametrize("rows", [16, 64, 128], ids=["mma_sync", "tcgen05", "tcgen05_pair"])
 
 
-@both_kernels
+@all_kernels
 @pytest.mark.parametrize("splits", [0, 3])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("case", ABSORBED, ids=lambda c: f"L{c[0][:3]}_q{c[1][:2]}_H{c[2]}_S{c[3]}")
@@ -114,7 +114,7 @@ def test_absorbed_parity(case, dtype, splits, rows):
     assert_latent_close(out.double().cpu().numpy(), want, max(lens), dtype, str(case))
 
 
-@both_kernels
+@all_kernels
 def test_absorbed_planner_splits_and_reruns_give_the_same_bits(rows):
     c = Case([20000, 777], [1, 1], heads=16, page=64, dtype="bf16", seed=8)
     d = Device(c, rows_per_tile=rows)
@@ -126,7 +126,7 @@ def test_absorbed_planner_splits_and_reruns_give_the_same_bits(rows):
     assert_latent_close(a.double().cpu().numpy(), want, 20000, "bf16")
 
 
-@both_kernels
+@all_kernels
 @pytest.mark.parametrize("splits", [0, 2])
 def test_absorbed_bad_pages_are_left_out(splits, rows):
     """One page of a sequence, every page of another (its rows get zeros)."""
@@ -142,7 +142,7 @@ def test_absorbed_bad_pages_are_left_out(splits, rows):
     assert torch.all(out[2] == 0)
 
 
-@both_kernels
+@all_kernels
 @pytest.mark.parametrize("scale", [1e-4, 1.0])
 def test_absorbed_scale_extremes(scale, rows):
     """Near-uniform weights, and weights that are almost one-hot with scores of
@@ -155,7 +155,7 @@ def test_absorbed_scale_extremes(scale, rows):
     assert_latent_close(out.double().cpu().numpy(), want, 1200, "fp16")
 
 
-@both_kernels
+@all_kernels
 def test_absorbed_offsets_past_32_bits(rows):
     """Pages beyond 2^31 elements (and 4 GB) of the pool."""
     pages = 2**32 // (16 * ROW * 2) + 40000       # 5 GB
@@ -177,7 +177,7 @@ def test_absorbed_offsets_past_32_bits(rows):
     assert_latent_close(out.double().cpu().numpy(), want, 300, "fp16")
 
 
-@both_kernels
+@all_kernels
 @pytest.mark.parametrize("splits", [1, 2])
 def test_absorbed_buffers_aligned_to_16_bytes_only(splits, rows):
     c = Case([300, 70], [2, 1], heads=12, page=16, seed=23)
@@ -327,7 +327,7 @@ def test_decode_steps_over_a_growing_cache():
         assert_latent_close(out.double().cpu().numpy(), want, 131, "bf16", f"step {step}")
 
 
-@both_kernels
+@all_kernels
 def test_captured_step_replays_and_follows_a_new_upload(rows):
     """append + attention in a CUDA graph; between replays a plan of the same
     structure is uploaded (longer sequences), two graphs on workspaces of their
@@ -396,7 +396,7 @@ def test_workspace_of_another_plan_is_flagged():
     assert torch.equal(d.pages.cpu(), c.pages)
 
 
-@both_kernels
+@all_kernels
 @pytest.mark.parametrize("splits", [1, 4])
 def test_waits_that_run_out_are_reported(splits, rows):
     """One nanosecond per wait: rows are left as they were or right, the status

@@ -44,7 +44,7 @@ BATCHES = [
 ]
 
 
-@pytest.mark.parametrize("rows", [0, 16, 128])
+@pytest.mark.parametrize("rows", [0, 16, 64, 128])
 @pytest.mark.parametrize("splits", [0, 1, 3])
 @pytest.mark.parametrize("case", BATCHES, ids=lambda c: f"B{len(c[0])}_H{c[2]}_L{max(c[0])}")
 def test_absorbed_plan_covers_every_row_and_token_once(lib, case, splits, rows):
@@ -54,7 +54,7 @@ def test_absorbed_plan_covers_every_row_and_token_once(lib, case, splits, rows):
     head, cu_q, cu_k, ranges, seg, merges = parts(p)
     most = max(q * heads for q in qs)
     R = head[7]
-    assert R == (rows or (16 if most <= 16 else 128)) == p.c.rows_per_tile
+    assert R == (rows or (16 if most <= 16 else 64 if most <= 64 else 128)) == p.c.rows_per_tile
     assert list(cu_q) == [0, *np.cumsum(qs)] and list(cu_k) == [0, *np.cumsum(lens)]
     stage = 128 if R == 128 else 64
     # ranges split the list of pieces, none is empty
@@ -142,7 +142,7 @@ def test_plan_refusals(lib):
         assert plan_code(good, lens, qs) == INVALID
     assert plan_code(good, [5, 3], [1, 1], sms=0) == INVALID
     assert plan_code(good, [5, 3], [1, 1], form=2) == INVALID
-    assert plan_code(good, [5, 3], [1, 1], rows=64) == INVALID
+    assert plan_code(good, [5, 3], [1, 1], rows=32) == INVALID
     assert plan_code(good, [5, 3], [1, 1], splits=-1) == INVALID
     assert plan_code(good, [5, 3], [1, 1], form=1, rows=128) == INVALID
     assert plan_code(good, [5, 3], [1, 1], form=1, splits=2) == INVALID
