@@ -47,8 +47,11 @@ std::atomic<uint64_t> g_latent_ids{1};
 // fixed cost of a piece, in stages: measured 2 to 2.8 of the 128-row kernel's
 // 2 us, about 1 of the 16-row kernel's 1.7 us
 constexpr int kPieceStages16 = 1, kPieceStages128 = 2;
-constexpr int kMinPiece = 2;     // stages of the shortest piece a cut leaves
-constexpr int kMinRange = 4;     // stages a range is worth launching a CTA for
+constexpr int kMinPiece = 1;     // stages of the shortest piece a cut leaves
+// stages a range is worth launching a CTA for: one sequence of 1000 tokens with
+// 16 heads takes 9.8 us with 1, 13.5 with 2, 17.0 with 4, 33 with 8; batches
+// that fill the GPU do not change
+constexpr int kMinRange = 1;
 
 struct Work {
   std::vector<int32_t> ranges;

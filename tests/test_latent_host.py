@@ -225,7 +225,7 @@ def test_call_refusals(lib, op):
     s = shape(2)
     s.num_heads = 200
     assert call(s=s) == UNSUPPORTED
-    for k, v in (("num_segments", 7), ("num_slots", -1), ("rows_per_tile", 32), ("form", 9),
+    for k, v in (("num_segments", 99), ("num_slots", -1), ("rows_per_tile", 32), ("form", 9),
                  ("workspace_bytes", 0)):
         plan = binding.PaLatentPlan.from_buffer_copy(c.p.c)
         setattr(plan, k, v)
