@@ -69,9 +69,11 @@ struct XLayout {
   static constexpr int Q_FULL = BARS;
   static constexpr int K_FULL = Q_FULL + 8;             // stages j & 1
   static constexpr int V_FULL = K_FULL + 16;            // stages j & 1
-  static constexpr int S_DONE = V_FULL + 16;            // one per tile, as PV_DONE
-  static constexpr int PV_DONE = S_DONE + 16;
-  static constexpr int V_CLEAR = PV_DONE + 16;          // the last stage's rows
+  // [tile][j & 1]: a copy thread that looks at stage j's late may find that of
+  // stage j + 1 complete too, but never that of stage j + 2
+  static constexpr int S_DONE = V_FULL + 16;
+  static constexpr int PV_DONE = S_DONE + 32;
+  static constexpr int V_CLEAR = PV_DONE + 32;          // the last stage's rows
   static constexpr int P_READY = V_CLEAR + 8;           // two halves per tile
   static constexpr int DRAIN = P_READY + 32;
   static constexpr int TMEM_SLOT = DRAIN + 8;
@@ -170,7 +172,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         for (int x = 0; x < per; ++x, ++u) {
           // the unit's slot was last used by unit u - ring, of stage (u - ring) / per
           for (; good && freed * per < u - ring + 1; ++freed)
-            good = mbar_wait_bounded_sleep(done + (n1 > freed ? 8 : 0), (uint32_t)(freed & 1), p.wait_ns);
+            good = mbar_wait_bounded_sleep(done + (n1 > freed ? 16 : 0) + 8 * (freed & 1),
+                                           (uint32_t)((freed >> 1) & 1), p.wait_ns);
           if (!good) break;
           const int slot = u % ring, tok = tile.k0 + j * kTokens + (keys ? 0 : x * (kTokens / 2));
           if (x == 0) mbar_arrive_expect_tx(bar, (uint32_t)(keys ? L::KB * L::BOX : 2 * L::VUNIT));
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             tc5::mma1(tmem + t * kTokens, tc5::desc_at(qb, b * L::BOX + k * 32), tc5::desc_at(kb, k * 32),
                       idesc_s, b > 0 || k > 0 ? 1u : 0u);
         }
-        tc5::commit(sb + L::S_DONE + 8 * t);
+        tc5::commit(sb + L::S_DONE + 16 * t + 8 * (j & 1));
       };
       bool good = wait(L::Q_FULL, 0u) && wait(L::K_FULL, 0u);
       if (good && n0 > 0) scores(0, 0);
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                                tc5::desc_at(vb, k * 2048), idesc_o, j > 0 || h > 0 || k > 0 ? 1u : 0u);
             }
             if (!good) break;
-            tc5::commit(sb + L::PV_DONE + 8 * t);
+            tc5::commit(sb + L::PV_DONE + 16 * t + 8 * (j & 1));
           }
         }
         for (int t = 0; t < 2 && good; ++t) {
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             if (!have_k) good = wait(L::K_FULL + 8 * ((j + 1) & 1), (uint32_t)(((j + 1) >> 1) & 1));
             have_k = true;
             // P V(j) reads P_t from the columns that S_t(j + 1) overwrites
-            good = good && wait(L::PV_DONE + 8 * t, (uint32_t)(j & 1));
+            good = good && wait(L::PV_DONE + 16 * t + 8 * (j & 1), (uint32_t)((j >> 1) & 1));
             if (good) scores(t, j + 1);
           }
         }
@@ -296,7 +299,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     float m_run = -INFINITY, l_run = 0.f;
     bool good = true;
     for (int j = 0; j < nt; ++j) {
-      good = __all_sync(kFull, mbar_wait_bounded_sleep(sb + L::S_DONE + 8 * t, (uint32_t)(j & 1), p.wait_ns));
+      good = __all_sync(kFull, mbar_wait_bounded_sleep(sb + L::S_DONE + 16 * t + 8 * (j & 1),
+                                                       (uint32_t)((j >> 1) & 1), p.wait_ns));
       if (!good) break;
       tc5::fence_after();
       float sv[kTokens];
@@ -358,7 +362,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       l_run = l_run * al + (s2.x + s2.y);
     }
     if (nt > 0 && good) {
-      good = __all_sync(kFull, mbar_wait_bounded_sleep(sb + L::PV_DONE + 8 * t, (uint32_t)((nt - 1) & 1),
+      good = __all_sync(kFull, mbar_wait_bounded_sleep(sb + L::PV_DONE + 16 * t + 8 * ((nt - 1) & 1),
+                                                       (uint32_t)(((nt - 1) >> 1) & 1),
                                                        p.wait_ns));
       if (good) {
         tc5::fence_after();

@@ -432,3 +432,84 @@ def test_expanded_waits_that_run_out_are_reported():
     out = d2.prefill()
     assert d2.done() == 0
     assert_latent_close(out.double().cpu().numpy(), want, 900, "fp16")
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_batches_against_the_oracle(seed):
+    """Random lengths, new tokens, heads, pages, types, tile rows, splits and
+    scales: append, rows read back, absorbed and expanded attention."""
+    rng = np.random.default_rng(1000 + seed)
+    B = int(rng.integers(1, 9))
+    lens = [int(x) for x in np.exp(rng.uniform(0, np.log(900), B))]
+    if rng.random() < 0.3:
+        lens[int(rng.integers(B))] = 0
+    qs = [int(min(n, rng.choice([0, 1, 1, 2, rng.integers(1, 300)]))) for n in lens]
+    heads = int(rng.choice([1, 2, 7, 16, 33, 64, 100, 128]))
+    qs = [q if q * heads < 3000 else 1 for q in qs]
+    page, hd = int(rng.choice([16, 32, 64, 128])), int(rng.choice([64, 128]))
+    dtype = str(rng.choice(["fp16", "bf16"]))
+    c = Case(lens, qs, heads=heads, head_dim=hd, page=page, dtype=dtype, seed=seed, poison=True,
+             scale=float(rng.uniform(0.01, 0.2)))
+    what = f"{lens} {qs} H{heads} S{page} D{hd} {dtype}"
+    after = oracle.latent_append(f64(c.pages), f64(c.c_new), f64(c.r_new), c.table.numpy(), lens, qs)
+    want = oracle.latent_attention(f64(c.q), after, c.table.numpy(), lens, qs, c.scale)
+    for rows in (0, 16, 64, 128):
+        d = Device(c, rows_per_tile=rows, forced_splits=int(rng.choice([0, 0, 2, 5])))
+        d.append()
+        out = d.attention()
+        assert d.done() == 0
+        assert_latent_close(out.double().cpu().numpy(), want, max(lens), dtype, f"{what} rows {rows}")
+    assert np.array_equal(np.nan_to_num(f64(d.gather().cpu())),
+                          np.nan_to_num(oracle.latent_gather(after, c.table.numpy(), lens)))
+    e = Device(c, form="expanded")
+    out = e.prefill()
+    assert e.done() == 0
+    want = oracle.latent_prefill(f64(c.qx), f64(c.k), f64(c.rows[:, LATENT:]), f64(c.v), lens, qs, c.scale)
+    assert_latent_close(out.double().cpu().numpy(), want, max(lens), dtype, what)
+
+
+def test_rows_behind_the_last_sequence_stay():
+    """Buffers with room behind the batch's rows: the rest keeps its contents."""
+    c = Case([70, 33], [3, 33], heads=5, head_dim=64, seed=24)
+    for form in ("absorbed", "expanded"):
+        d = Device(c, form=form)
+        width = LATENT if form == "absorbed" else 64
+        big = torch.full((c.T + 9, 5, width), 3.0, dtype=DT["fp16"], device="cuda")
+        (d.attention if form == "absorbed" else d.prefill)(big[:c.T])
+        rows = torch.full((c.Tk + 9, ROW), 3.0, dtype=DT["fp16"], device="cuda")
+        binding.latent_gather(d.shape, d.plan, d.pages, d.table, rows[:c.Tk], d.ws, d.status)
+        assert d.done() == 0
+        assert torch.all(big[c.T:] == 3) and torch.all(rows[c.Tk:] == 3)
+        assert not torch.any(torch.all(big[:c.T] == 3, dim=-1))
+
+
+def test_expanded_captured_and_replayed_with_new_inputs():
+    c = Case([500, 90], [500, 33], heads=2, seed=25)
+    d = Device(c, form="expanded")
+    out = d.prefill()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        d.prefill(out)
+    other = Case([500, 90], [500, 33], heads=2, seed=26)
+    for src, dst in ((other.qx, d.qx), (other.kv, d.kv), (other.rows, d.rows)):
+        dst.copy_(src)
+    out.fill_(float("nan"))
+    for _ in range(3):
+        g.replay()
+    assert d.done() == 0
+    want = oracle.latent_prefill(f64(other.qx), f64(other.k), f64(other.rows[:, LATENT:]), f64(other.v),
+                                 c.lens, c.qs, c.scale)
+    assert_latent_close(out.double().cpu().numpy(), want, 500, "fp16")
+
+
+@all_kernels
+def test_one_sequence_of_many_pieces(rows):
+    """A sequence cut into more pieces than a warp has lanes."""
+    c = Case([3000], [1], heads=16, page=64, dtype="bf16", seed=27)
+    d = Device(c, rows_per_tile=rows, forced_splits=47)
+    out = d.attention()
+    assert d.done() == 0
+    assert d.plan.c.num_slots == min(47, -(-3000 // (128 if rows == 128 else 64)))
+    want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), c.lens, c.qs, c.scale)
+    assert_latent_close(out.double().cpu().numpy(), want, 3000, "bf16")
