@@ -65,9 +65,8 @@ cudaError_t launch_split_q8(const SplitParams& p, int head_dim, int group, int f
   return cudaErrorInvalidValue;
 }
 
-// cuTensorMapEncodeTiled, reached through the runtime's driver entry point
-// (nullptr where the driver has none).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+// cuTensorMapEncodeTiled, reached through the runtime's driver entry point.
+static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {

@@ -1,11 +1,29 @@
 // Latent attention: the entry points, and the kernels that move rows.
 #include <math.h>
 
+#include <mutex>
+
 #include "device_common.cuh"
 #include "latent_params.h"
-#include "split_launch.cuh"
+#include "latent_launch.cuh"
 
 namespace pa {
+
+PFN_cuTensorMapEncodeTiled_v12000 latent_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    else
+      (void)cudaGetLastError();
+  });
+  return fn;
+}
 
 namespace {
 
@@ -106,7 +124,7 @@ cudaError_t launch_rows(const LatentRowsParams& p, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
   const int64_t blocks = ((int64_t)p.total + 8 * kWarpRows - 1) / (8 * kWarpRows);
   const int grid = (int)(blocks < kRowBlocks ? blocks : kRowBlocks);
-  return launch_pdl(latent_rows_kernel<APPEND>, 0, configured, p, grid, 256, stream);
+  return launch_latent(latent_rows_kernel<APPEND>, 0, configured, grid, 256, stream, p);
 }
 
 }  // namespace

@@ -30,7 +30,7 @@
 #include "device_common.cuh"
 #include "elem.cuh"
 #include "latent_segment.cuh"
-#include "split_launch.cuh"
+#include "latent_launch.cuh"
 
 namespace pa {
 
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kMergeWarps(WARPS) * 32)
 // The pool [P][S][576] with boxes of 16 whole rows, 128-byte swizzle over
 // their 128-byte lines.
 bool encode_latent_map(CUtensorMap* map, const void* pages, const pa_latent_shape_t& s) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 enc = latent_map_encoder();
   if (!enc) return false;
   const cuuint64_t row = kLatentRow * 2;
   cuuint64_t dims[4] = {64, kLatentRow / 64, (cuuint64_t)s.page_size, (cuuint64_t)s.num_pages};
@@ -469,8 +469,8 @@ bool encode_latent_map(CUtensorMap* map, const void* pages, const pa_latent_shap
 template <typename T>
 cudaError_t launch_mma_t(const LatentParams& p, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
-  return launch_pdl(latent_mma_kernel<T>, MmaLayout::BYTES, configured, p, p.num_ranges, kMmaThreads,
-                    stream);
+  return launch_latent(latent_mma_kernel<T>, MmaLayout::BYTES, configured, p.num_ranges, kMmaThreads,
+                       stream, p);
 }
 
 template <typename T>
@@ -478,8 +478,8 @@ cudaError_t launch_merge_t(const LatentParams& p, cudaStream_t stream) {
   static std::atomic<unsigned long long> one{0}, several{0};
   const int64_t rows = (int64_t)p.num_merges * p.rows;
   if (rows >= kManyMergeRows)
-    return launch_pdl(latent_merge_kernel<T, 1>, 0, one, p, (int)(rows / 4), 128, stream);
-  return launch_pdl(latent_merge_kernel<T, 8>, 0, several, p, (int)rows, 256, stream);
+    return launch_latent(latent_merge_kernel<T, 1>, 0, one, (int)(rows / 4), 128, stream, p);
+  return launch_latent(latent_merge_kernel<T, 8>, 0, several, (int)rows, 256, stream, p);
 }
 
 }  // namespace

@@ -36,7 +36,7 @@
 
 #include "latent_segment.cuh"
 #include "latent_tc5.cuh"
-#include "split_launch.cuh"
+#include "latent_launch.cuh"
 
 namespace pa {
 
@@ -556,8 +556,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 template <typename T>
 cudaError_t launch_t(const LatentParams& p, const CUtensorMap& q_map, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
-  return launch_pdl(latent_pair_kernel<T>, PLayout::BYTES, configured, p, 2 * p.num_ranges,
-                    kPairThreads, stream, q_map);
+  return launch_latent(latent_pair_kernel<T>, PLayout::BYTES, configured, 2 * p.num_ranges, kPairThreads,
+                       stream, p, q_map);
 }
 
 }  // namespace

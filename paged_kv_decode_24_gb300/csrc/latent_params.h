@@ -9,7 +9,8 @@
 
 namespace pa {
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // api.cu
+// cuTensorMapEncodeTiled; nullptr where the driver has none (latent.cu)
+PFN_cuTensorMapEncodeTiled_v12000 latent_map_encoder();
 
 // Rows between packed tensors and pages (append and gather).
 struct LatentRowsParams {

@@ -18,7 +18,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <new>
 #include <vector>
 
 #include "latent.h"
@@ -190,9 +189,10 @@ extern "C" pa_status_t pa_latent_plan(const pa_latent_shape_t* shape, const int3
     const int32_t len = seq_lens_host[b], q = q_lens_host[b];
     if (q < 0 || q > len || (int64_t)len > (int64_t)shape->max_pages_per_seq * shape->page_size)
       return PA_ERR_INVALID_ARG;
-    // the packed rows are indexed with 32 bits, heads included
+    // the packed rows are indexed with 32 bits, heads included; the kernels look
+    // a few stages past the last token
     if (((int64_t)cu_q[(size_t)b] + q) * shape->num_heads > INT32_MAX ||
-        (int64_t)cu_k[(size_t)b] + len > INT32_MAX)
+        (int64_t)cu_k[(size_t)b] + len > INT32_MAX - 65536)
       return PA_ERR_INVALID_ARG;
     cu_q[(size_t)b + 1] = cu_q[(size_t)b] + q;
     cu_k[(size_t)b + 1] = cu_k[(size_t)b] + len;
@@ -254,7 +254,7 @@ extern "C" pa_status_t pa_latent_plan(const pa_latent_shape_t* shape, const int3
   plan_out->host_blob = blob;
   plan_out->wait_limit_ns = o.wait_limit_ns;
   return PA_OK;
-} catch (const std::bad_alloc&) {
+} catch (...) {  // the only exceptions here are failed allocations
   return PA_ERR_NO_MEMORY;
 }
 

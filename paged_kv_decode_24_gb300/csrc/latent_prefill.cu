@@ -39,7 +39,7 @@
 
 #include "latent_params.h"
 #include "latent_tc5.cuh"
-#include "split_launch.cuh"
+#include "latent_launch.cuh"
 
 namespace pa {
 
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
 bool encode_rows(CUtensorMap* map, const void* ptr, int dtype, int box_tokens, int width,
                  int64_t tokens, int64_t token_stride, int64_t heads, int64_t head_stride,
                  bool token_major) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 enc = latent_map_encoder();
   if (!enc) return false;
   const cuuint64_t nt = (cuuint64_t)tokens, nh = (cuuint64_t)heads;
   cuuint64_t dims[3] = {(cuuint64_t)width, token_major ? nh : nt, token_major ? nt : nh};
@@ -425,8 +425,8 @@ bool encode_rows(CUtensorMap* map, const void* ptr, int dtype, int box_tokens, i
 template <typename T, int D>
 cudaError_t launch_t(const LatentPrefillParams& p, const XMaps& maps, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
-  return launch_pdl(latent_prefill_kernel<T, D>, XLayout<D>::BYTES, configured, p, p.num_tiles,
-                    kPrefillThreads, stream, maps);
+  return launch_latent(latent_prefill_kernel<T, D>, XLayout<D>::BYTES, configured, p.num_tiles,
+                       kPrefillThreads, stream, p, maps);
 }
 
 }  // namespace

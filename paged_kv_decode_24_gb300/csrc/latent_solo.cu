@@ -26,7 +26,7 @@
 
 #include "latent_segment.cuh"
 #include "latent_tc5.cuh"
-#include "split_launch.cuh"
+#include "latent_launch.cuh"
 
 namespace pa {
 
@@ -478,8 +478,8 @@ __global__ void __launch_bounds__(kSoloThreads, 1)
 template <typename T>
 cudaError_t launch_t(const LatentParams& p, const CUtensorMap& q_map, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
-  return launch_pdl(latent_solo_kernel<T>, SoloLayout::BYTES, configured, p, p.num_ranges, kSoloThreads,
-                    stream, q_map);
+  return launch_latent(latent_solo_kernel<T>, SoloLayout::BYTES, configured, p.num_ranges, kSoloThreads,
+                       stream, p, q_map);
 }
 
 }  // namespace

@@ -114,7 +114,7 @@ __device__ __forceinline__ void row_pair_barrier(int warp) {  // the two warps t
 
 // q as [T * H][576], with boxes of 64 rows by 64 dims.
 inline bool encode_latent_q(CUtensorMap* map, const LatentParams& p, int dtype) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 enc = latent_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[2] = {kLatentRow, (cuuint64_t)p.total_q * (cuuint64_t)p.heads};
   cuuint64_t strides[1] = {kLatentRow * 2};
@@ -130,7 +130,7 @@ inline bool encode_latent_q(CUtensorMap* map, const LatentParams& p, int dtype) 
 // The pool [P][S][576] with boxes of `tokens` tokens by 64 dims.  (With the
 // row split into a dimension of nine boxes the copies run 12 % slower.)
 inline bool encode_latent_boxes(CUtensorMap* map, const void* pages, const pa_latent_shape_t& s, int tokens) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 enc = latent_map_encoder();
   if (!enc) return false;
   const cuuint64_t row = kLatentRow * 2;
   cuuint64_t dims[3] = {kLatentRow, (cuuint64_t)s.page_size, (cuuint64_t)s.num_pages};

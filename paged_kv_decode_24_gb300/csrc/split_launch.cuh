@@ -14,11 +14,9 @@ namespace pa {
 // of dynamic shared memory, allowing programmatic dependent launch after the
 // previous kernel in the stream.  The shared-memory limit is raised once per
 // device; `configured` is the instance's own bit set of configured devices.
-// `more`: further arguments of the kernel (tensor maps).
-template <typename Kernel, typename Params, typename... More>
+template <typename Kernel, typename Params>
 cudaError_t launch_pdl(Kernel kern, int smem, std::atomic<unsigned long long>& configured,
-                       const Params& params, int grid, int threads, cudaStream_t stream,
-                       const More&... more) {
+                       const Params& params, int grid, int threads, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -38,7 +36,7 @@ cudaError_t launch_pdl(Kernel kern, int smem, std::atomic<unsigned long long>& c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, params, more...);
+  return cudaLaunchKernelEx(&cfg, kern, params);
 }
 
 // A split-decode kernel: CTAs of kWarpsPerCta warps.
