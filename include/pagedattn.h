@@ -595,7 +595,8 @@ typedef struct {
   int32_t rows_per_tile;    /* absorbed: 16, 64 or 128 (0: the planner's choice by the rows of a
                                sequence); expanded: 0 */
   int32_t forced_splits;    /* absorbed: cut every tile's tokens into this many pieces, as far
-                               as it has stages of 64 tokens (0: the planner's choice) */
+                               as it has stages of 64 tokens, or of 128 with 128-row tiles
+                               (0: the planner's choice); expanded: 0 */
   uint64_t wait_limit_ns;   /* how long a warp waits on one barrier before it gives up, sets
                                PA_DEV_TIMEOUT and leaves its rows unwritten (0: 1 s) */
 } pa_latent_options_t;
@@ -641,8 +642,9 @@ pa_status_t pa_latent_gather(const pa_latent_shape_t* shape, const pa_latent_pla
  * are left out and set PA_DEV_BAD_PAGE; a row left without any token gets
  * zeros.  The cached rows of a sequence's own tokens have to be finite (a
  * query's weight of a later token is 0, but its product may be formed); what
- * no sequence owns may hold anything.  Long sequences are cut into pieces over their tokens, whose
- * partial results a second kernel merges (one launch when nothing was cut).
+ * no sequence owns may hold anything.  Long sequences are cut into pieces over
+ * their tokens, whose partial results a second kernel merges (one launch when
+ * nothing was cut).
  * The same bits on every call.  The plan's form must be PA_LATENT_ABSORBED. */
 pa_status_t pa_latent_attention(const pa_latent_shape_t* shape, const pa_latent_plan_t* plan,
                                 const void* q, const void* pages, const int32_t* block_table,

@@ -101,9 +101,11 @@ __global__ void __launch_bounds__(256) latent_rows_kernel(const LatentRowsParams
       if (!APPEND)
         v[i] = static_cast<const uint4*>(p.pages)[cached + ch];
       else if (ch < kCChunks)
-        v[i] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.c) + (r0 + u) * p.c_stride)[ch];
+        v[i] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.c) +
+                                              (r0 + u) * p.c_stride)[ch];
       else
-        v[i] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.r) + (r0 + u) * p.r_stride)[ch - kCChunks];
+        v[i] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.r) +
+                                              (r0 + u) * p.r_stride)[ch - kCChunks];
     }
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
@@ -162,8 +164,9 @@ pa_status_t check_latent_call(const pa_latent_shape_t* s, const pa_latent_plan_t
       (form >= 0 && plan->form != form))
     return PA_ERR_PLAN;
   const int rows = plan->rows_per_tile;
-  if (plan->form == PA_LATENT_ABSORBED ? rows != kLatentRowsMma && rows != kLatentRowsSolo && rows != kLatentRowsPair
-                                       : rows != kLatentRowsExpanded)
+  const bool absorbed_rows =
+      rows == kLatentRowsMma || rows == kLatentRowsSolo || rows == kLatentRowsPair;
+  if (plan->form == PA_LATENT_ABSORBED ? !absorbed_rows : rows != kLatentRowsExpanded)
     return PA_ERR_PLAN;
   if (plan->num_ranges < 0 || plan->num_segments < 0 || plan->num_merges < 0 ||
       plan->num_slots < 0 || plan->total_q < 0 || plan->total_k < 0)
