@@ -49,7 +49,7 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int batch, int r, 
 // Two consecutive packed rows per warp and turn: 144 chunks of 16 bytes, up to
 // five a lane, in flight at once behind one look-up of the rows' places (lane
 // u looks up row u).  Both directions only move bytes.  Measured against the
-// copy bandwidth: contexts of 292 MB read back at 93 %, prompts of 125 MB
+// copy bandwidth: contexts of 292 MB read back at 90 to 93 %, prompts of 125 MB
 // written at 85 % (one row per warp 83 and 85 %, four 89 and 67 %: the lanes'
 // registers then leave too few warps), with up to 16 blocks an SM (8: 90 and
 // 83 %).

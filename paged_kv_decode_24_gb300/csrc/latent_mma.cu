@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 // WARPS warps share a row's pieces, each covering all 512 values: one where
 // many rows were cut (each warp then has its few pieces' loads in flight at
 // once), eight where few rows were cut into many pieces.  Measured on either
-// side of the limit, whole calls: 1344 rows of about 8 pieces 33.5 us with one
+// side of the limit, whole calls: 1280 rows of about 8 pieces 33.5 us with one
 // warp a row, 35.4 with eight.  One sequence has 16 to 128 rows of up to 152
 // pieces, of which one warp would read four at a time.
 // A merge by the last piece of a tile to end, inside the first kernel, was
