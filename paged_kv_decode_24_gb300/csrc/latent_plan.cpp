@@ -9,7 +9,8 @@
 // A tile that a cut falls into becomes several pieces, whose partial results
 // are merged.  A piece costs its stages and a fixed part (queries in, output
 // out), kPieceStages16 or 128; a cut that would leave a piece of less than
-// kMinPiece stages is moved to the tile's edge.
+// kMinPiece stages is moved to the tile's edge.  Few tiles may be cut one by one
+// instead (piece_stages).
 //
 // Expanded form.  A tile is up to kLatentRowsExpanded query tokens of one
 // head, the costliest first, so that the cheap ones fill the tail of the grid.
@@ -49,10 +50,16 @@ std::atomic<uint64_t> g_latent_ids{1};
 // 1, 2 and 3.
 constexpr int kPieceStages16 = 1, kPieceStages128 = 2;
 constexpr int kMinPiece = 1;     // stages of the shortest piece a cut leaves
-// Stages a range is worth launching a CTA for: one sequence of 1000 tokens with
-// 16 heads takes 9.8 us with 1, 13.5 with 2, 17.0 with 4, 33 with 8; batches
-// that fill the GPU do not change
-constexpr int kMinRange = 1;
+constexpr int kMinRange = 1;     // stages a range is worth launching a CTA for
+
+// What a batch's time has beside the stages of its longest range, in hundredths
+// of a stage: each piece (its partials out and in again) and the merge, by the
+// kernel of 16, 64 and 128 rows.  From calls of 1 to 16 sequences of 64 to 2048
+// tokens, with stages of 1.85, 1.45 and 1.5 us.
+struct PieceTimes {
+  int64_t piece, merge;
+};
+constexpr PieceTimes kTimes16 = {1, 130}, kTimes64 = {4, 290}, kTimes128 = {7, 270};
 
 struct Work {
   std::vector<int32_t> ranges;
@@ -68,12 +75,46 @@ struct AbsorbedTile {
   int32_t b, row0, nrows, span;  // span: tokens its last row sees
 };
 
+// Where every tile has a CTA of its own, tiles may also be cut one by one: into
+// pieces of up to `longest` stages, one a CTA.  This returns the length with
+// the least time, 0 where ranges of equal work take less: those keep every CTA
+// busy to the end, but most CTAs then have two pieces to write.  Whole and cut
+// tiles, us: 8 sequences of 256 tokens with 64 heads 10.9 and 13.1; of 1024 with
+// 16 heads 33.4, and 9.4 in pieces of one stage (equal ranges 10.7); 16 of 1024
+// with 64 heads 30.5, and 16.7 in pieces of four (equal ranges 22).
+int64_t piece_stages(const std::vector<int64_t>& stages, int rows, int64_t workers,
+                     int64_t piece_cost, int64_t equal_ranges, int64_t equal_quota) {
+  const PieceTimes& t = rows == kLatentRowsMma    ? kTimes16
+                        : rows == kLatentRowsSolo ? kTimes64
+                                                  : kTimes128;
+  const int64_t tiles = (int64_t)stages.size();
+  if (tiles > workers) return 0;
+  const int64_t longest = *std::max_element(stages.begin(), stages.end());
+  int64_t best = 100 * (equal_quota - piece_cost) + t.piece * (tiles + equal_ranges) + t.merge;
+  int64_t found = 0, last = 0;
+  for (int64_t k = 1; k <= std::min(workers, longest); ++k) {
+    const int64_t n = (longest + k - 1) / k;
+    if (n == last) continue;
+    last = n;
+    int64_t pieces = 0;
+    for (int64_t x : stages) pieces += (x + n - 1) / n;
+    if (pieces > workers) break;
+    const int64_t time = 100 * n + t.piece * pieces + (pieces > tiles ? t.merge : 0);
+    if (time <= best) {
+      best = time;
+      found = n;
+    }
+  }
+  return found;
+}
+
 void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_t* qs,
                    const std::vector<int32_t>& cu_q, int rows, int workers, int forced, Work* w) {
   const int64_t stage = rows == kLatentRowsPair ? kLatentStagePair : kLatentStage;
   const int64_t piece_cost = rows == kLatentRowsPair ? kPieceStages128 : kPieceStages16;
   auto stages_of = [&](int64_t tokens) { return (tokens + stage - 1) / stage; };
   std::vector<AbsorbedTile> tiles;
+  std::vector<int64_t> stages;
   int64_t total = 0;
   for (int b = 0; b < s.batch; ++b) {
     const int64_t all = (int64_t)qs[b] * s.num_heads;
@@ -82,7 +123,8 @@ void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_
       const int32_t last = (int32_t)((r + n - 1) / s.num_heads);  // query token of its last row
       const int32_t span = lens[b] - qs[b] + last + 1;
       tiles.push_back({b, (int32_t)r, n, span});
-      total += stages_of(span) + piece_cost;
+      stages.push_back(stages_of(span));
+      total += stages.back() + piece_cost;
     }
   }
   if (tiles.empty()) {
@@ -95,6 +137,7 @@ void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_
   // every range but the last is expected to end in a cut, a piece more
   auto share = [&](int64_t open) { return (total + piece_cost * (open - 1) + open - 1) / open; };
   int64_t quota = share(ranges);
+  const int64_t each = forced ? 0 : piece_stages(stages, rows, workers, piece_cost, ranges, quota);
   int64_t left = quota;  // of the range that is being filled
   w->ranges.push_back(0);
   auto close = [&] {
@@ -109,8 +152,8 @@ void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_
     int64_t at = 0, piece = 0;
     while (at < n) {
       int64_t take = n - at;
-      if (forced > 0) {
-        const int64_t parts = std::min<int64_t>(forced, n);
+      if (forced > 0 || each > 0) {
+        const int64_t parts = forced > 0 ? std::min<int64_t>(forced, n) : (n + each - 1) / each;
         ++piece;
         take = n * piece / parts - at;
         close();
@@ -129,7 +172,7 @@ void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_
       at += take;
       left -= take + piece_cost;
       total -= take + (at == n ? piece_cost : 0);
-      if (forced == 0 && left <= 0) close();
+      if (forced == 0 && each == 0 && left <= 0) close();
     }
     const size_t pieces = w->segments.size() - first;
     if (pieces > 1) {

@@ -101,6 +101,30 @@ def test_absorbed_ranges_have_equal_work(lib):
         assert per.max() <= per.mean() + 2 + fixed + 2, (heads, per.max(), per.mean())
 
 
+def test_few_tiles_are_cut_one_by_one(lib):
+    def counts(lens, heads):
+        p = binding.LatentPlan(shape(len(lens), heads, max_pages=3000), lens, [1] * len(lens), 152)
+        _, _, _, ranges, seg, _ = parts(p)
+        return len(ranges) - 1, len(seg), p.c.num_merges, seg
+    # short tiles stay whole
+    assert counts([128] * 8, 16)[:3] == (8, 8, 0) and counts([256] * 8, 64)[:3] == (8, 8, 0)
+    assert counts([384, 3, 100], 128)[:3] == (3, 3, 0) and counts([100] * 152, 16)[:3] == (152, 152, 0)
+    # longer ones become pieces of about one length, one for each SM (or pair) at most
+    for lens, heads, most in (([1024] * 8, 16, 152), ([3000, 500, 64], 64, 152), ([4000, 9000], 128, 76),
+                              ([30000], 16, 152)):
+        n, pieces, merges, seg = counts(lens, heads)
+        assert n == pieces <= most and merges > 0
+        unit = 128 if heads == 128 else 64
+        size = -(-(seg[:, 4] - seg[:, 3]) // unit)
+        for b, length in enumerate(lens):
+            mine = size[seg[:, 0] == b]
+            assert mine.max() - mine.min() <= 1 and mine.sum() == -(-length // unit)
+        assert size.max() <= size[seg[:, 0] == int(np.argmax(lens))].max()
+    # more tiles than SMs: ranges of equal work
+    n, pieces, _, _ = counts([500] * 200, 16)
+    assert n == 152 and pieces > 200
+
+
 @pytest.mark.parametrize("case", BATCHES, ids=lambda c: f"B{len(c[0])}_H{c[2]}_L{max(c[0])}")
 def test_expanded_plan_covers_every_token_and_head_once(lib, case):
     lens, qs, heads = case
