@@ -29,7 +29,7 @@
 // merge included, 73 % of the copy bandwidth; in its steady state a stage of 64
 // tokens takes 1.7 us on every SM at once, 95 % of it.  The rest is the start,
 // the last pieces' output and the merge, about 10 us.  One sequence of 1000
-// tokens: 9.8 us.
+// tokens: 8.6 us.
 #include <math.h>
 
 #include "decode_tc.cuh"
@@ -43,8 +43,9 @@ namespace pa {
 namespace {
 
 constexpr int kWorkWarps = 8;
-constexpr int kManyMergeRows = 608;  // cut rows from which the merge gives a row one warp
-                                     // (four an SM)
+// Warps of the merge in all up to which a warp may have as few as two pieces of a
+// row, and three (about 7 and 20 an SM).
+constexpr int kMergeFewWarps = 1100, kMergeMostWarps = 3040;
 PA_HD constexpr int kMergeWarps(int warps_per_row) { return warps_per_row < 4 ? 4 : warps_per_row; }
 constexpr int kMmaThreads = (kWorkWarps + 1) * 32;
 
@@ -368,12 +369,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 // no piece that completed has: its rows stay unwritten.
 // The partials come from L2, where they were written a moment before: the time
 // is that of a launch and of a row's loads, one behind the other.
-// WARPS warps share a row's pieces, each covering all 512 values: one where
-// many rows were cut (each warp then has its few pieces' loads in flight at
-// once), eight where few rows were cut into many pieces.  Measured on either
-// side of the limit, whole calls: 1280 rows of about 8 pieces 33.5 us with one
-// warp a row, 35.4 with eight.  One sequence has 16 to 128 rows of up to 152
-// pieces, of which one warp would read four at a time.
+// WARPS warps share a row's pieces, each covering all 512 values: as many as
+// leave each a few pieces and run at once.  Measured, whole calls: 1280 rows of 7
+// pieces (64-row tiles) 31.7 us with one warp a row, 29.9 with two, 30.5 with
+// four; 512 rows of 8 pieces 14.8 with two, 16.2 with four, 17.1 with eight; 128
+// rows of 16 pieces 10.0 with four, 9.4 with eight; 64 rows of 152 pieces 26.6
+// with four, 23.6 with eight; 1024 rows of 4 pieces 14.7 with one, 15.9 with two.
 // A merge by the last piece of a tile to end, inside the first kernel, was
 // slower (batch of 64, 16 heads: 69.6 against 64.5 us): its reads began when
 // everything else was over, on one SM a tile.
@@ -382,19 +383,20 @@ __global__ void __launch_bounds__(kMergeWarps(WARPS) * 32)
     latent_merge_kernel(const __grid_constant__ LatentParams p) {
   constexpr int ROWS = kMergeWarps(WARPS) / WARPS;  // rows of a block
   constexpr int BATCH = 4;                          // pieces in flight
-  __shared__ float4 acc_s[WARPS > 1 ? WARPS : 1][kLatent / 4];
-  __shared__ float sum_s[WARPS];
+  __shared__ float4 acc_s[kMergeWarps(WARPS)][WARPS > 1 ? kLatent / 4 : 1];
+  __shared__ float sum_s[kMergeWarps(WARPS)];
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+  const int part = warp % WARPS;
   const bool planned = latent_planned(p, p.rows);
   const int which = (int)blockIdx.x * ROWS + warp / WARPS;  // row of all tiles' rows
   const LatentMerge m = p.merges[which / p.rows];           // p.rows is a multiple of ROWS
   const int row = which % p.rows;
   pdl_launch_dependents();
   pdl_wait_primary();
-  if (!planned) return;  // reported already
-  if (row >= m.nrows || m.slot0 < 0 || m.n < 1 || (int64_t)m.slot0 + m.n > p.num_slots || m.row0 < 0 ||
-      (int64_t)m.row0 + m.nrows > (int64_t)p.total_q * p.heads)
-    return;
+  if (!planned) return;  // reported already; the same in the whole grid
+  const bool ok = row < m.nrows && m.slot0 >= 0 && m.n >= 1 && (int64_t)m.slot0 + m.n <= p.num_slots &&
+                  m.row0 >= 0 && (int64_t)m.row0 + m.nrows <= (int64_t)p.total_q * p.heads;
+  const int n = ok ? m.n : 0;
   const float* lse = p.part_lse + (int64_t)m.slot0 * p.rows + row;
   const float4* o =
       reinterpret_cast<const float4*>(p.part_o + ((int64_t)m.slot0 * p.rows + row) * kLatent) + lane;
@@ -405,26 +407,26 @@ __global__ void __launch_bounds__(kMergeWarps(WARPS) * 32)
     for (int b = 0; b < BATCH; ++b)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        v[b][c] = s0 + b * WARPS < m.n ? __ldcg(o + (int64_t)(s0 + b * WARPS) * step + 32 * c)
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[b][c] = s0 + b * WARPS < n ? __ldcg(o + (int64_t)(s0 + b * WARPS) * step + 32 * c)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
   };
-  load(warp % WARPS);  // in flight while the weights are found
+  load(part);  // in flight while the weights are found
   float mx = -INFINITY;
-  for (int s = lane; s < m.n; s += 32) mx = fmaxf(mx, __ldcg(lse + (int64_t)s * p.rows));
+  for (int s = lane; s < n; s += 32) mx = fmaxf(mx, __ldcg(lse + (int64_t)s * p.rows));
 #pragma unroll
   for (int w = 16; w >= 1; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, w));
-  if (mx == INFINITY) return;  // the same in every warp of the row
+  const bool whole = ok && mx != INFINITY;  // the same in every warp of the row
   const float ref = mx == -INFINITY ? 0.f : mx;
   float4 acc[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-  for (int s0 = warp % WARPS; s0 < m.n; s0 += BATCH * WARPS) {
+  for (int s0 = part; s0 < n; s0 += BATCH * WARPS) {
     if (s0 >= WARPS) load(s0);
 #pragma unroll
     for (int b = 0; b < BATCH; ++b) {
       const int s = s0 + b * WARPS;
-      if (s >= m.n) break;
+      if (s >= n) break;
       const float w = ex2(__ldcg(lse + (int64_t)s * p.rows) - ref);
       sum += w;
 #pragma unroll
@@ -441,9 +443,9 @@ __global__ void __launch_bounds__(kMergeWarps(WARPS) * 32)
     for (int c = 0; c < 4; ++c) acc_s[warp][lane + 32 * c] = acc[c];
     if (lane == 0) sum_s[warp] = sum;
     __syncthreads();
-    if (warp > 0) return;
+    if (part > 0) return;
 #pragma unroll 1
-    for (int g = 1; g < WARPS; ++g) {
+    for (int g = warp + 1; g < warp + WARPS; ++g) {
       sum += sum_s[g];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -455,6 +457,7 @@ __global__ void __launch_bounds__(kMergeWarps(WARPS) * 32)
       }
     }
   }
+  if (!whole) return;
   const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
   uint2* out = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + ((int64_t)m.row0 + row) * kLatent) + lane;
 #pragma unroll
@@ -487,13 +490,26 @@ cudaError_t launch_mma_t(const LatentParams& p, cudaStream_t stream) {
                        stream, p);
 }
 
-template <typename T>
+template <typename T, int WARPS>
 cudaError_t launch_merge_t(const LatentParams& p, cudaStream_t stream) {
-  static std::atomic<unsigned long long> one{0}, several{0};
+  static std::atomic<unsigned long long> configured{0};
+  constexpr int ROWS = kMergeWarps(WARPS) / WARPS;
   const int64_t rows = (int64_t)p.num_merges * p.rows;
-  if (rows >= kManyMergeRows)
-    return launch_latent(latent_merge_kernel<T, 1>, 0, one, (int)(rows / 4), 128, stream, p);
-  return launch_latent(latent_merge_kernel<T, 8>, 0, several, (int)rows, 256, stream, p);
+  return launch_latent(latent_merge_kernel<T, WARPS>, 0, configured, (int)(rows / ROWS),
+                       kMergeWarps(WARPS) * 32, stream, p);
+}
+
+template <typename T>
+cudaError_t launch_merge_any(const LatentParams& p, cudaStream_t stream) {
+  const int64_t rows = (int64_t)p.num_merges * p.rows, pieces = p.num_slots / p.num_merges;
+  int warps = 8;
+  while (warps > 1 && !(rows * warps <= kMergeFewWarps && pieces >= 2 * warps) &&
+         !(rows * warps <= kMergeMostWarps && pieces >= 3 * warps))
+    warps /= 2;
+  if (warps == 1) return launch_merge_t<T, 1>(p, stream);
+  if (warps == 2) return launch_merge_t<T, 2>(p, stream);
+  if (warps == 4) return launch_merge_t<T, 4>(p, stream);
+  return launch_merge_t<T, 8>(p, stream);
 }
 
 }  // namespace
@@ -507,8 +523,8 @@ cudaError_t launch_latent_mma(const LatentParams& params, const pa_latent_shape_
 }
 
 cudaError_t launch_latent_merge(const LatentParams& p, int dtype, cudaStream_t stream) {
-  if (dtype == PA_DTYPE_BF16) return launch_merge_t<__nv_bfloat16>(p, stream);
-  return launch_merge_t<__half>(p, stream);
+  if (dtype == PA_DTYPE_BF16) return launch_merge_any<__nv_bfloat16>(p, stream);
+  return launch_merge_any<__half>(p, stream);
 }
 
 }  // namespace pa
