@@ -574,7 +574,8 @@ typedef struct {
 typedef struct {
   pa_latent_shape_t shape;  /* the shape the plan was made for */
   int32_t form;             /* PA_LATENT_ABSORBED or PA_LATENT_EXPANDED */
-  int32_t rows_per_tile;    /* query rows of one tile: which kernel the work was cut for */
+  int32_t rows_per_tile;    /* absorbed: query rows of one tile, which kernel the work was cut
+                               for; expanded: 256, the most query tokens of a tile */
   int32_t num_ranges;       /* absorbed: work ranges (one CTA, or one CTA pair, each);
                                expanded: tiles */
   int32_t num_segments;     /* absorbed: (tile, token range) pieces over all ranges */
@@ -593,7 +594,7 @@ typedef struct {
 /* Options of a latent plan; a zeroed struct or NULL gives the defaults. */
 typedef struct {
   int32_t rows_per_tile;    /* absorbed: 16, 64 or 128 (0: the planner's choice by the rows of a
-                               sequence); expanded: 0 */
+                               sequence); expanded: 128 or 256 (0: its choice by the tiles) */
   int32_t forced_splits;    /* absorbed: cut every tile's tokens into this many pieces, as far
                                as it has stages of 64 tokens, or of 128 with 128-row tiles
                                (0: the planner's choice); expanded: 0 */

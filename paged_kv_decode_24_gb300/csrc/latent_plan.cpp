@@ -12,13 +12,16 @@
 // kMinPiece stages is moved to the tile's edge.  Few tiles may be cut one by one
 // instead (piece_stages).
 //
-// Expanded form.  A tile is up to kLatentRowsExpanded query tokens of one
-// head, the costliest first, so that the cheap ones fill the tail of the grid.
+// Expanded form.  A tile is up to 256 query tokens of one head, or up to 128
+// where that is estimated to end sooner (few tiles), the longest first, so that
+// the short ones fill the tail of the grid.
 #include <stdlib.h>
 #include <string.h>
 
 #include <algorithm>
 #include <atomic>
+#include <functional>
+#include <queue>
 #include <vector>
 
 #include "latent.h"
@@ -60,6 +63,13 @@ struct PieceTimes {
   int64_t piece, merge;
 };
 constexpr PieceTimes kTimes16 = {1, 130}, kTimes64 = {4, 290}, kTimes128 = {7, 270};
+
+// Expanded tiles: their start and output, and a stage of a tile of more than 128
+// query tokens and of fewer, in 0.05 us (contexts of 4096 and 8192 tokens, 32
+// heads: one tile of 256 takes 71 and 137 us, two of 128 side by side 56 and
+// 106).
+constexpr int kExpandedFixed = 100, kExpandedWhole = 41, kExpandedHalf = 32;
+constexpr int kExpandedFew = 2;  // whole tiles for each SM up to which halves are considered
 
 struct Work {
   std::vector<int32_t> ranges;
@@ -185,24 +195,58 @@ void absorbed_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_
     w->ranges.push_back((int32_t)w->segments.size());
 }
 
-void expanded_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_t* qs,
-                   const std::vector<int32_t>& cu_q, const std::vector<int32_t>& cu_k, int rows,
-                   Work* w) {
-  struct Sized {
-    LatentTile t;
-    int64_t cost;
-  };
+struct Sized {
+  LatentTile t;
+  int64_t stages, cost;
+};
+
+// The tiles of up to `rows` query tokens, those with most stages first.  (By
+// their cost, which puts short whole tiles before long halves, six chunks of 513
+// tokens take 170 us, this way 158: a chunk's tiles that run together share
+// its keys and values in L2.)
+std::vector<Sized> expanded_tiles(const pa_latent_shape_t& s, const int32_t* lens, const int32_t* qs,
+                                  const std::vector<int32_t>& cu_q, const std::vector<int32_t>& cu_k,
+                                  int rows) {
   std::vector<Sized> all;
   for (int b = 0; b < s.batch; ++b)
     for (int32_t t0 = 0; t0 < qs[b]; t0 += rows) {
       const int32_t n = std::min(rows, qs[b] - t0), pos0 = lens[b] - qs[b] + t0;
-      const int64_t cost = ((int64_t)pos0 + n + 127) / 128;  // stages
+      const int64_t stages = ((int64_t)pos0 + n + 127) / 128;
+      const int64_t cost =
+          kExpandedFixed + stages * (n > kLatentRowsExpanded / 2 ? kExpandedWhole : kExpandedHalf);
       for (int h = 0; h < s.num_heads; ++h)
-        all.push_back({{h, n, cu_q[(size_t)b] + t0, pos0, cu_k[(size_t)b], 0, 0, 0}, cost});
+        all.push_back({{h, n, cu_q[(size_t)b] + t0, pos0, cu_k[(size_t)b], 0, 0, 0}, stages, cost});
     }
   std::stable_sort(all.begin(), all.end(),
-                   [](const Sized& x, const Sized& y) { return x.cost > y.cost; });
-  for (const Sized& x : all) w->tiles.push_back(x.t);
+                   [](const Sized& x, const Sized& y) { return x.stages > y.stages; });
+  return all;
+}
+
+// When the last of `workers` CTAs ends that take the tiles in this order.
+int64_t expanded_end(const std::vector<Sized>& tiles, int workers) {
+  std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> ends;
+  int64_t last = 0;
+  for (const Sized& x : tiles) {
+    int64_t end = x.cost;
+    if ((int64_t)ends.size() == workers) {
+      end += ends.top();
+      ends.pop();
+    }
+    ends.push(end);
+    last = std::max(last, end);
+  }
+  return last;
+}
+
+void expanded_work(const pa_latent_shape_t& s, const int32_t* lens, const int32_t* qs,
+                   const std::vector<int32_t>& cu_q, const std::vector<int32_t>& cu_k, int rows,
+                   int workers, Work* w) {
+  std::vector<Sized> tiles = expanded_tiles(s, lens, qs, cu_q, cu_k, rows ? rows : kLatentRowsExpanded);
+  if (!rows && (int64_t)tiles.size() <= (int64_t)kExpandedFew * workers) {
+    std::vector<Sized> halves = expanded_tiles(s, lens, qs, cu_q, cu_k, kLatentRowsExpanded / 2);
+    if (expanded_end(halves, workers) * 100 <= expanded_end(tiles, workers) * 95) tiles.swap(halves);
+  }
+  for (const Sized& x : tiles) w->tiles.push_back(x.t);
 }
 
 }  // namespace
@@ -224,7 +268,8 @@ extern "C" pa_status_t pa_latent_plan(const pa_latent_shape_t* shape, const int3
     return PA_ERR_INVALID_ARG;
   if (absorbed ? (o.rows_per_tile != 0 && o.rows_per_tile != kLatentRowsMma &&
                   o.rows_per_tile != kLatentRowsSolo && o.rows_per_tile != kLatentRowsPair)
-               : (o.rows_per_tile != 0 || o.forced_splits != 0))
+               : (o.rows_per_tile != 0 && o.rows_per_tile != kLatentRowsExpanded / 2 &&
+                  o.rows_per_tile != kLatentRowsExpanded) || o.forced_splits != 0)
     return PA_ERR_INVALID_ARG;
   const int B = shape->batch;
   if (B > 0 && (!seq_lens_host || !q_lens_host)) return PA_ERR_INVALID_ARG;
@@ -263,7 +308,7 @@ extern "C" pa_status_t pa_latent_plan(const pa_latent_shape_t* shape, const int3
     absorbed_work(*shape, seq_lens_host, q_lens_host, cu_q, rows,
                   rows == kLatentRowsPair ? std::max(1, num_sms / 2) : num_sms, o.forced_splits, &w);
   else
-    expanded_work(*shape, seq_lens_host, q_lens_host, cu_q, cu_k, rows, &w);
+    expanded_work(*shape, seq_lens_host, q_lens_host, cu_q, cu_k, o.rows_per_tile, num_sms, &w);
   const size_t ranges = absorbed ? w.ranges.size() - 1 : w.tiles.size();
   if (ranges > (size_t)INT32_MAX || w.segments.size() > (size_t)INT32_MAX ||
       w.slots > INT32_MAX / rows)

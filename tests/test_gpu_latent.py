@@ -212,12 +212,13 @@ EXPANDED = [
 ]
 
 
+@pytest.mark.parametrize("rows", [128, 256])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("case", EXPANDED, ids=lambda c: f"L{c[0][:3]}_q{c[1][:2]}_H{c[2]}_D{c[3]}")
-def test_expanded_parity(case, dtype):
+def test_expanded_parity(case, dtype, rows):
     lens, qs, heads, hd = case
     c = Case(lens, qs, heads=heads, head_dim=hd, dtype=dtype, seed=seed_of(case))
-    d = Device(c, form="expanded")
+    d = Device(c, form="expanded", rows_per_tile=rows)
     out = d.prefill()
     assert d.done() == 0
     want = oracle.latent_prefill(f64(c.qx), f64(c.k), f64(c.rows[:, LATENT:]), f64(c.v), lens, qs,
@@ -239,14 +240,15 @@ def test_expanded_takes_other_strides():
     assert_latent_close(out.double().cpu().numpy(), want, 200, "fp16")
 
 
-def test_expanded_other_sequences_never_leak():
+@pytest.mark.parametrize("rows", [128, 256])
+def test_expanded_other_sequences_never_leak(rows):
     """The neighbours of a sequence in the packed rows hold NaN and infinity:
     its own output stays finite and right."""
     c = Case([100, 77, 100], [100, 50, 100], heads=2, head_dim=128, seed=13)
     for x in (c.kv, c.rows):
         x[:100] = float("nan")
         x[177:] = float("inf")
-    d = Device(c, form="expanded")
+    d = Device(c, form="expanded", rows_per_tile=rows)
     out = d.prefill()[100:150]
     assert d.done() == 0
     s = slice(100, 177)
@@ -255,10 +257,11 @@ def test_expanded_other_sequences_never_leak():
     assert_latent_close(out.double().cpu().numpy(), want, 77, "fp16")
 
 
+@pytest.mark.parametrize("rows", [128, 256])
 @pytest.mark.parametrize("scale", [1e-4, 2.0])
-def test_expanded_scale_extremes(scale):
+def test_expanded_scale_extremes(scale, rows):
     c = Case([700], [700], heads=2, seed=14, scale=scale)
-    d = Device(c, form="expanded")
+    d = Device(c, form="expanded", rows_per_tile=rows)
     out = d.prefill()
     assert d.done() == 0
     want = oracle.latent_prefill(f64(c.qx), f64(c.k), f64(c.rows[:, LATENT:]), f64(c.v), c.lens, c.qs,
@@ -417,9 +420,10 @@ def test_waits_that_run_out_are_reported(splits, rows):
     assert_latent_close(out.double().cpu().numpy(), want, 1500, "fp16")
 
 
-def test_expanded_waits_that_run_out_are_reported():
+@pytest.mark.parametrize("rows", [128, 256])
+def test_expanded_waits_that_run_out_are_reported(rows):
     c = Case([900, 300], [900, 40], heads=3, seed=22)
-    d = Device(c, form="expanded", wait_limit_ns=1)
+    d = Device(c, form="expanded", rows_per_tile=rows, wait_limit_ns=1)
     out = d.prefill()
     assert d.done() == binding.PA_DEV_TIMEOUT
     got = out.double().cpu().numpy()
@@ -461,11 +465,12 @@ def test_random_batches_against_the_oracle(seed):
         assert_latent_close(out.double().cpu().numpy(), want, max(lens), dtype, f"{what} rows {rows}")
     assert np.array_equal(np.nan_to_num(f64(d.gather().cpu())),
                           np.nan_to_num(oracle.latent_gather(after, c.table.numpy(), lens)))
-    e = Device(c, form="expanded")
-    out = e.prefill()
-    assert e.done() == 0
     want = oracle.latent_prefill(f64(c.qx), f64(c.k), f64(c.rows[:, LATENT:]), f64(c.v), lens, qs, c.scale)
-    assert_latent_close(out.double().cpu().numpy(), want, max(lens), dtype, what)
+    for rows in (0, 128, 256):
+        e = Device(c, form="expanded", rows_per_tile=rows)
+        out = e.prefill()
+        assert e.done() == 0
+        assert_latent_close(out.double().cpu().numpy(), want, max(lens), dtype, f"{what} tiles {rows}")
 
 
 def test_rows_behind_the_last_sequence_stay():
@@ -507,9 +512,23 @@ def test_expanded_captured_and_replayed_with_new_inputs():
 def test_one_sequence_of_many_pieces(rows):
     """A sequence cut into more pieces than a warp has lanes."""
     c = Case([3000], [1], heads=16, page=64, dtype="bf16", seed=27)
-    d = Device(c, rows_per_tile=rows, forced_splits=47)
+    d = Device(c, rows_per_tile=rows, forced_splits=47)   # 64-token stages: 47, 128: 24
     out = d.attention()
     assert d.done() == 0
     assert d.plan.c.num_slots == min(47, -(-3000 // (128 if rows == 128 else 64)))
     want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), c.lens, c.qs, c.scale)
     assert_latent_close(out.double().cpu().numpy(), want, 3000, "bf16")
+
+
+@all_kernels
+@pytest.mark.parametrize("batch,splits", [(1, 40), (8, 16), (20, 7), (40, 2), (9, 3)])
+def test_merge_by_every_number_of_warps(batch, splits, rows):
+    """Few and many rows, few and many pieces: 1, 2, 4 and 8 warps a row."""
+    heads = {16: 16, 64: 48, 128: 100}[rows]
+    c = Case([splits * 128] * batch, [1] * batch, heads=heads, page=32, seed=29 + splits)
+    d = Device(c, rows_per_tile=rows, forced_splits=splits)
+    out = d.attention()
+    assert d.done() == 0 and d.plan.c.num_slots == batch * splits
+    want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), c.lens, c.qs, c.scale)
+    assert_latent_close(out.double().cpu().numpy(), want, splits * 128, "fp16")
+    assert torch.equal(d.attention(), out)

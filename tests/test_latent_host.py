@@ -101,6 +101,18 @@ def test_absorbed_ranges_have_equal_work(lib):
         assert per.max() <= per.mean() + 2 + fixed + 2, (heads, per.max(), per.mean())
 
 
+def test_few_expanded_tiles_are_halves(lib):
+    def longest_tile(lens, qs, heads):
+        p = binding.LatentPlan(shape(len(lens), heads, max_pages=3000), lens, qs, 152, form="expanded")
+        tiles = parts(p)[3]
+        return len(tiles), int(tiles[:, 1].max())
+    assert longest_tile([8192], [256], 32) == (64, 128)
+    assert longest_tile([2048], [2048], 8) == (128, 128)
+    assert longest_tile([8192] * 2, [256] * 2, 76) == (152, 256)   # halves would need two turns
+    assert longest_tile([8192], [8192], 32) == (1024, 256)
+    assert longest_tile([130, 5], [130, 5], 3)[1] <= 256
+
+
 def test_few_tiles_are_cut_one_by_one(lib):
     def counts(lens, heads):
         p = binding.LatentPlan(shape(len(lens), heads, max_pages=3000), lens, [1] * len(lens), 152)
@@ -125,10 +137,12 @@ def test_few_tiles_are_cut_one_by_one(lib):
     assert n == 152 and pieces > 200
 
 
+@pytest.mark.parametrize("rows", [0, 128, 256])
 @pytest.mark.parametrize("case", BATCHES, ids=lambda c: f"B{len(c[0])}_H{c[2]}_L{max(c[0])}")
-def test_expanded_plan_covers_every_token_and_head_once(lib, case):
+def test_expanded_plan_covers_every_token_and_head_once(lib, case, rows):
     lens, qs, heads = case
-    p = binding.LatentPlan(shape(len(lens), heads, max_pages=3000), lens, qs, 152, form="expanded")
+    p = binding.LatentPlan(shape(len(lens), heads, max_pages=3000), lens, qs, 152, form="expanded",
+                           rows_per_tile=rows)
     head, cu_q, cu_k, tiles = parts(p)
     assert p.c.num_ranges == len(tiles) and p.c.workspace_bytes >= p.c.blob_bytes
     seen = set()
@@ -136,7 +150,7 @@ def test_expanded_plan_covers_every_token_and_head_once(lib, case):
         b = int(np.searchsorted(cu_q, q0, side="right")) - 1
         while qs[b] == 0:
             b -= 1
-        assert 1 <= n <= 256 and k0 == cu_k[b] and pos0 == lens[b] - qs[b] + q0 - cu_q[b]
+        assert 1 <= n <= (rows or 256) and k0 == cu_k[b] and pos0 == lens[b] - qs[b] + q0 - cu_q[b]
         assert q0 + n <= cu_q[b + 1]
         seen |= {(q0 + i, h) for i in range(n)}
     assert len(seen) == sum(qs) * heads == int(tiles[:, 1].sum())
@@ -168,7 +182,9 @@ def test_plan_refusals(lib):
     assert plan_code(good, [5, 3], [1, 1], form=2) == INVALID
     assert plan_code(good, [5, 3], [1, 1], rows=32) == INVALID
     assert plan_code(good, [5, 3], [1, 1], splits=-1) == INVALID
-    assert plan_code(good, [5, 3], [1, 1], form=1, rows=128) == INVALID
+    assert plan_code(good, [5, 3], [1, 1], form=1, rows=64) == INVALID
+    assert plan_code(good, [5, 3], [1, 1], form=1, rows=128) == 0
+    assert plan_code(good, [5, 3], [1, 1], rows=256) == INVALID
     assert plan_code(good, [5, 3], [1, 1], form=1, splits=2) == INVALID
     for k, v, want in (("num_heads", 129, UNSUPPORTED), ("num_heads", 0, INVALID),
                        ("head_dim", 96, UNSUPPORTED), ("latent_dim", 256, UNSUPPORTED),
