@@ -40,7 +40,7 @@
 // of visible pairs (78 % of what cuBLAS sustains under the power cap); a stage
 // takes 2.05 us where few CTAs run, 2.3 on all SMs (clocks under the cap).  A
 // tile of 128 tokens or fewer takes 1.6 us a stage: nothing overlaps its
-// softmax.  Six chunks of 513 tokens behind up to 5700 with 16 heads of 128:
+// softmax.  (So whole tiles where there are enough of them, see the planner.)  Six chunks of 513 tokens behind up to 5700 with 16 heads of 128:
 // 157 us, a fifth of it the tiles of the 513th tokens, the rest uneven ends.
 #include <math.h>
 
