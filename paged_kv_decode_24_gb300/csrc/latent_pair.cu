@@ -518,6 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           tc5::fence_after();
 #pragma unroll 2
           for (int x = 0; x < 256; x += 32) {
+            __syncwarp();  // the rows that are written have branched
             float ov[32];
             tc5::ld16(t_o + (uint32_t)x + lane_off, ov);
             tc5::ld16(t_o + (uint32_t)x + 16u + lane_off, ov + 16);

@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        __syncwarp();  // lanes may have branched, and what follows is for a whole warp
 #pragma unroll
         for (int c0 = 64 * h; c0 < 64 * h + 64; c0 += 32) {
           uint32_t pk[16];
@@ -379,6 +380,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                  ((int64_t)(tile.q0 + t * kRows + row) * p.heads + tile.head) * D;
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
+          __syncwarp();  // the rows that are written have branched
           float ov[32];
           tc5::ld32(t_o + (uint32_t)c, ov);
           tc5::wait_ld();
