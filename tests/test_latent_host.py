@@ -5,6 +5,9 @@ planner's work lists, the oracle against its own definition, and every refusal
 from __future__ import annotations
 
 import ctypes
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -353,3 +356,54 @@ def test_oracle_closed_forms():
     assert np.allclose(out[0], mean[None], atol=1e-14)
     out = oracle.latent_attention(q, pages, table, [20], [1], 1.0, bad_pages=[(0, 0), (0, 1)])[0]
     assert np.all(out == 0)
+
+
+C_STRUCTS = {"pa_latent_shape_t": "PaLatentShape", "pa_latent_plan_t": "PaLatentPlan",
+             "pa_latent_options_t": "PaLatentOptions"}
+
+
+def test_structs_and_plans_from_c(lib, tmp_path):
+    """The binding's structures have the C structs' sizes and offsets, and a C
+    program makes a plan of either form."""
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    lines = []
+    for c, py in C_STRUCTS.items():
+        lines.append(f'printf("{c} - %zu\\n", sizeof({c}));')
+        lines += [f'printf("{c} {f[0]} %zu\\n", offsetof({c}, {f[0]}));'
+                  for f in getattr(binding, py)._fields_]
+    code = """#include <stddef.h>
+#include <stdio.h>
+#include "pagedattn.h"
+int main(void) {
+  pa_latent_shape_t s = {2, 16, 128, 512, 64, 16, 64, 100, PA_DTYPE_BF16};
+  const int32_t lens[2] = {700, 33}, qs[2] = {1, 33};
+  pa_latent_options_t o = {0, 2, 0};
+  pa_latent_plan_t p;
+  if (pa_latent_plan(&s, lens, qs, 152, PA_LATENT_ABSORBED, &o, &p) != PA_OK) return 1;
+  if (p.total_q != 34 || p.total_k != 733 || p.num_slots < 2) return 2;
+  pa_latent_plan_free(&p);
+  if (pa_latent_plan(&s, lens, qs, 152, PA_LATENT_EXPANDED, NULL, &p) != PA_OK) return 3;
+  pa_latent_plan_free(&p);
+  if (p.host_blob != NULL) return 4;
+  %s
+  return 0;
+}
+""" % "\n  ".join(lines)
+    src, exe = tmp_path / "latent.c", str(tmp_path / "latent")
+    src.write_text(code)
+    root, libdir = os.path.dirname(os.path.dirname(os.path.abspath(__file__))), os.path.dirname(binding.LIB_PATH)
+    r = subprocess.run([cc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", "-I",
+                        os.path.join(root, "include"), str(src), "-o", exe, "-L", libdir, "-lpagedattn",
+                        "-Wl,-rpath," + libdir], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0
+    n = 0
+    for line in r.stdout.split("\n")[:-1]:
+        c, field, value = line.split()
+        cls = getattr(binding, C_STRUCTS[c])
+        assert (ctypes.sizeof(cls) if field == "-" else getattr(cls, field).offset) == int(value), line
+        n += 1
+    assert n == sum(1 + len(getattr(binding, py)._fields_) for py in C_STRUCTS.values())
