@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
 
   if (warp == 9 || warp == 10) {
     // ================= copies =================
+    const int valid = span - (n - 1) * kTokens;  // rows of the last stage that some row sees
     if (lane == 0 && n > 0) {
       const bool keys = warp == 9;
       const uint64_t keep = tc5::l2_evict_normal_policy(), once = l2_evict_first_policy();
@@ -197,6 +198,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           }
         }
       }
+      // rows to clear: the last stage's copies land before the zeros are written
+      if (good && !keys && valid < kTokens)
+        good = mbar_wait_bounded_sleep(full + 8 * ((n - 1) & 1), (uint32_t)(((n - 1) >> 1) & 1), p.wait_ns);
       if (!good) {
         set_status(p.status, PA_DEV_TIMEOUT);
         *flag = 1;
@@ -208,8 +212,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     }
     __syncwarp();
     // Rows of the last stage that no row of the tile sees become zeros (the
-    // copies have landed, and no product reads them before).
-    const int valid = span - (n - 1) * kTokens;
+    // copies have landed, and no product reads them before).  A CTA that gave up
+    // leaves them and V_CLEAR alone: the product is not formed.
     if (warp == 10 && n > 0 && *flag == 0 && valid < kTokens) {
       for (int h = 0; h < 2; ++h) {
         const int v0 = min(64, max(0, valid - h * 64)), chunks = (64 - v0) * 8;

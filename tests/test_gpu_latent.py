@@ -532,3 +532,28 @@ def test_merge_by_every_number_of_warps(batch, splits, rows):
     want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), c.lens, c.qs, c.scale)
     assert_latent_close(out.double().cpu().numpy(), want, splits * 128, "fp16")
     assert torch.equal(d.attention(), out)
+
+
+@pytest.mark.parametrize("rows", [128, 256])
+def test_expanded_rows_to_clear_under_any_wait_limit(rows):
+    """Neighbours that hold NaN behind the last visible token, and wait limits
+    from none to longer than the call: every row of the sequence between is as it
+    was or right, and a row that was left has its status."""
+    c = Case([100, 333, 100], [100, 300, 100], heads=3, head_dim=128, seed=31)
+    for x in (c.kv, c.rows):
+        x[:100] = float("nan")
+        x[433:] = float("nan")
+    s = slice(100, 433)
+    want = oracle.latent_prefill(f64(c.qx[100:400]), f64(c.k[s]), f64(c.rows[s, LATENT:]),
+                                 f64(c.v[s]), [333], [300], c.scale)
+    for limit in (1, 300, 1000, 2000, 3000, 5000, 8000, 20000, 10**9):
+        d = Device(c, form="expanded", rows_per_tile=rows, wait_limit_ns=limit)
+        out = torch.full((c.T, 3, 128), 7.0, dtype=DT["fp16"], device="cuda")
+        d.prefill(out)
+        status = d.done()
+        got = out[100:400].double().cpu().numpy()
+        left = (got == 7).all(axis=-1)
+        assert status == (binding.PA_DEV_TIMEOUT if left.any() else status) and status in (0, 8)
+        assert limit < 10**9 or (status == 0 and not left.any())
+        if not left.all():
+            assert_latent_close(got[~left], tuple(x[~left] for x in want), 333, "fp16", f"{limit} ns")

@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import re
 import shutil
 import subprocess
 
@@ -407,3 +408,31 @@ int main(void) {
         assert (ctypes.sizeof(cls) if field == "-" else getattr(cls, field).offset) == int(value), line
         n += 1
     assert n == sum(1 + len(getattr(binding, py)._fields_) for py in C_STRUCTS.values())
+
+
+# ---- hand-overs, by reading: what a wait that gave up may still let happen
+# cannot be brought about on a GPU without stalling it
+
+def kernel_source(name):
+    """A kernel's source without comments, white space as single blanks."""
+    path = os.path.join(os.path.dirname(binding.LIB_PATH), os.pardir, "csrc", name)
+    with open(path, encoding="utf-8") as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    return re.sub(r"\s+", " ", text)
+
+
+def test_value_rows_are_cleared_only_after_a_wait_whose_answer_counts():
+    """Expanded form: the zeros behind the last visible token may be written
+    only once the last stage's copies have landed.  That wait has the plan's
+    limit, and its failure sets the status and the flag that keeps the rows from
+    being cleared and handed over; the short drain waits, whose answers are not
+    used, come after it."""
+    src = kernel_source("latent_prefill.cu")
+    copies = src[src.index("warp == 9 || warp == 10"):src.index("} else if (warp == 8)")]
+    landed = copies.find("good = mbar_wait_bounded_sleep(full + 8 * ((n - 1) & 1), "
+                         "(uint32_t)(((n - 1) >> 1) & 1), p.wait_ns)")
+    assert landed >= 0, "no wait with the plan's limit before the rows are cleared"
+    gave_up = copies.index("if (!good) { set_status(p.status, PA_DEV_TIMEOUT); *flag = 1; }")
+    clears = copies.index("make_uint4(0u, 0u, 0u, 0u)")
+    assert landed < gave_up < copies.index("kDrainWaitNs") < clears < copies.index("L::V_CLEAR")
+    assert "*flag == 0" in copies[gave_up:clears]
