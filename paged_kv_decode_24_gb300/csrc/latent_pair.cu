@@ -383,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tc5::commit2(sb + L::DRAIN);
     }
     __syncwarp();
-    tc5::warp_wait(sb + L::DRAIN, 0u, kDrainWaitNs);
+    if (rank == 0) tc5::warp_wait(sb + L::DRAIN, 0u, kDrainWaitNs);
   } else {
     // ================= softmax and output =================
     const int row = (warp & 1) * 32 + lane;        // of the CTA's 64
@@ -560,8 +560,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   tc5::fence_before();
   __syncthreads();
-  cluster_sync();  // nothing is in flight between the CTAs any more
+  cluster_sync();  // the first CTA has committed its last products and seen them end
   if (warp == 4) {
+    // the commit's arrival here: counted from the barrier, so that the limit holds
+    // whatever the range took
+    if (rank != 0) tc5::warp_wait(sb + L::DRAIN, 0u, kDrainWaitNs);
     tc5::fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }

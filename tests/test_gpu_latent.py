@@ -557,3 +557,43 @@ def test_expanded_rows_to_clear_under_any_wait_limit(rows):
         assert limit < 10**9 or (status == 0 and not left.any())
         if not left.all():
             assert_latent_close(got[~left], tuple(x[~left] for x in want), 333, "fp16", f"{limit} ns")
+
+
+def test_pair_call_that_takes_longer_than_a_drain():
+    """One pair of SMs works through eight long sequences, well over the 10 ms of
+    the waits at a kernel's end: the call is right, and so is the next one."""
+    lens, heads, page = [131072 - 77 * b for b in range(8)], 128, 128
+    counts = [-(-n // page) for n in lens]
+    g = torch.Generator(device="cuda").manual_seed(32)
+    shape = binding.make_latent_shape(8, heads, 128, page, max(counts), sum(counts), "bf16")
+    pages = torch.randn(sum(counts), page, ROW, generator=g, device="cuda").bfloat16()
+    order = torch.randperm(sum(counts), generator=g, device="cuda").int()
+    table = torch.full((8, max(counts)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(counts):
+        table[b, :n] = order[at:at + n]
+        at += n
+    q = torch.randn(8, heads, ROW, generator=g, device="cuda").bfloat16()
+    plan = binding.LatentPlan(shape, lens, [1] * 8, 2)
+    assert plan.c.num_ranges == 1 and plan.c.num_segments == 8
+    ws = binding.alloc_workspace(plan)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    binding.latent_upload(plan, ws)
+    outs = []
+    for _ in range(2):
+        out = torch.full((8, heads, LATENT), float("nan"), dtype=torch.bfloat16, device="cuda")
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        binding.latent_attention(shape, plan, q, pages, table, 0.07, out, ws, status)
+        end.record()
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0 and start.elapsed_time(end) > 10
+        outs.append(out)
+    assert torch.equal(bits(outs[0]), bits(outs[1]))
+    for b, n in enumerate(lens):
+        z = pages[table[b, :counts[b]].long()].reshape(-1, ROW)[:n].double()
+        x = q[b].double()
+        w = torch.softmax(x @ z.T * 0.07, 1)
+        want = [w @ z[:, :LATENT], w @ z[:, :LATENT].abs(), (x.abs() @ z.abs().T * 0.07).amax(1)]
+        assert_latent_close(outs[0][b].double().cpu().numpy(), [y.cpu().numpy() for y in want], n,
+                            "bf16", f"sequence {b}")

@@ -436,3 +436,20 @@ def test_value_rows_are_cleared_only_after_a_wait_whose_answer_counts():
     clears = copies.index("make_uint4(0u, 0u, 0u, 0u)")
     assert landed < gave_up < copies.index("kDrainWaitNs") < clears < copies.index("L::V_CLEAR")
     assert "*flag == 0" in copies[gave_up:clears]
+
+
+def test_second_cta_waits_for_the_drain_after_the_first_has_committed_it():
+    """Pairs: the last commit arrives in both CTAs.  The second one, which issues
+    no products, starts its limited wait only behind the cluster barrier that the
+    first CTA reaches after the commit, whatever the call takes, and neither frees
+    tensor memory or ends before."""
+    src = kernel_source("latent_pair.cu")
+    src = src[src.index("latent_pair_kernel("):src.index("cudaError_t launch_t(")]
+    commit = src.index("commit2(sb + L::DRAIN)")
+    waits = [m.start() for m in re.finditer(r"L::DRAIN, 0u, kDrainWaitNs\)", src)]
+    meet = src.index("cluster_sync();", commit)
+    free = src.index("tcgen05.dealloc")
+    assert len(waits) == 2 and commit < waits[0] < meet < waits[1] < free, (commit, waits, meet, free)
+    first, second = (src[src.rindex("if (", 0, w):w] for w in waits)
+    assert first.startswith("if (rank == 0)") and second.startswith("if (rank != 0)")
+    assert src.index("cluster_sync();", meet + 1) > free
