@@ -69,6 +69,7 @@ struct MmaLayout {
 static_assert(MmaLayout::BYTES <= kMaxCtaSmem, "ring does not fit in shared memory");
 
 __device__ __forceinline__ void work_barrier() {
+  __syncwarp();  // the barrier is for converged warps
   asm volatile("bar.sync 1, %0;" ::"n"(kWorkWarps * 32) : "memory");
 }
 

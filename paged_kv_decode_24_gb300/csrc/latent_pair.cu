@@ -105,6 +105,7 @@ __device__ __forceinline__ uint32_t cta_rank() {
 }
 
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();  // the barrier is for converged warps
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
@@ -172,6 +173,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     fence_barrier_init();
   }
   if (warp == 4) {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      sb + L::TMEM_SLOT)
                  : "memory");
@@ -431,6 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           wait(L::S_DONE + 8 * (cs & 1), (uint32_t)((cs >> 1) & 1));
           tc5::fence_after();
           float sv[64];
+          __syncwarp();  // the wait's lanes meet: tensor memory is for a whole warp
 #pragma unroll
           for (int x = 0; x < 64; x += 16) tc5::ld16(t_s + (uint32_t)(64 * (cs & 1) + x) + lane_off, sv + x);
           tc5::wait_ld();
@@ -479,6 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
           if (j > 0 && __any_sync(kFull, resc)) {
             const float f = resc ? al : 1.f;
+            __syncwarp();  // rows whose maximum rose have branched
 #pragma unroll 4
             for (int x = 0; x < 256; x += 16) {
               float ov[16];
@@ -566,6 +570,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // whatever the range took
     if (rank != 0) tc5::warp_wait(sb + L::DRAIN, 0u, kDrainWaitNs);
     tc5::fence_after();
+    __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
   cluster_sync();

@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     fence_barrier_init();
   }
   if (warp == 8) {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      sb + L::TMEM_SLOT)
                  : "memory");
@@ -315,6 +316,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       if (!good) break;
       tc5::fence_after();
       float sv[kTokens];
+      __syncwarp();  // the wait's lanes meet: tensor memory is for a whole warp
 #pragma unroll
       for (int c = 0; c < kTokens; c += 32) tc5::ld32(t_s + (uint32_t)c, sv + c);
       tc5::wait_ld();
@@ -337,6 +339,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       // S(j) was issued after P V(j - 1) was done, so O may be rescaled now
       if (j > 0 && __any_sync(kFull, resc)) {
         const float f = resc ? al : 1.f;
+        __syncwarp();  // rows whose maximum rose have branched
 #pragma unroll 2
         for (int c = 0; c < D; c += 16) {
           float ov[16];
@@ -409,6 +412,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   __syncthreads();
   if (warp == 8) {
     tc5::fence_after();
+    __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }

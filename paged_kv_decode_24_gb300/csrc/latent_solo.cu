@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kSoloThreads, 1)
     fence_barrier_init();
   }
   if (warp == 4) {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      sb + L::TMEM_SLOT)
                  : "memory");
@@ -352,6 +353,7 @@ __global__ void __launch_bounds__(kSoloThreads, 1)
           wait(L::S_DONE + 8 * (cs & 1), (uint32_t)((cs >> 1) & 1));
           tc5::fence_after();
           float sv[32];
+          __syncwarp();  // the wait's lanes meet: tensor memory is for a whole warp
           tc5::ld32(t_s + (uint32_t)(32 * (cs & 1)) + lane_off, sv);
           tc5::wait_ld();
           const int tok = s.tok0 + j * kSoloTokens + half * 32;
@@ -399,6 +401,7 @@ __global__ void __launch_bounds__(kSoloThreads, 1)
                 make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
           if (j > 0 && __any_sync(kFull, resc)) {
             const float f = resc ? al : 1.f;
+            __syncwarp();  // rows whose maximum rose have branched
 #pragma unroll 4
             for (int x = 0; x < 256; x += 16) {
               float ov[16];
@@ -482,6 +485,7 @@ __global__ void __launch_bounds__(kSoloThreads, 1)
   __syncthreads();
   if (warp == 4) {
     tc5::fence_after();
+    __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }

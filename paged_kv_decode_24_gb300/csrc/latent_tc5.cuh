@@ -109,6 +109,7 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t* w, bool whole
 }
 
 __device__ __forceinline__ void row_pair_barrier(int warp) {  // the two warps that share 32 rows
+  __syncwarp();  // the barrier is for converged warps
   asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 1)) : "memory");
 }
 

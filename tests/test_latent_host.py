@@ -453,3 +453,26 @@ def test_second_cta_waits_for_the_drain_after_the_first_has_committed_it():
     first, second = (src[src.rindex("if (", 0, w):w] for w in waits)
     assert first.startswith("if (rank == 0)") and second.startswith("if (rank != 0)")
     assert src.index("cluster_sync();", meet + 1) > free
+
+
+@pytest.mark.parametrize("name", ["latent_prefill.cu", "latent_solo.cu", "latent_pair.cu"])
+def test_aligned_instructions_follow_a_reconvergence(name):
+    """Tensor-memory accesses and hand-written barriers are for a whole converged
+    warp.  Between a branch, a vote or a wait and the next of them stands a
+    __syncwarp: nothing relies on where the compiler lets a warp's lanes meet."""
+    src = kernel_source(name)
+    src = src[src.index("__launch_bounds__"):src.index("cudaError_t launch_t(")]
+    access = r"tc5::(?:ld16|ld32|st16|st16u|wait_ld|wait_st)\(|tcgen05\.(?:alloc|dealloc|relinquish)"
+    branch = r"\bif \(|__any_sync|__all_sync|warp_wait\(|\bwait\(|mbar_\w+\("
+    last, checked = "", 0
+    for m in re.finditer(f"(?P<sync>__syncwarp\\(\\))|(?P<access>{access})|(?P<branch>{branch})", src):
+        if m.lastgroup == "access":
+            assert last != "branch", src[max(0, m.start() - 160):m.end() + 40]
+            checked += 1
+        last = m.lastgroup
+    assert checked >= 10
+    for path, func in (("latent_tc5.cuh", "void row_pair_barrier("), ("latent_pair.cu", "void cluster_sync("),
+                       ("latent_mma.cu", "void work_barrier(")):
+        text = kernel_source(path)
+        body = text[text.index(func):]
+        assert 0 < body.index("__syncwarp()") < body.index("asm volatile"), path
