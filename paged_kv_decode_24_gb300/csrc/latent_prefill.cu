@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     // Rows of the last stage that no row of the tile sees become zeros (the
     // copies have landed, and no product reads them before).  A CTA that gave up
     // leaves them and V_CLEAR alone: the product is not formed.
-    if (warp == 10 && n > 0 && *flag == 0 && valid < kTokens) {
+    // (One vote decides for the warp: another warp may set the flag while it is read.)
+    if (warp == 10 && n > 0 && valid < kTokens && __all_sync(kFull, *flag == 0)) {
       for (int h = 0; h < 2; ++h) {
         const int v0 = min(64, max(0, valid - h * 64)), chunks = (64 - v0) * 8;
         unsigned char* unit = base + L::V + (2 * (n - 1) + h) % L::NV * L::VUNIT;

@@ -476,3 +476,11 @@ def test_aligned_instructions_follow_a_reconvergence(name):
         text = kernel_source(path)
         body = text[text.index(func):]
         assert 0 < body.index("__syncwarp()") < body.index("asm volatile"), path
+
+
+def test_a_flag_that_others_may_set_is_read_by_a_vote():
+    """Expanded form: the lanes that clear rows meet in __syncwarp, so all of them
+    or none take that branch, also when another warp gives up meanwhile."""
+    src = kernel_source("latent_prefill.cu")
+    reads = [src[max(0, m.start() - 20):m.end()] for m in re.finditer(r"\*flag == 0", src)]
+    assert reads and all("__all_sync(kFull, *flag == 0" in r for r in reads), reads
