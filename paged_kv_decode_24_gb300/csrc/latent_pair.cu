@@ -205,6 +205,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // whose own copy warps announce the bytes of both.
     const bool keys = warp == 5;
     int c = 0, qc = 0;
+    int issued = 0;  // groups of stage c whose copies are under way
     bool good = true;
     const uint64_t once = l2_evict_first_policy(), keep = tc5::l2_evict_normal_policy();
     const int box = p.page_size < 64 ? p.page_size : 64;  // tokens of one copy
@@ -263,6 +264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               for (int b = L::BPG * g; b < L::BPG * (g + 1); ++b)
                 tma_load_3d_pair(sb + L::K + b * L::KBOX + u * box * 128, &p.pages_map, b * 64, row, page,
                                  full0 + 8 * g, keep);
+            issued = g + 1;
           } else {     // four boxes, the CTA's half of the values, of 64 tokens
             const unsigned mask = ((1u << per) - 1u) << (g * per);
             // rows to clear: the second CTA's copies complete on its own barrier
@@ -283,11 +285,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               for (int b = 0; b < 4; ++b)
                 tma_load_3d_pair(sb + L::V + g * L::VGROUP + b * L::VBOX + u * box * 128, &p.pages_map,
                                  ((b >> 1) * 4 + rank * 2 + (b & 1)) * 64, row, page, bar, keep);
+            issued = g + 1;
             if (clear) {  // the rest of the last 16 tokens, and the tokens of bad pages
-              good = rank == 0 ? tc5::warp_wait(sb + L::V_FULL + 8 * g, (uint32_t)(c & 1), p.wait_ns)
-                               : tc5::warp_wait(sb + L::V_HERE + 8 * g, (uint32_t)(clears >> g & 1), p.wait_ns);
+              const uint32_t landed = sb + (rank == 0 ? L::V_FULL : L::V_HERE) + 8 * g;
+              const uint32_t parity = (uint32_t)((rank == 0 ? c : clears >> g) & 1);
+              good = tc5::warp_wait(landed, parity, p.wait_ns);
               clears ^= 1 << g;
-              if (!good) break;
+              if (!good) {
+                tc5::warp_wait(landed, parity, kDrainWaitNs);
+                break;
+              }
               __syncwarp();
               for (int v = 0; v < 4; ++v) {
                 const int at = g * 64 + v * kLatentBlock;  // first token of the block
@@ -306,14 +313,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
           __syncwarp();
         }
+        if (!good) break;
+        issued = 0;
       }
     }
-    if (!good && lane == 0) set_status(p.status, PA_DEV_TIMEOUT);
-    // every copy has been read, and with it every arrival that the MMAs send
-    // here has come, before the CTA ends
-    if (c > 0)
-      for (int g = 0; g < groups; ++g) wait_free(g, c - 1, kDrainWaitNs);
-    if (qc > 0) tc5::warp_wait(sb + L::Q_FREE, (uint32_t)((qc - 1) & 1), kDrainWaitNs);
+    if (good) {
+      // every copy has been read, and with it every arrival that the MMAs send
+      // here has come, before the CTA ends
+      if (c > 0)
+        for (int g = 0; g < groups; ++g) wait_free(g, c - 1, kDrainWaitNs);
+      if (qc > 0) tc5::warp_wait(sb + L::Q_FREE, (uint32_t)((qc - 1) & 1), kDrainWaitNs);
+    } else {
+      if (lane == 0) set_status(p.status, PA_DEV_TIMEOUT);
+      // What is under way lands before the CTAs meet at the end: each group's last
+      // use, of stage c or of the one before.  The first CTA's barriers count the
+      // copies of both (the arrivals of the MMAs come before that of DRAIN).
+      if (rank == 0) {
+        for (int g = 0; g < groups; ++g) {
+          const int u = c - (g < issued ? 0 : 1);
+          if (u >= 0)
+            tc5::warp_wait(sb + (keys ? L::K_FULL : L::V_FULL) + 8 * g, (uint32_t)(u & 1), kDrainWaitNs);
+        }
+        if (!keys && qc > 0) tc5::warp_wait(sb + L::Q_FULL, (uint32_t)((qc - 1) & 1), kDrainWaitNs);
+      }
+    }
     __syncwarp();
   } else if (warp == 4) {
     // ================= MMAs (one thread of the first CTA) =================

@@ -180,9 +180,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         const uint32_t bar = full + 8 * (j & 1);
         for (int x = 0; x < per; ++x, ++u) {
           // the unit's slot was last used by unit u - ring, of stage (u - ring) / per
-          for (; good && freed * per < u - ring + 1; ++freed)
+          for (; freed * per < u - ring + 1; ++freed) {
             good = mbar_wait_bounded_sleep(done + (n1 > freed ? 16 : 0) + 8 * (freed & 1),
                                            (uint32_t)((freed >> 1) & 1), p.wait_ns);
+            if (!good) break;
+          }
           if (!good) break;
           const int slot = u % ring, tok = tile.k0 + j * kTokens + (keys ? 0 : x * (kTokens / 2));
           if (x == 0) mbar_arrive_expect_tx(bar, (uint32_t)(keys ? L::KB * L::BOX : 2 * L::VUNIT));
@@ -206,9 +208,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         set_status(p.status, PA_DEV_TIMEOUT);
         *flag = 1;
       }
-      // copies in flight land before the CTA exits
+      // copies in flight land before the CTA exits: those of every stage that is not
+      // known to be free, in order, since a barrier's parity tells a stage only from
+      // the next one on the same barrier
       if (keys) mbar_wait_bounded_sleep(sb + L::Q_FULL, 0u, kDrainWaitNs);
-      for (int i = j < 2 ? 0 : j - 2; i < j; ++i)
+      for (int i = freed; i < j; ++i)
         mbar_wait_bounded_sleep(full + 8 * (i & 1), (uint32_t)((i >> 1) & 1), kDrainWaitNs);
     }
     __syncwarp();

@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kSoloThreads, 1)
     // Stages are counted over all segments: stage c uses buffer c & 1 for the
     // (c >> 1)-th time.
     int c = 0, qc = 0;
+    int issued = 0;  // groups of stage c whose copies are under way
     bool good = true;
     const uint64_t once = l2_evict_first_policy();
     const int box = p.page_size < 64 ? p.page_size : 64;  // tokens of one copy
@@ -196,8 +197,10 @@ __global__ void __launch_bounds__(kSoloThreads, 1)
             for (int b = 4 * g; b < (g ? 9 : 4); ++b)
               tma_load_box(kb + b * L::BOX + lane * box * 128, &p.pages_map, b * 64, row, page, full, once);
           __syncwarp();
+          issued = g + 1;
         }
-        if (good && clear) {  // the rest of the last 16 tokens, and the tokens of bad pages
+        if (!good) break;
+        if (clear) {  // the rest of the last 16 tokens, and the tokens of bad pages
           for (int g = 0; g < 2 && good; ++g)
             good = tc5::warp_wait(sb + L::K_FULL + 16 * buf + 8 * g, (uint32_t)((c >> 1) & 1), p.wait_ns);
           if (!good) break;
@@ -214,16 +217,19 @@ __global__ void __launch_bounds__(kSoloThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(sb + L::CLEARED + 8 * buf);
         }
+        issued = 0;
       }
     }
     if (!good && lane == 0) set_status(p.status, PA_DEV_TIMEOUT);
-    // copies in flight land before the CTA ends
-    for (int u = c < 2 ? 0 : c - 2; u < c; ++u)
-      for (int g = 0; g < 2; ++g)
+    // copies in flight land before the CTA ends: each group's last use of stage c's
+    // buffer, where stage c itself was begun if the warp gave up, and stage c - 1
+    for (int g = 0; g < 2; ++g) {
+      const int u = c - (g < issued ? 0 : 2);
+      if (u >= 0)
         tc5::warp_wait(sb + L::K_FULL + 16 * (u & 1) + 8 * g, (uint32_t)((u >> 1) & 1), kDrainWaitNs);
-    if (!good)  // one stage more may have been begun
-      for (int g = 0; g < 2; ++g)
-        tc5::warp_wait(sb + L::K_FULL + 16 * (c & 1) + 8 * g, (uint32_t)((c >> 1) & 1), kDrainWaitNs);
+      if (c > 0)
+        tc5::warp_wait(sb + L::K_FULL + 16 * ((c - 1) & 1) + 8 * g, (uint32_t)(((c - 1) >> 1) & 1), kDrainWaitNs);
+    }
     if (qc > 0) tc5::warp_wait(sb + L::Q_FULL, (uint32_t)((qc - 1) & 1), kDrainWaitNs);
   } else if (warp == 4) {
     // ================= MMAs (one thread) =================

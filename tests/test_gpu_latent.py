@@ -597,3 +597,24 @@ def test_pair_call_that_takes_longer_than_a_drain():
         want = [w @ z[:, :LATENT], w @ z[:, :LATENT].abs(), (x.abs() @ z.abs().T * 0.07).amax(1)]
         assert_latent_close(outs[0][b].double().cpu().numpy(), [y.cpu().numpy() for y in want], n,
                             "bf16", f"sequence {b}")
+
+
+@all_kernels
+def test_absorbed_under_any_wait_limit(rows):
+    """Wait limits from none to longer than the call, ranges of several pieces with
+    rows to clear: every row is as it was or right, a row that was left has its
+    status, and the next call with the default limit is right."""
+    lens, qs = [900, 77, 1500, 30, 333], [1, 2, 1, 1, 3]
+    c = Case(lens, qs, heads=16, seed=33, poison=True)
+    want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), lens, qs, c.scale)
+    for limit in (1, 300, 1000, 2000, 3000, 5000, 8000, 20000, 0):
+        d = Device(c, rows_per_tile=rows, num_sms=4, wait_limit_ns=limit)
+        out = torch.full((c.T, 16, LATENT), 7.0, dtype=DT["fp16"], device="cuda")
+        d.attention(out)
+        status = d.done()
+        got = out.double().cpu().numpy()
+        left = (got == 7).all(axis=-1)
+        assert status == (binding.PA_DEV_TIMEOUT if left.any() else status) and status in (0, 8)
+        assert limit or (status == 0 and not left.any())
+        if not left.all():
+            assert_latent_close(got[~left], tuple(x[~left] for x in want), 1500, "fp16", f"{limit} ns")

@@ -484,3 +484,56 @@ def test_a_flag_that_others_may_set_is_read_by_a_vote():
     src = kernel_source("latent_prefill.cu")
     reads = [src[max(0, m.start() - 20):m.end()] for m in re.finditer(r"\*flag == 0", src)]
     assert reads and all("__all_sync(kFull, *flag == 0" in r for r in reads), reads
+
+
+def drains_cover_what_is_under_way(full, first, ring, seed):
+    """Model of a copy warp that gives up: `full` barriers hold a count of finished
+    phases and answer a parity test as an mbarrier does, copies land at random
+    times.  first(issued, stages) names the stages the warp's last waits go
+    through, in order.  True if nothing is under way after them."""
+    rng = np.random.default_rng(seed)
+    stages = int(rng.integers(1, 9))
+    land = rng.exponential(1.0, stages) + np.arange(stages) * rng.choice([0.0, 0.5])
+    freed, issued = 0, 0
+    for j in range(stages):
+        while freed < j - ring + 1:
+            if rng.random() < 0.3 or not (land[freed] <= rng.uniform(0, 3)):
+                break          # the wait gave up, wherever that stage stands
+            freed += 1
+        if freed < j - ring + 1:
+            break
+        issued += 1
+    now = 0.0
+    done = [land[i] if i < issued else np.inf for i in range(stages + 2)]
+    for i in range(freed):
+        done[i] = 0.0          # known to be read
+
+    def phases(bar, t):        # finished phases of a barrier, in the order of its uses
+        n = 0
+        for i in range(bar, stages + 2, full):
+            if done[i] > t:
+                break
+            n += 1
+        return n
+    for i in first(freed, issued):
+        bar, use = i % full, i // full
+        times = [now, *sorted(x for x in done if now < x < np.inf)]
+        t = next((t for t in times if (phases(bar, t) & 1) != (use & 1)), now)
+        now = max(now, t)
+    return all(x <= now for x in done[:issued])
+
+
+def test_last_waits_of_the_copy_warps():
+    """A barrier's parity cannot tell a use from the one two before it, so a warp
+    that gave up waits for the uses that are under way in order, from the first one
+    not known to be read; waiting for the last two stages only may wait for
+    nothing."""
+    assert all(drains_cover_what_is_under_way(2, lambda freed, issued: range(freed, issued), 2, s)
+               for s in range(3000))
+    assert not all(drains_cover_what_is_under_way(
+        2, lambda freed, issued: range(max(0, issued - 1), issued + 1), 2, s) for s in range(3000))
+    prefill, solo, pair = (kernel_source(f"latent_{x}.cu") for x in ("prefill", "solo", "pair"))
+    assert "for (int i = freed; i < j; ++i) mbar_wait_bounded_sleep(full + 8 * (i & 1)" in prefill
+    assert "for (; freed * per < u - ring + 1; ++freed) { good = " in prefill     # exact when it gave up
+    assert "const int u = c - (g < issued ? 0 : 2);" in solo and "if (!good) break; if (clear)" in solo
+    assert "const int u = c - (g < issued ? 0 : 1);" in pair and "if (!good) break; issued = 0;" in pair
