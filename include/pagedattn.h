@@ -612,7 +612,11 @@ pa_status_t pa_latent_plan(const pa_latent_shape_t* shape, const int32_t* seq_le
 void pa_latent_plan_free(pa_latent_plan_t* plan);
 
 /* Copy the plan into the head of a device workspace of at least
- * plan->workspace_bytes (16-byte aligned), asynchronously on stream. */
+ * plan->workspace_bytes (16-byte aligned), asynchronously on stream.  host_blob
+ * is read when the copy runs: free the plan only after that.  An upload that is
+ * captured in a CUDA graph reads it at every replay, so the plan has to outlive
+ * the graph; a graph that leaves the upload out and is replayed behind one
+ * follows any plan of the same structure instead. */
 pa_status_t pa_latent_plan_upload(const pa_latent_plan_t* plan, void* workspace,
                                   size_t workspace_bytes, void* stream);
 

@@ -677,6 +677,8 @@ class LatentPlan:
     def free(self):
         if _lib is not None and getattr(self, "c", None) is not None and self.c.host_blob:
             _lib.pa_latent_plan_free(ctypes.byref(self.c))
+        if self in _captured_plans:
+            _captured_plans.remove(self)
 
     def __del__(self):
         try:
@@ -747,9 +749,24 @@ def _latent_status(status, stream):
     return [_dev_ptr(status, torch.int32, "status"), _stream(stream)]
 
 
-def latent_upload(plan: LatentPlan, workspace, stream=None):
-    """pa_latent_plan_upload."""
+# Plans whose upload was captured in a graph: each replay reads their host copy.
+_captured_plans: list = []
+
+
+def _capturing(stream) -> bool:
     torch = _torch()
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def latent_upload(plan: LatentPlan, workspace, stream=None):
+    """pa_latent_plan_upload.  A plan whose upload is captured in a graph is kept
+    until its free() is called: every replay reads its host copy."""
+    torch = _torch()
+    if _capturing(stream) and plan not in _captured_plans:
+        _captured_plans.append(plan)
     _check("pa_latent_plan_upload", load().pa_latent_plan_upload(
         ctypes.byref(plan.c), _latent_ptr(workspace, torch.uint8, workspace.shape, "workspace"),
         workspace.numel(), _stream(stream)))

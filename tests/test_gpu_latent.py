@@ -618,3 +618,31 @@ def test_absorbed_under_any_wait_limit(rows):
         assert limit or (status == 0 and not left.any())
         if not left.all():
             assert_latent_close(got[~left], tuple(x[~left] for x in want), 1500, "fp16", f"{limit} ns")
+
+
+def test_captured_upload_outlives_its_plan_object():
+    """A graph of upload, append and attention, replayed after the program has
+    dropped the plan and made others: the workspace holds the plan again."""
+    c = Case([500, 90], [1, 1], heads=16, seed=34)
+    d = Device(c)
+    out = d.attention()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        binding.latent_upload(d.plan, d.ws)
+        d.append()
+        d.attention(out)
+    kept = d.plan
+    d.plan = None
+    del kept
+    others = [binding.LatentPlan(d.shape, [9 + i, 400], [1, 1], 152) for i in range(50)]
+    for _ in range(2):
+        out.fill_(float("nan"))
+        d.ws.zero_()
+        torch.cuda.synchronize()   # calls may read the plan before the kernel ahead has ended
+        g.replay()
+        assert d.done() == 0
+        pool = oracle.latent_append(f64(c.pages), f64(c.c_new), f64(c.r_new), c.table.numpy(), c.lens, c.qs)
+        want = oracle.latent_attention(f64(c.q), pool, c.table.numpy(), c.lens, c.qs, c.scale)
+        assert_latent_close(out.double().cpu().numpy(), want, 500, "fp16")
+    assert len(others) == 50

@@ -5,10 +5,12 @@ planner's work lists, the oracle against its own definition, and every refusal
 from __future__ import annotations
 
 import ctypes
+import gc
 import os
 import re
 import shutil
 import subprocess
+import weakref
 
 import numpy as np
 import pytest
@@ -537,3 +539,35 @@ def test_last_waits_of_the_copy_warps():
     assert "for (; freed * per < u - ring + 1; ++freed) { good = " in prefill     # exact when it gave up
     assert "const int u = c - (g < issued ? 0 : 2);" in solo and "if (!good) break; if (clear)" in solo
     assert "const int u = c - (g < issued ? 0 : 1);" in pair and "if (!good) break; issued = 0;" in pair
+
+
+def test_a_captured_upload_keeps_its_plan(lib, monkeypatch):
+    """A graph's replays read the plan's host copy, so the binding keeps a plan
+    whose upload was captured, until free(); others go with their last
+    reference."""
+    torch = pytest.importorskip("torch")
+    seen = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return getattr(lib, name)
+
+        def pa_latent_plan_upload(self, plan, workspace, n, stream):
+            seen.append(n)
+            return 0
+    monkeypatch.setattr(binding, "load", lambda: Lib())
+    monkeypatch.setattr(binding, "_latent_ptr", lambda t, dtype, size, name: PTR)
+    monkeypatch.setattr(binding, "_stream", lambda stream=None: None)
+    ws = torch.zeros(64, dtype=torch.uint8)
+    for capturing in (False, True):
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+        plan = binding.LatentPlan(shape(2), [5, 3], [1, 3], 152)
+        ref = weakref.ref(plan)
+        binding.latent_upload(plan, ws)
+        binding.latent_upload(plan, ws)
+        del plan
+        gc.collect()
+        assert (ref() is not None) == capturing
+    ref().free()
+    gc.collect()
+    assert ref() is None and seen == [64] * 4
