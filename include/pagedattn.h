@@ -535,7 +535,8 @@ pa_status_t pa_prefill_attention(const pa_shape_t* shape, const pa_prefill_plan_
  *    multiplies them into k = W_h c and v = U_h c, and
  *        out[r][h] = sum_t softmax_t(scale * (q_nope . k_th + q_rope . r_t)) v_th.
  * The projections are the caller's; scale is that of the expanded form in
- * both, normally 1/sqrt(head_dim + 64).
+ * both, normally 1/sqrt(head_dim + 64); it has to be positive and stay finite in
+ * fp32 times log2(e).
  *
  * As in the multi-token calls, sequence b has seq_lens[b] tokens, the newest
  * q_lens[b] of which are this step's queries, packed by sequence: query i

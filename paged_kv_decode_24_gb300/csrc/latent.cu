@@ -180,6 +180,9 @@ pa_status_t check_latent_call(const pa_latent_shape_t* s, const pa_latent_plan_t
   return PA_OK;
 }
 
+// The scale of scores in log2 units; infinite where it leaves fp32.
+float log2_scale(float scale) { return (float)((double)scale * 1.4426950408889634); }
+
 // Strides in elements: multiples of 16 bytes below 2^40 bytes.
 bool stride_ok(int64_t stride, int width) {
   return stride >= width && stride % 8 == 0 && stride < (int64_t)1 << 39;
@@ -279,7 +282,8 @@ extern "C" pa_status_t pa_latent_attention(const pa_latent_shape_t* shape,
   if (!aligned(q, 16) || !aligned(pages, 16) || !aligned(out, 16) || !aligned(block_table, 4) ||
       !aligned(dev_status, 4))
     return PA_ERR_INVALID_ARG;
-  if (!isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
+  const float qscale = log2_scale(scale);
+  if (!(scale > 0.f) || !isfinite(qscale)) return PA_ERR_INVALID_ARG;
   if (plan->num_ranges < 1 || plan->num_segments < plan->num_ranges) return PA_ERR_PLAN;
   LatentParams p{};
   const LatentLayout l = latent_layout(shape->batch, plan->form, plan->rows_per_tile,
@@ -297,7 +301,7 @@ extern "C" pa_status_t pa_latent_attention(const pa_latent_shape_t* shape,
   p.part_o = reinterpret_cast<float*>(ws + l.o);
   p.status = dev_status;
   p.wait_ns = wait_limit_or_default(plan->wait_limit_ns);
-  p.qscale = (float)((double)scale * 1.4426950408889634);  // log2(e)
+  p.qscale = qscale;
   p.batch = shape->batch;
   p.heads = shape->num_heads;
   p.max_pages = shape->max_pages_per_seq;
@@ -333,7 +337,8 @@ extern "C" pa_status_t pa_latent_prefill(const pa_latent_shape_t* shape,
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(k_rope, 16) || !aligned(v, 16) ||
       !aligned(out, 16) || !aligned(dev_status, 4))
     return PA_ERR_INVALID_ARG;
-  if (!isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
+  const float qscale = log2_scale(scale);
+  if (!(scale > 0.f) || !isfinite(qscale)) return PA_ERR_INVALID_ARG;
   if (!planes_ok(k_token_stride, k_head_stride, plan->total_k, shape->num_heads, shape->head_dim) ||
       !planes_ok(v_token_stride, v_head_stride, plan->total_k, shape->num_heads, shape->head_dim) ||
       !stride_ok(kr_stride, kRope))
@@ -356,7 +361,7 @@ extern "C" pa_status_t pa_latent_prefill(const pa_latent_shape_t* shape,
   p.v_token = v_token_stride;
   p.v_head = v_head_stride;
   p.wait_ns = wait_limit_or_default(plan->wait_limit_ns);
-  p.qscale = (float)((double)scale * 1.4426950408889634);  // log2(e)
+  p.qscale = qscale;
   p.batch = shape->batch;
   p.heads = shape->num_heads;
   p.num_tiles = plan->num_ranges;

@@ -571,3 +571,11 @@ def test_a_captured_upload_keeps_its_plan(lib, monkeypatch):
     ref().free()
     gc.collect()
     assert ref() is None and seen == [64] * 4
+
+
+def test_a_scale_that_leaves_fp32_in_log2_units_is_refused(lib):
+    """The kernels hold scale x log2(e): from 3.4028e38 / 1.4427 on that is
+    infinite, and 0 times infinity would turn scores of zero into NaN."""
+    a, e = Call(lib), Call(lib, "expanded")
+    for scale in (2.36e38, 3e38, 3.4e38, float("-inf")):
+        assert a.attention(scale=scale) == INVALID and e.prefill(scale=scale) == INVALID
