@@ -205,7 +205,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // whose own copy warps announce the bytes of both.
     const bool keys = warp == 5;
     int c = 0, qc = 0;
-    int issued = 0;  // groups of stage c whose copies are under way
+    int issued = 0;  // after giving up: groups of stage c whose copies are under way
     bool good = true;
     const uint64_t once = l2_evict_first_policy(), keep = tc5::l2_evict_normal_policy();
     const int box = p.page_size < 64 ? p.page_size : 64;  // tokens of one copy
@@ -250,7 +250,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int valid = min(kPairTokens, s.tok1 - s.tok0 - j * kPairTokens);
         for (int g = 0; g < groups; ++g) {
           good = c == 0 || wait_free(g, c - 1, p.wait_ns);
-          if (!good) break;
+          if (!good) {
+            issued = g;
+            break;
+          }
           // One lane a copy
           if (keys) {  // boxes of the CTA's half of the tokens
             if (rank == 0 && lane == 0) {
@@ -264,7 +267,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               for (int b = L::BPG * g; b < L::BPG * (g + 1); ++b)
                 tma_load_3d_pair(sb + L::K + b * L::KBOX + u * box * 128, &p.pages_map, b * 64, row, page,
                                  full0 + 8 * g, keep);
-            issued = g + 1;
           } else {     // four boxes, the CTA's half of the values, of 64 tokens
             const unsigned mask = ((1u << per) - 1u) << (g * per);
             // rows to clear: the second CTA's copies complete on its own barrier
@@ -285,7 +287,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               for (int b = 0; b < 4; ++b)
                 tma_load_3d_pair(sb + L::V + g * L::VGROUP + b * L::VBOX + u * box * 128, &p.pages_map,
                                  ((b >> 1) * 4 + rank * 2 + (b & 1)) * 64, row, page, bar, keep);
-            issued = g + 1;
             if (clear) {  // the rest of the last 16 tokens, and the tokens of bad pages
               const uint32_t landed = sb + (rank == 0 ? L::V_FULL : L::V_HERE) + 8 * g;
               const uint32_t parity = (uint32_t)((rank == 0 ? c : clears >> g) & 1);
@@ -293,6 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               clears ^= 1 << g;
               if (!good) {
                 tc5::warp_wait(landed, parity, kDrainWaitNs);
+                issued = g + 1;
                 break;
               }
               __syncwarp();
@@ -314,7 +316,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           __syncwarp();
         }
         if (!good) break;
-        issued = 0;
       }
     }
     if (good) {
@@ -482,8 +483,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             resc = m_run != -INFINITY;
             m_run = mx;
           }
-          const float nm = m_run == -INFINITY ? -INFINITY : kBias - m_run;  // no token yet: weights 0
-          const float2 qs2 = make_float2(p.qscale, p.qscale), nm2 = make_float2(nm, nm);
+          float nm = m_run == -INFINITY ? -INFINITY : kBias - m_run;  // no token yet: weights 0
+          float qs = p.qscale;
+          if (beyond_fused(m_run)) {
+            rounded_differences(sv, qs, m_run);
+            qs = 1.f;
+            if (m_run != -INFINITY) nm = kBias;
+          }
+          const float2 qs2 = make_float2(qs, qs), nm2 = make_float2(nm, nm);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           uint32_t pk[32];
 #pragma unroll

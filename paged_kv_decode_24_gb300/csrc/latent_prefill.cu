@@ -315,6 +315,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     constexpr float kBias = std::is_same<T, __half>::value ? 7.f : 0.f;
     float m_run = -INFINITY, l_run = 0.f;
     bool good = true;
+    bool beyond = false;  // some row of the warp has scores beyond the fused product's range
     for (int j = 0; j < nt; ++j) {
       good = __all_sync(kFull, mbar_wait_bounded_sleep(sb + L::S_DONE + 16 * t + 8 * (j & 1),
                                                        (uint32_t)((j >> 1) & 1), p.wait_ns));
@@ -335,48 +336,81 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       for (int c = 4; c < kTokens; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], sv[c]);
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.qscale;
       float al = 1.f;
-      bool resc = false;
+      bool resc = false, raised = false;
       if (mx > m_run + kLazyLog2) {
+        raised = true;
         al = ex2(m_run - mx);  // 0 when the row had no weight yet
         resc = m_run != -INFINITY;
         m_run = mx;
       }
       // S(j) was issued after P V(j - 1) was done, so O may be rescaled now
-      if (j > 0 && __any_sync(kFull, resc)) {
+      if (__any_sync(kFull, raised)) {
+        beyond = beyond_fused(m_run);
         const float f = resc ? al : 1.f;
-        __syncwarp();  // rows whose maximum rose have branched
+        if (j > 0) {
+          __syncwarp();  // rows whose maximum rose have branched
 #pragma unroll 2
-        for (int c = 0; c < D; c += 16) {
-          float ov[16];
-          tc5::ld16(t_o + (uint32_t)c, ov);
-          tc5::wait_ld();
+          for (int c = 0; c < D; c += 16) {
+            float ov[16];
+            tc5::ld16(t_o + (uint32_t)c, ov);
+            tc5::wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) ov[i] *= f;
-          tc5::st16(t_o + (uint32_t)c, ov);
+            for (int i = 0; i < 16; ++i) ov[i] *= f;
+            tc5::st16(t_o + (uint32_t)c, ov);
+          }
         }
       }
       const float nm = m_run == -INFINITY ? -INFINITY : kBias - m_run;  // no token yet: weights 0
       const float2 qs2 = make_float2(p.qscale, p.qscale), nm2 = make_float2(nm, nm);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        __syncwarp();  // lanes may have branched, and what follows is for a whole warp
-#pragma unroll
-        for (int c0 = 64 * h; c0 < 64 * h + 64; c0 += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float2 x = ffma2(make_float2(sv[c0 + c], sv[c0 + c + 1]), qs2, nm2);
-            const float2 w = make_float2(ex2(x.x), ex2(x.y));
-            sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], w);
-            pk[c >> 1] = Elem<T>::from_f2(w.x, w.y);
-          }
-          tc5::st16u(t_s + (uint32_t)(c0 / 2), pk);
-        }
+      auto hand_over = [&](int h) {  // half h of the weights is written
         tc5::wait_st();
         tc5::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(sb + L::P_READY + 16 * t + 8 * h);
+      };
+      if (!beyond) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          __syncwarp();  // lanes may have branched, and what follows is for a whole warp
+#pragma unroll
+          for (int c0 = 64 * h; c0 < 64 * h + 64; c0 += 32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const float2 x = ffma2(make_float2(sv[c0 + c], sv[c0 + c + 1]), qs2, nm2);
+              const float2 w = make_float2(ex2(x.x), ex2(x.y));
+              sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], w);
+              pk[c >> 1] = Elem<T>::from_f2(w.x, w.y);
+            }
+            tc5::st16u(t_s + (uint32_t)(c0 / 2), pk);
+          }
+          hand_over(h);
+        }
+      } else {  // from the scores in tensor memory again, which P has not reached yet
+#pragma unroll 1
+        for (int c0 = 0; c0 < kTokens; c0 += 32) {
+          uint32_t pk[16];
+          const int seen = qpos - j * kTokens - c0;
+#pragma unroll
+          for (int b = 0; b < 32; b += 16) {
+            __syncwarp();
+            float x[16];
+            tc5::ld16(t_s + (uint32_t)(c0 + b), x);
+            tc5::wait_ld();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) x[c] = b + c <= seen ? x[c] : -INFINITY;
+            rounded_differences(x, p.qscale, m_run);
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              const float2 w = make_float2(ex2(x[c] + kBias), ex2(x[c + 1] + kBias));
+              sum[0] = fadd2(sum[0], w);
+              pk[(b + c) >> 1] = Elem<T>::from_f2(w.x, w.y);
+            }
+          }
+          tc5::st16u(t_s + (uint32_t)(c0 / 2), pk);
+          if (c0 % 64 == 32) hand_over(c0 / 64);
+        }
       }
       const float2 s2 = fadd2(sum[0], sum[1]);
       l_run = l_run * al + (s2.x + s2.y);

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kSoloThreads, 1)
     // Stages are counted over all segments: stage c uses buffer c & 1 for the
     // (c >> 1)-th time.
     int c = 0, qc = 0;
-    int issued = 0;  // groups of stage c whose copies are under way
+    int issued = 0;  // after giving up: groups of stage c whose copies are under way
     bool good = true;
     const uint64_t once = l2_evict_first_policy();
     const int box = p.page_size < 64 ? p.page_size : 64;  // tokens of one copy
@@ -183,7 +183,10 @@ __global__ void __launch_bounds__(kSoloThreads, 1)
         for (int g = 0; g < 2; ++g) {
           good = c < 2 || tc5::warp_wait(sb + (g ? L::PV_DONE : L::K_FREE) + 8 * buf,
                                          (uint32_t)(((c >> 1) - 1) & 1), p.wait_ns);
-          if (!good) break;
+          if (!good) {
+            issued = g;
+            break;
+          }
           const uint32_t full = sb + L::K_FULL + 16 * buf + 8 * g;
           if (lane == 0) {
             const uint32_t bytes = (uint32_t)(__popc(have) * box * 128 * (g ? 5 : 4));
@@ -197,13 +200,15 @@ __global__ void __launch_bounds__(kSoloThreads, 1)
             for (int b = 4 * g; b < (g ? 9 : 4); ++b)
               tma_load_box(kb + b * L::BOX + lane * box * 128, &p.pages_map, b * 64, row, page, full, once);
           __syncwarp();
-          issued = g + 1;
         }
         if (!good) break;
         if (clear) {  // the rest of the last 16 tokens, and the tokens of bad pages
           for (int g = 0; g < 2 && good; ++g)
             good = tc5::warp_wait(sb + L::K_FULL + 16 * buf + 8 * g, (uint32_t)((c >> 1) & 1), p.wait_ns);
-          if (!good) break;
+          if (!good) {
+            issued = 2;
+            break;
+          }
           __syncwarp();
           for (int at = 0; at < valid; at += kLatentBlock) {
             const int from = missing >> (at / box) & 1 ? 0 : valid - at, rows = kLatentBlock - from;
@@ -217,7 +222,6 @@ __global__ void __launch_bounds__(kSoloThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(sb + L::CLEARED + 8 * buf);
         }
-        issued = 0;
       }
     }
     if (!good && lane == 0) set_status(p.status, PA_DEV_TIMEOUT);
@@ -384,8 +388,14 @@ __global__ void __launch_bounds__(kSoloThreads, 1)
             resc = m_run != -INFINITY;
             m_run = mx;
           }
-          const float nm = m_run == -INFINITY ? -INFINITY : kBias - m_run;  // no token yet: weights 0
-          const float2 qs2 = make_float2(p.qscale, p.qscale), nm2 = make_float2(nm, nm);
+          float nm = m_run == -INFINITY ? -INFINITY : kBias - m_run;  // no token yet: weights 0
+          float qs = p.qscale;
+          if (beyond_fused(m_run)) {
+            rounded_differences(sv, qs, m_run);
+            qs = 1.f;
+            if (m_run != -INFINITY) nm = kBias;
+          }
+          const float2 qs2 = make_float2(qs, qs), nm2 = make_float2(nm, nm);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           uint32_t pk[16];
 #pragma unroll

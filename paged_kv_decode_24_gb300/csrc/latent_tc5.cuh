@@ -88,6 +88,26 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
 
 }  // namespace tc5
 
+// Weights are 2^(s qscale - m) in one fused multiply-add, with m the rounded
+// product of a maximal score.  The fused product is exact, so the exponent keeps
+// what m lost in its rounding, up to half of m's last place, the same for the
+// whole row: no error of the weights until it reaches many units, beyond
+// |m| = 2^24, where it would overflow or empty them.  A warp that has a row
+// beyond 2^23 therefore takes the product rounded as m was: its scores become
+// s qscale - m, to be used with a factor of 1 and m = 0.
+constexpr float kFusedLog2 = 8388608.f;
+
+__device__ __forceinline__ bool beyond_fused(float m) {
+  return __any_sync(kFull, fabsf(m) > kFusedLog2 && m != -INFINITY) != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void rounded_differences(float (&s)[N], float qscale, float m) {
+  const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] = __fsub_rn(__fmul_rn(s[i], qscale), ref);
+}
+
 // The page of token tok, -1 from `end` on.  A volatile load, which stays where
 // it is written: a stage ahead of its use.
 __device__ __forceinline__ int table_entry(const int32_t* table, int page_size, int tok, int end) {

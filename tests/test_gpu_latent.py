@@ -646,3 +646,38 @@ def test_captured_upload_outlives_its_plan_object():
         want = oracle.latent_attention(f64(c.q), pool, c.table.numpy(), c.lens, c.qs, c.scale)
         assert_latent_close(out.double().cpu().numpy(), want, 500, "fp16")
     assert len(others) == 50
+
+
+@pytest.mark.parametrize("dtype,power", [("bf16", 8), ("bf16", 15), ("bf16", 23), ("fp16", 12)])
+@pytest.mark.parametrize("splits", [0, 2])
+def test_scores_far_beyond_the_exponential(dtype, power, splits):
+    """Scores of 10^8 to 10^18.  Inputs are whole numbers up to 7 times a power of
+    two, so that scores are exact in fp32 and differ by at least 2^16 x 1.7: where
+    one token has the largest, it has all the weight.  Weight and result are
+    each rounded at most once (half a step each, 2 u in all), and nothing is lost to
+    infinity or zero."""
+    c = Case([300, 70, 520], [3, 1, 20], heads=7, dtype=dtype, seed=40, scale=1.7)
+    g = torch.Generator().manual_seed(41)
+    for name in ("q", "pages", "qx", "kv", "rows"):
+        t = getattr(c, name)
+        setattr(c, name, (torch.randint(-7, 8, t.shape, generator=g) * 2.0**power).to(t.dtype))
+    u = 2 * torch.finfo(DT[dtype]).eps / 2
+
+    def check(out, want, what):
+        one = (want[1] == np.abs(want[0])).all(axis=-1)
+        assert one.mean() > 0.8
+        got = out.double().cpu().numpy()
+        assert np.all(np.isfinite(got)), what
+        assert np.all(np.abs(got - want[0])[one] <= u * (1 + u) * np.abs(want[0])[one]), what
+    want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), c.lens, c.qs, c.scale)
+    for rows in (16, 64, 128):
+        d = Device(c, rows_per_tile=rows, forced_splits=splits)
+        out = d.attention()
+        assert d.done() == 0
+        check(out, want, f"rows {rows}")
+    want = oracle.latent_prefill(f64(c.qx), f64(c.k), f64(c.rows[:, LATENT:]), f64(c.v), c.lens, c.qs, c.scale)
+    for rows in (128, 256):
+        d = Device(c, form="expanded", rows_per_tile=rows)
+        out = d.prefill()
+        assert d.done() == 0
+        check(out, want, f"tiles {rows}")
