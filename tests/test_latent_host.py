@@ -538,7 +538,7 @@ def test_last_waits_of_the_copy_warps():
     assert "for (int i = freed; i < j; ++i) mbar_wait_bounded_sleep(full + 8 * (i & 1)" in prefill
     assert "for (; freed * per < u - ring + 1; ++freed) { good = " in prefill     # exact when it gave up
     assert "const int u = c - (g < issued ? 0 : 2);" in solo and "if (!good) { issued = g; break; }" in solo
-    assert "const int u = c - (g < issued ? 0 : 1);" in pair and "if (!good) { issued = g; break; }" in pair
+    assert "const int issued = g + (begun ? 1 : 0);" in pair and "c - 1 - (x < issued ? 0 : 1);" in pair
 
 
 def test_a_captured_upload_keeps_its_plan(lib, monkeypatch):
