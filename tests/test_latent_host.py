@@ -579,3 +579,36 @@ def test_a_scale_that_leaves_fp32_in_log2_units_is_refused(lib):
     a, e = Call(lib), Call(lib, "expanded")
     for scale in (2.36e38, 3e38, 3.4e38, float("-inf")):
         assert a.attention(scale=scale) == INVALID and e.prefill(scale=scale) == INVALID
+
+
+@pytest.mark.parametrize("rows", [0, 128, 256])
+@pytest.mark.parametrize("case", BATCHES, ids=lambda c: f"B{len(c[0])}_H{c[2]}_L{max(c[0])}")
+def test_expanded_tiles_are_whole_but_for_the_last(lib, case, rows):
+    """Each sequence's tiles have exactly the plan's tile size, the last one the
+    rest; the planner's own choice is one of the two sizes for the whole call."""
+    lens, qs, heads = case
+    p = binding.LatentPlan(shape(len(lens), heads, max_pages=3000), lens, qs, 152, form="expanded",
+                           rows_per_tile=rows)
+    tiles = parts(p)[3]
+    got = sorted((int(q0), int(h), int(n)) for h, n, q0 in tiles[:, :3].tolist())
+
+    def cut(size):
+        cu = [0, *np.cumsum(qs)]
+        return sorted((cu[b] + t, h, min(size, qs[b] - t)) for b in range(len(qs)) for t in range(0, qs[b], size)
+                      for h in range(heads))
+    assert got in ([cut(rows)] if rows else [cut(256), cut(128)])
+
+
+def test_absorbed_ranges_stay_within_two_stages_of_the_mean(lib):
+    """The bound of equal work, exactly: a range ends in a cut at most one stage, the
+    piece's fixed cost and the shortest piece (one stage) behind its share."""
+    rng = np.random.default_rng(7)
+    for heads, unit, fixed in ((16, 64, 1), (48, 64, 1), (128, 128, 2)):
+        for _ in range(20):
+            n = int(rng.integers(160, 400))
+            lens = rng.integers(200, 9000, n).tolist()
+            s = shape(n, heads, max_pages=1000)
+            _, _, _, ranges, seg, _ = parts(binding.LatentPlan(s, lens, [1] * n, 152))
+            cost = -(-(seg[:, 4] - seg[:, 3]) // unit) + fixed
+            per = np.add.reduceat(cost, ranges[:-1])
+            assert per.max() <= per.mean() + fixed + 2, (heads, per.max(), per.mean())
