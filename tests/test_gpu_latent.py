@@ -681,3 +681,113 @@ def test_scores_far_beyond_the_exponential(dtype, power, splits):
         out = d.prefill()
         assert d.done() == 0
         check(out, want, f"tiles {rows}")
+
+
+# batches whose ranges hold several pieces of several tiles, on few SMs
+MANY_PIECES = [
+    # lens, q_lens, heads, page, num_sms
+    ([500, 77, 0, 1300, 64, 257, 30, 900], [1] * 2 + [0] + [1] * 5, 16, 16, 4),
+    ([700, 128, 65, 1029], [3, 1, 2, 5], 20, 32, 2),              # tiles that begin inside a token
+    ([129, 1000, 15, 513, 384, 2000], [1, 2, 1, 1, 3, 1], 128, 64, 8),
+    ([63, 1, 190, 2, 64, 333, 128, 16, 127], [1] * 9, 48, 128, 2),   # one range, tails of every kind
+]
+
+
+@all_kernels
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("case", MANY_PIECES, ids=lambda c: f"B{len(c[0])}_H{c[2]}_S{c[3]}_sm{c[4]}")
+def test_ranges_of_many_pieces(case, dtype, rows):
+    """A CTA (or pair) works through pieces of several tiles in turn: queries,
+    accumulators, statistics and barriers are used again."""
+    lens, qs, heads, page, sms = case
+    c = Case(lens, qs, heads=heads, page=page, dtype=dtype, seed=seed_of(case), poison=True)
+    d = Device(c, num_sms=sms, rows_per_tile=rows)
+    assert d.plan.c.num_ranges <= sms and d.plan.c.num_segments >= 2 * d.plan.c.num_ranges
+    out = d.attention()
+    assert d.done() == 0
+    want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), lens, qs, c.scale)
+    assert_latent_close(out.double().cpu().numpy(), want, max(lens), dtype, str(case))
+    assert torch.equal(bits(d.attention()), bits(out))
+
+
+@all_kernels
+def test_ranges_of_many_pieces_with_bad_pages(rows):
+    """Rows to clear in some pieces of a range and not in others."""
+    lens, qs = [200, 70, 333, 48, 500, 90], [1, 2, 1, 1, 1, 1]
+    c = Case(lens, qs, heads=16, page=16, seed=35, poison=True)
+    bad = [(0, 3), (1, 0), (3, 0), (3, 1), (3, 2), (4, 31)]
+    for b, j in bad:
+        c.table[b, j] = -1 if j % 2 else c.num_pages
+    d = Device(c, num_sms=2, rows_per_tile=rows)
+    assert d.plan.c.num_segments >= 3 * d.plan.c.num_ranges
+    out = d.attention()
+    assert d.done() == binding.PA_DEV_BAD_PAGE
+    want = oracle.latent_attention(f64(c.q), f64(c.pages), c.table.numpy(), lens, qs, c.scale, bad_pages=bad)
+    assert_latent_close(out.double().cpu().numpy(), want, 500, "fp16")
+    assert torch.all(out[4] == 0)
+
+
+def test_a_long_prompt_and_a_long_context():
+    """Expanded attention over many stages: the rings turn often."""
+    c = Case([4100, 6001], [300, 129], heads=2, seed=36, dtype="bf16")
+    for rows in (128, 256):
+        d = Device(c, form="expanded", rows_per_tile=rows)
+        out = d.prefill()
+        assert d.done() == 0
+        want = oracle.latent_prefill(f64(c.qx), f64(c.k), f64(c.rows[:, LATENT:]), f64(c.v), c.lens, c.qs,
+                                     c.scale)
+        assert_latent_close(out.double().cpu().numpy(), want, 6001, "bf16")
+
+
+def test_binding_refuses_wrong_sizes_and_devices():
+    """Sizes, dense last dimensions and element types are checked for each tensor
+    before the library is called; nothing is written."""
+    c = Case([40, 9], [7, 9], heads=2, head_dim=64, seed=37)
+    a, e = Device(c), Device(c, form="expanded")
+    out, outx = torch.zeros(16, 2, LATENT, device="cuda").half(), torch.zeros(16, 2, 64, device="cuda").half()
+    rows = torch.zeros(49, ROW, device="cuda").half()
+    before = a.pages.clone()
+
+    def append(**kw):
+        x = {"c": a.c_new, "r": a.r_new, "pages": a.pages, "table": a.table, **kw}
+        binding.latent_append(a.shape, a.plan, x["c"], x["r"], x["pages"], x["table"], a.ws, a.status)
+
+    def attention(**kw):
+        x = {"q": a.q, "pages": a.pages, "table": a.table, "out": out, "ws": a.ws, **kw}
+        binding.latent_attention(a.shape, a.plan, x["q"], x["pages"], x["table"], 0.1, x["out"], x["ws"], a.status)
+
+    def prefill(**kw):
+        x = {"q": e.qx, "k": e.k, "r": e.k_rope, "v": e.v, "out": outx, **kw}
+        binding.latent_prefill(e.shape, e.plan, x["q"], x["k"], x["r"], x["v"], 0.1, x["out"], e.ws, e.status)
+
+    def gather(**kw):
+        x = {"rows": rows, **kw}
+        binding.latent_gather(a.shape, a.plan, a.pages, a.table, x["rows"], a.ws, a.status)
+
+    size, dense, element = "must have shape", "dense in its last|contiguous", "must be"
+    for call, kw, kind, what in [
+            (append, {"c": a.c_new[:-1]}, ValueError, size), (append, {"c": a.c_new[:, :-8]}, ValueError, size),
+            (append, {"r": a.r_new.float()}, TypeError, element),
+            (append, {"r": a.r_new.t().contiguous().t()}, ValueError, dense),
+            (append, {"table": a.table[:, :-1].contiguous()}, ValueError, size),
+            (append, {"table": a.table.long()}, TypeError, element),
+            (append, {"pages": a.pages[:-1]}, ValueError, size), (append, {"c": c.c_new}, TypeError, element),
+            (attention, {"q": a.q[:, :1].contiguous()}, ValueError, size),
+            (attention, {"q": a.q.transpose(0, 1).contiguous().transpose(0, 1)}, ValueError, dense),
+            (attention, {"out": out[:-1]}, ValueError, size), (attention, {"out": out.float()}, TypeError, element),
+            (attention, {"pages": a.pages[:, :, ::2]}, ValueError, dense),
+            (attention, {"ws": a.ws[:, None]}, ValueError, "one-dimensional"),
+            (gather, {"rows": rows[1:]}, ValueError, size), (gather, {"rows": rows.bfloat16()}, TypeError, element),
+            (prefill, {"k": e.k[:, :, :32]}, ValueError, size), (prefill, {"k": e.k[1:]}, ValueError, size),
+            (prefill, {"v": e.v[:, :1]}, ValueError, size),
+            (prefill, {"v": torch.cat([e.v, e.v], 2)[..., ::2]}, ValueError, dense),
+            (prefill, {"r": e.k_rope[:, :56]}, ValueError, size),
+            (prefill, {"q": e.qx[..., :-8]}, ValueError, dense), (prefill, {"out": outx[:, 0]}, ValueError, dense)]:
+        with pytest.raises(kind, match=what):
+            call(**kw)
+    for call, kw in [(append, {"c": a.c_new[:1].expand(16, -1)}), (prefill, {"k": e.k[:, :1].expand(-1, 2, -1)}),
+                     (attention, {"ws": a.ws[:-1]})]:
+        with pytest.raises(binding.PagedAttnError):    # broadcast strides, a workspace too small
+            call(**kw)
+    assert a.done() == 0 and e.done() == 0
+    assert torch.equal(bits(a.pages), bits(before)) and not out.any() and not outx.any() and not rows.any()
