@@ -643,8 +643,13 @@ pa_status_t pa_latent_gather(const pa_latent_shape_t* shape, const pa_latent_pla
                              const void* workspace, size_t workspace_bytes, int32_t* dev_status,
                              void* stream);
 
-/* Absorbed attention.  q: [T][H][576] dense; out: [T][H][512] dense.  fp32
- * accumulation and softmax.  Tokens of a page whose index is out of range
+/* Absorbed attention.  q: [T][H][576] dense; out: [T][H][512] dense.  Scores,
+ * softmax statistics, accumulation and partial results are fp32.  Each weight
+ * is rounded once to the element type before it multiplies the latents with
+ * tiles of 64 and 128 rows (the row's sum keeps the fp32 weights); tiles of 16
+ * rows hold it in two parts, to about twice the type's bits.  The planner takes
+ * the tile by the rows of the largest sequence; the option rows_per_tile fixes
+ * it.  Tokens of a page whose index is out of range
  * are left out and set PA_DEV_BAD_PAGE; a row left without any token gets
  * zeros.  The cached rows of a sequence's own tokens have to be finite (a
  * query's weight of a later token is 0, but its product may be formed); what
@@ -664,6 +669,8 @@ pa_status_t pa_latent_attention(const pa_latent_shape_t* shape, const pa_latent_
  * apart (the tail of pa_latent_gather's rows, kr_stride = 576).  Values
  * dense within a head; pointers 16-byte aligned; strides multiples of 8
  * elements that keep tokens and heads apart (either may be the outer one).
+ * Scores, statistics and accumulation are fp32, weights rounded once to the
+ * element type.
  * Weights of later tokens are 0, but their values are read up to the next
  * multiple of 128 tokens that some query sees: values of a sequence's own
  * tokens have to be finite.  Rows of other sequences may hold anything.
