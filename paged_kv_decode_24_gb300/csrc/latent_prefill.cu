@@ -36,12 +36,12 @@
 // may hold anything) become zeros before P V reads them.  Every wait is
 // bounded; a CTA that gave up writes nothing.
 //
-// Measured: a prompt of 8192 tokens with 32 heads of 128, 520 to 530 us, 1300 TFLOP/s
+// Measured: a prompt of 8192 tokens with 32 heads of 128, 515 to 535 us, 1300 TFLOP/s
 // of visible pairs (77 % of what cuBLAS sustains under the power cap); a stage
 // takes 2.05 us where few CTAs run, 2.3 on all SMs (clocks under the cap).  A
 // tile of 128 tokens or fewer takes 1.6 us a stage: nothing overlaps its
 // softmax.  (So whole tiles where there are enough of them, see the planner.)  Six chunks of 513 tokens behind up to 5700 with 16 heads of 128:
-// 157 us, a fifth of it the tiles of the 513th tokens, the rest uneven ends.
+// 161 us, a fifth of it the tiles of the 513th tokens, the rest uneven ends.
 #include <math.h>
 
 #include "latent_params.h"

@@ -26,9 +26,9 @@
 // cleared rows, bounded waits: as in latent_pair.cu.
 //
 // Measured, merge included: 64 sequences of 500 to 8001 tokens, 322 MB, with 32
-// heads 65.7 us (72 % of the copy bandwidth; 71.6 on pairs of SMs, 117 with
-// 16-row tiles), with 64 heads 72 us (77 on pairs).  21 sequences of 200 to 6003
-// tokens, three new tokens each, 20 heads: 29.8 us for 11.7 us of bytes: the
+// heads 66.9 us (71 % of the copy bandwidth; 71.6 on pairs of SMs, 117 with
+// 16-row tiles), with 64 heads 72.6 us (77 on pairs).  21 sequences of 200 to 6003
+// tokens, three new tokens each, 20 heads: 30.0 us for 11.7 us of bytes: the
 // start about 5, eight stages 12, a piece's output (128 KB of fp32 per CTA at
 // what one SM writes to L2) 3.5, the merge and its launch the rest.
 #include <math.h>
