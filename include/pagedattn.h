@@ -889,14 +889,13 @@ pa_status_t pa_diff_attention(const pa_shape_t* shape, const pa_diff_plan_t* pla
 /* The same of several new tokens of each sequence, causal: T rows packed as in
  * pa_prefill_attention, whose plan it takes (in the workspace; rows_per_tile
  * has to be 128).  q: [T][Hq][D], out: [T][H][2D].  Scores, statistics and
- * accumulation are fp32; weights keep about twice the element type's bits where a
- * tile of 128 rows (128 / G tokens) ends within the first 1024 tokens, and are
- * rounded once to it beyond.  Tokens of a page whose index is out of range are left out (PA_DEV_BAD_PAGE); a row left
- * without any token gets zeros.  Weights of later tokens of the sequence are
- * 0, but their products are formed: queries and the rows of a sequence's own
- * tokens have to be finite.  Rows that no sequence owns may hold anything.  Device-side
- * problems are reported as pa_prefill_attention's; the same bits on every
- * call. */
+ * accumulation are fp32; weights keep about twice the element type's bits.
+ * Tokens of a page whose index is out of range are left out (PA_DEV_BAD_PAGE);
+ * a row left without any token gets zeros.  Weights of later tokens of the
+ * sequence are 0, but their products are formed: queries and the rows of a
+ * sequence's own tokens have to be finite.  Rows that no sequence owns may hold
+ * anything.  Device-side problems are reported as pa_prefill_attention's; the
+ * same bits on every call. */
 pa_status_t pa_diff_prefill(const pa_shape_t* shape, const pa_prefill_plan_t* plan,
                             const pa_diff_t* diff, const void* q, const void* k_pages,
                             const void* v_pages, const int32_t* block_table,

@@ -8,10 +8,12 @@
 // With both maps' sums known, their difference is formed as one weight before
 // it meets the values.  That is as many operations as two products with the
 // values (12 D a head and visible pair: 4 D of scores twice, 4 D of values, with
-// values twice as wide as keys), but the weights are rounded once where they
-// are small differences of large ones, one accumulator of 2D columns is left of
-// two (with D = 128 two do not fit in tensor memory), and it is never
-// rescaled.  It costs every exponential twice.
+// values twice as wide as keys), but one weight is rounded where there were two,
+// one accumulator of 2D columns is left of two (with D = 128 two do not fit in
+// tensor memory), and it is never rescaled.  It costs every exponential twice.
+// A weight is kept in two parts of the element type, what rounding left of the
+// first being the second: rounded once, the outputs of long prompts were 1.35 to
+// 1.4 times as far from the 64-bit ones as those of fp32 weights.
 // The tiles are those of the multi-token plan, 128 rows (128 / G query tokens
 // times the G heads of a KV head), of which the plan lists two for each pair of
 // KV heads.  A CTA (one per SM) takes both as one:
@@ -34,20 +36,17 @@
 // Pass 2, 64 tokens at a time, B buffers:
 //   S_2(i), S_1(i) = q_k K_k(i)^T     D/16 MMAs each, M = 128, N = 64
 //   weights in registers, written over S_1(i)
-//   O += P(i) V(i)                    4 MMAs, N = 2D (twice that for weights in two
-//                                     parts: what rounding left of them, rounded too)
+//   O += P(i) V(i)                    8 MMAs, N = 2D: both parts of the weights
 //   S_2(i + B), then, once P V(i) is done, S_1(i + B)
 // Value rows past the tile's last visible token and of bad pages (which may
 // hold anything) become zeros before P V reads them.  Every wait is bounded; a
 // CTA that gave up writes nothing.
 //
-// Measured: a prompt of 8192 tokens with 32 query heads of 128 (16 heads), 577 us,
-// 1430 TFLOP/s of visible pairs (1899 is what cuBLAS reaches in a burst, 1705 under
-// the power cap); there the tensor cores and the thread that feeds them
-// bound it, in pass 2 with 64-token score tiles that read q from shared memory at two
-// thirds of their rate.  4100 tokens, 32 query heads of 64: 143 us, 723 TFLOP/s: a
-// stage of 64 tokens takes 1850 clocks for 1024 of exponentials (32 a clock and SM,
-// each taken twice), and the threads that issue are near their limits too.
+// Measured: a prompt of 8192 tokens with 32 query heads of 128 (16 heads), 762 us, 1080
+// TFLOP/s of the formula's operations (12 D a visible pair; the second parts of the
+// weights are 4 D more: 1440 TFLOP/s with them, of the 1705 that a library product
+// reaches under the power cap).  4100 tokens, 32 query heads of 64: 152 us, 679 TFLOP/s.  Weights rounded
+// once took 620 and 143 us.
 #include <math.h>
 
 #include "diff.h"
@@ -69,10 +68,6 @@ constexpr float kFoldedLog2 = 1024.f;
 // reference stays: weights are then below it, and two of them times the factor of
 // fp16 (2^7) below that type's largest value.
 constexpr float kLateSum = 128.f;
-// Tiles that see at most this many tokens keep the weights in two parts, others
-// round them once.  A row of many tokens averages the roundings, to as much as that
-// of its output; one of few tokens may meet a single large one.
-constexpr int kTwoParts = 1024;
 
 template <int D>
 struct DPLayout {
@@ -308,7 +303,6 @@ __global__ void __launch_bounds__(kDiffPrefillThreads, 1)
   const int n = (span + KT - 1) / KT;                   // stages (0: nothing to do)
   const int parts = (span + kTokens - 1) / kTokens;     // buffers of pass 2
   const int npages = (span + kPageSize - 1) / kPageSize;
-  const bool two = span <= kTwoParts;  // parts of the weights
 
   if (warp >= kRowWarps + 2) {
     // ================= copies =================
@@ -573,12 +567,9 @@ __global__ void __launch_bounds__(kDiffPrefillThreads, 1)
           for (int k = 0; k < kTokens / kPageSize; ++k)
             tc5::mma1_tmem(tmem + L::O, t_p + column_of(k), tc5::desc_at(vb, k * L::VPAGE), idesc,
                            i > 0 || k > 0 ? 1u : 0u);
-          if (two) {
 #pragma unroll
-            for (int k = 0; k < kTokens / kPageSize; ++k)
-              tc5::mma1_tmem(tmem + L::O, t_p + column_of(k) + L::MINE / 2, tc5::desc_at(vb, k * L::VPAGE), idesc,
-                             1u);
-          }
+          for (int k = 0; k < kTokens / kPageSize; ++k)  // the second parts
+            tc5::mma1_tmem(tmem + L::O, t_p + column_of(k) + L::MINE / 2, tc5::desc_at(vb, k * L::VPAGE), idesc, 1u);
           tc5::commit(sb + L::PV_DONE + 8 * at);
           if (++part == L::PARTS) {
             part = 0;
@@ -861,16 +852,14 @@ __global__ void __launch_bounds__(kDiffPrefillThreads, 1)
           }
           __syncwarp();  // lanes may have branched, and what follows is for a whole warp
           st8u(columns + (uint32_t)(8 * half), w);
-          if (two) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const float2 hi = Elem<T>::to_f2(w[c]);
-              const float2 rest = unpack(fma2(pack(hi.x, hi.y), minus1, d[c]));  // exact
-              w[c] = Elem<T>::from_f2(rest.x, rest.y);
-            }
-            __syncwarp();
-            st8u(columns + (uint32_t)(L::MINE / 2 + 8 * half), w);
+          for (int c = 0; c < 8; ++c) {
+            const float2 hi = Elem<T>::to_f2(w[c]);
+            const float2 rest = unpack(fma2(pack(hi.x, hi.y), minus1, d[c]));  // exact
+            w[c] = Elem<T>::from_f2(rest.x, rest.y);
           }
+          __syncwarp();
+          st8u(columns + (uint32_t)(L::MINE / 2 + 8 * half), w);
         };
         load(0);
         __syncwarp();

@@ -5,9 +5,8 @@ Tolerance of an attention output.  u is half a step of the element type
 relative to the value (fp16 2^-11, bf16 2^-8).  A value before the norm,
 o = sum_t (P1[t] - lambda P2[t]) V[t], differs from the float64 one on the same
 16-bit inputs by
-  - the rounding of the weights, uw of each: uw = u where a kernel keeps the
-    weights in the element type (several tokens); where it keeps them in two
-    parts (one token), the second part leaves u^2 of each;
+  - the rounding of the weights, uw of each: kept in two parts, the second part
+    leaves u^2 of each (both calls); kept in the element type alone, it would be u;
   - fp32 arithmetic: a score is a sum of D products, each addition off by at most
     2^-23 of the sum A of their absolute values, so a weight is off by at most
     2 D 2^-23 A, relatively; a sum over L tokens adds L 2^-23; exponentials, their
