@@ -874,8 +874,9 @@ pa_status_t pa_diff_plan_upload(const pa_diff_plan_t* plan, void* workspace, siz
 
 /* Differential attention of one new token of every sequence over its
  * seq_lens[b] cached tokens (the new one included).  q: [B][Hq][D], out:
- * [B][H][2D].  Weights keep about twice the element type's bits.  Splits are
- * joined in a fixed order, the same bits on every call: by the last task of the
+ * [B][H][2D].  Weights keep about twice the element type's bits (fp16: those
+ * below 2^-18 of their row's largest are kept to 2^-40 of it).  Splits are joined
+ * in a fixed order, the same bits on every call: by the last task of the
  * (sequence, pair), or, where some sequence has more than 8, by a second kernel.
  * A sequence of length 0, or without a valid page, gets zeros.  Rows past a
  * sequence's end may hold anything, queries and its own rows have to be finite.

@@ -29,6 +29,8 @@
 // 28.3 us: 22.8 in this kernel (87 %), the rest in the join of 76 splits.
 #pragma once
 
+#include <type_traits>
+
 #include "decode_tc.cuh"
 #include "diff.h"
 #include "elem.cuh"
@@ -46,6 +48,22 @@ struct DiffLayout {
   static constexpr int FLAG = RINGS + NW * EXTRA;
   static constexpr int BYTES = FLAG + 16 + 1024;      // + slack to align the base to 1024
 };
+
+// Weights are 2^(s - m + kDiffBias), m the row's running maximum.  In fp16 both parts of
+// a weight have their smallest step at 2^-24: of a largest weight of 1, one 2^-20 of it
+// was off by up to 3 %, and beside a first token that takes nearly all of both maps such
+// weights are what the difference is made of.  With a largest weight of 2^15 (below
+// fp16's 65,504) they keep the two parts' bits down to 2^-18 of it and 2^-40 of it at least.
+// The factor is in the sums as well, and leaves with them.
+template <typename T>
+constexpr float kDiffBias = std::is_same<T, __half>::value ? 15.f : 0.f;
+
+template <typename T>
+__device__ __forceinline__ float diff_weight(float s, float m) {
+  float x = s - m;
+  if constexpr (kDiffBias<T> != 0.f) x += kDiffBias<T>;
+  return ex2(x);
+}
 
 // Lane's share of head dims: chunk i holds dims 128 i + 4 lane .. + 3.  The
 // order of the sum of squares is the same wherever a head is finished.
@@ -344,10 +362,10 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
         const bool deadA = nA == -INFINITY, deadB = nB == -INFINITY;
         al[n][0] = deadA ? 1.f : ex2(m_run[n][0] - nA);
         al[n][1] = deadB ? 1.f : ex2(m_run[n][1] - nB);
-        const float p0 = deadA ? 0.f : ex2(s[0] - nA);
-        const float p2 = deadA ? 0.f : ex2(s[2] - nA);
-        const float p1 = deadB ? 0.f : ex2(s[1] - nB);
-        const float p3 = deadB ? 0.f : ex2(s[3] - nB);
+        const float p0 = deadA ? 0.f : diff_weight<T>(s[0], nA);
+        const float p2 = deadA ? 0.f : diff_weight<T>(s[2], nA);
+        const float p1 = deadB ? 0.f : diff_weight<T>(s[1], nB);
+        const float p3 = deadB ? 0.f : diff_weight<T>(s[3], nB);
         l_part[n][0] = l_part[n][0] * al[n][0] + (p0 + p2);
         l_part[n][1] = l_part[n][1] * al[n][1] + (p1 + p3);
         m_run[n][0] = nA;
@@ -475,7 +493,8 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
           stage[row * VD + 16 * mt + g + 8] = o[mt][n][2 + i] * inv;
         }
         if (is_split && g == 0)
-          p.part_lse[(size_t)slot * R + row] = l_part[n][i] > 0.f ? m_run[n][i] + lg2(l_part[n][i]) : -INFINITY;
+          p.part_lse[(size_t)slot * R + row] =
+              l_part[n][i] > 0.f ? m_run[n][i] + (lg2(l_part[n][i]) - kDiffBias<T>) : -INFINITY;
       }
     __syncwarp();
     if (!is_split) {
@@ -554,7 +573,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
       }
     }
     const float inv = Z > 0.f || Z != Z ? 1.f / Z : 0.f;
-    lse = Z > 0.f ? M + lg2(Z) : -INFINITY;
+    lse = Z > 0.f ? M + (lg2(Z) - kDiffBias<T>) : -INFINITY;
     return make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv);
   };
   float lse;

@@ -24,6 +24,8 @@ off by half of 2^-24 instead.
 
 from __future__ import annotations
 
+import math
+
 import numpy as np
 import torch
 
@@ -131,6 +133,43 @@ class Case:
         worst = float((err / tol).max(initial=0.0))
         assert worst <= 1.0, f"{what}: error {worst:.3g} of the bound"
         return worst
+
+
+# --------------------------------------------------------------------------
+# cases with exact scores
+
+def sink(gap, dtype, dim, group, lens, qs):
+    """A first token with values of zero stands `gap` log2 units above all others in both maps.
+    Scores are exact: one product of a query's 1 with a multiple of 1/8 below 32."""
+    c = Case(lens, qs, pairs=1, group=group, dim=dim, dtype=dtype, seed=gap, eps=0.0, factor=2.0**gap / 256,
+             weight=False, lam=0.25, scale=float(np.float32(math.log(2))))
+    g = torch.Generator().manual_seed(gap + 1)
+    c.q.zero_()
+    c.q[..., 0] = 1
+    c.k_pages[..., 0] = -torch.randint(0, 8, c.k_pages.shape[:-1], generator=g).to(DT[dtype]) / 8
+    c.v_pages.copy_((1 + c.v_pages.float() / 4).to(DT[dtype]))
+    for b in range(len(lens)):
+        c.k_pages[c.table[b, 0].long(), :, 0, 0] = gap
+        c.v_pages[c.table[b, 0].long(), :, 0] = 0
+    return c
+
+
+def check_sink(c, got):
+    """Beside the terms of tests/diff.py: exact scores leave the roundings of score x scale, of
+    the difference to the reference and of the exponent's offset, each at most half a step of
+    numbers up to 64 in log2 units, 3 x 2^-19 x ln 2 of a weight, and a scale off by 2^-24 of
+    32 units.  A weight in two parts of fp16 is off by at most 2^-25, half of the smallest
+    step, times the factor that weights are kept with: 2^-39 where a weight of 1 is 2^14."""
+    out, o, base, _ = c.want()
+    u, longest = HALF_STEP[c.dtype], max(c.lens)
+    absolute = 0.0
+    if c.dtype == "fp16":
+        absolute = 2.0**-39 * (1 + abs(float(c.lam[0]))) * longest * float(c.v_pages.float().abs().max())
+    rel = u * u + 3 * 2.0**-19 * 0.7 + 2.0**-19 + longest * 2.0**-23 + 2.0**-18
+    tol = c.factor * (rel * base + absolute) + (u + 2.0**-20) * np.abs(out) + 2.0**-25
+    err = np.abs(f64(got) - out)
+    worst = float((err / tol).max())
+    assert worst <= 1.0, f"error {worst:.3g} of the bound"
 
 
 class Device:

@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.diff import DT, PAGE, Case, f64
+from tests.diff import DT, PAGE, Case, check_sink, f64, sink
 
 
 def rounded(x, dtype, factor, parts):
@@ -70,3 +70,17 @@ def test_equal_weights_reject_a_missing_second_part(dtype, n):
     c.check(model(c, 2.0**14 if dtype == "fp16" else 1.0, 2, joint=True), want, True)
     # relative to the row's largest coefficient a weight is 1 - lambda
     assert not accepted(lambda: c.check(model(c, n, 1, joint=True), want, True))
+
+
+@pytest.mark.parametrize("gap", [16, 20, 24, 28])
+def test_a_sink_rejects_weights_without_room_below_them(gap):
+    """fp16 weights of a largest 1 have their smallest step 24 log2 units below it; with 2^15 of it
+    (one token), or 2^14 of a whole row's weight (several), they pass."""
+    one, several = sink(gap, "fp16", 64, 1, [300, 40], [1, 1]), sink(gap, "fp16", 64, 1, [300, 40], [3, 5])
+    check_sink(one, model(one, 2.0**15, 2))
+    check_sink(several, model(several, 2.0**14, 2, joint=True))
+    assert not accepted(lambda: check_sink(one, model(one, 1.0, 2)))
+    assert not accepted(lambda: check_sink(one, torch.zeros(2, 1, 128)))
+    b = sink(gap, "bf16", 64, 1, [300, 40], [1, 1])
+    check_sink(b, model(b, 1.0, 2))
+    assert not accepted(lambda: check_sink(b, model(b, 1.0, 2).flip(0) * 1.1))

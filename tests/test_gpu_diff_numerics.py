@@ -14,7 +14,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
-from tests.diff import DT, HALF_STEP, Case, Device  # noqa: E402
+from tests.diff import DT, HALF_STEP, Case, Device, check_sink, sink  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -44,3 +44,15 @@ def test_prefill_keeps_two_parts_of_the_weights_at_every_length(lens, qs, dim, g
     assert d.done() == 0
     c.check(got, c.want(rows), True, rows=rows)
     assert bool(torch.isfinite(got).all())
+
+
+@pytest.mark.parametrize("gap", [16, 20, 24, 28])
+@pytest.mark.parametrize("dim,group", [(64, 1), (64, 8), (128, 4)])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_decode_of_small_weights_beside_a_sink(gap, dim, group, dtype):
+    c = sink(gap, dtype, dim, group, [300, 40], [1, 1])
+    for splits in (1, 3, 12):
+        d = Device(c).make_plan(forced_splits=splits)
+        got = d.decode()
+        assert d.done() == 0
+        check_sink(c, got)
