@@ -65,8 +65,7 @@ constexpr int kDiffPrefillThreads = (kRowWarps + 4) * 32;
 // sum as well (2^-14 of a weight at 2^10): the factor is multiplied instead.
 constexpr float kFoldedLog2 = 1024.f;
 // A stage's sum of weights, relative to the row's reference, up to which that
-// reference stays: weights are then below it, and two of them times the factor of
-// fp16 (2^7) below that type's largest value.
+// reference stays.
 constexpr float kLateSum = 128.f;
 
 template <int D>
@@ -594,7 +593,10 @@ __global__ void __launch_bounds__(kDiffPrefillThreads, 1)
     // last visible token; rows that are not there see all of zero queries' scores
     const int qpos = ok ? pos0 + tt : span - 1;
     const uint32_t t_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    constexpr float kBias = std::is_same<T, __half>::value ? 7.f : 0.f;  // keeps small fp16 weights normal
+    // log2 of a factor of the weights, which are at most 2 in size without it.  fp16's
+    // smallest step is 2^-24: beside a token that takes nearly all of both maps, the others'
+    // weights keep the two parts' bits down to 2^-17 of it, and 2^-39 of it at least.
+    constexpr float kBias = std::is_same<T, __half>::value ? 14.f : 0.f;
 
     // q into shared memory (zeros where there is none): K-major, 16-byte chunk c of a
     // row's 128-byte box at chunk c ^ (row % 8).
@@ -777,13 +779,11 @@ __global__ void __launch_bounds__(kDiffPrefillThreads, 1)
     };
     const float2 st1 = joined(low.x, low.y, high.x, high.y), st2v = joined(low.z, low.w, high.z, high.w);
 
-    // ---- pass 2: weights f (2^(s_1 - m_1) / l_1 - lambda 2^(s_2 - m_2) / l_2), with f the
-    // factor that brings the larger of the two coefficients to 1
-    // (Quotients within 2 units in the last place: 8.7 -> 8.4 us, 3 prompts of up to 130 tokens.)
+    // ---- pass 2: weights f (2^(s_1 - m_1) / l_1 - lambda 2^(s_2 - m_2) / l_2), f = 1 / max(1, |lambda|)
+    // (The other quotients within 2 units in the last place: 8.7 -> 8.4 us, 3 prompts of up to 130 tokens.)
     const float c1 = st1.y > 0.f || st1.y != st1.y ? __fdividef(1.f, st1.y) : 0.f;
     const float c2 = st2v.y > 0.f || st2v.y != st2v.y ? __fdividef(fabsf(lambda), st2v.y) : 0.f;
-    const float big = fmaxf(c1, c2);
-    const float f = big > 0.f ? 1.f / big : 0.f;
+    const float most = fmaxf(1.f, fabsf(lambda)), f = 1.f / most;
     const float sgn = lambda < 0.f ? 1.f : -1.f;
     const bool far = __any_sync(kFull, (fabsf(st1.x) > kFoldedLog2 && st1.x != -INFINITY) ||
                                            (fabsf(st2v.x) > kFoldedLog2 && st2v.x != -INFINITY)) != 0;
@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(kDiffPrefillThreads, 1)
       *flag = 1;
     }
     tc5::fence_after();
-    const float inv = f > 0.f || f != f ? exp2f(-kBias) / f : 0.f;
+    const float inv = exp2f(-kBias) * most;
     const uint32_t t_o = t_row + (uint32_t)(L::O + D / 2 * g);
     float sum = 0.f;
 #pragma unroll

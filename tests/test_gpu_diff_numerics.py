@@ -56,3 +56,14 @@ def test_decode_of_small_weights_beside_a_sink(gap, dim, group, dtype):
         got = d.decode()
         assert d.done() == 0
         check_sink(c, got)
+
+
+@pytest.mark.parametrize("gap", [16, 20, 24, 28])
+@pytest.mark.parametrize("dim,group", [(64, 1), (64, 8), (128, 4)])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_prefill_of_small_weights_beside_a_sink(gap, dim, group, dtype):
+    c = sink(gap, dtype, dim, group, [300, 40], [3, 30])
+    d = Device(c).make_prefill_plan()
+    got = d.prefill()
+    assert d.done() == 0
+    check_sink(c, got)
