@@ -119,7 +119,10 @@ extern "C" pa_status_t pa_diff_plan(const pa_shape_t* shape, const int32_t* seq_
   plan_out->owns_blob = 1;
   plan_out->plan_id = plan.plan_id;
   plan_out->blob_bytes = plan.blob_bytes;
-  plan_out->workspace_bytes = plan.workspace_bytes;
+  const int rows = 2 * (shape->num_q_heads / shape->num_kv_heads);
+  plan_out->workspace_bytes = diff_workspace_bytes(
+      layout(plan.num_work_items, plan.num_groups, plan.num_split_items, rows, pairs.head_dim),
+      plan.num_split_items, rows);
   plan_out->host_blob = plan.host_blob;
   plan_out->wait_limit_ns = o.wait_limit_ns;
   return PA_OK;
@@ -163,7 +166,7 @@ extern "C" pa_status_t pa_diff_attention(const pa_shape_t* shape, const pa_diff_
     return PA_ERR_PLAN;
   const int G = shape->num_q_heads / shape->num_kv_heads, D = shape->head_dim;
   const Layout lay = layout(plan->num_work_items, plan->num_groups, plan->num_split_items, 2 * G, 2 * D);
-  if (plan->workspace_bytes != lay.total) return PA_ERR_PLAN;
+  if (plan->workspace_bytes != diff_workspace_bytes(lay, plan->num_split_items, 2 * G)) return PA_ERR_PLAN;
   if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
       !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(dev_status, 4) ||
       !aligned(workspace, 256))
@@ -184,6 +187,7 @@ extern "C" pa_status_t pa_diff_attention(const pa_shape_t* shape, const pa_diff_
   s.counters = (int*)(ws + lay.counters_off);
   s.part_lse = (float*)(ws + lay.lse_off);
   s.part_o = (float*)(ws + lay.o_off);
+  p.part_sum = (float*)(ws + lay.total);
   s.status = dev_status;
   s.batch = shape->batch;
   s.num_q_heads = shape->num_q_heads;

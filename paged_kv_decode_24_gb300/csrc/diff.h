@@ -41,10 +41,20 @@ struct DiffEpilogue {
 };
 
 struct DiffDecodeParams {
-  SplitParams s;  // num_kv_heads counts pairs, the partials hold 2G rows of 2D values;
-                  // fuse_merge 0: launch_diff_merge joins them
+  SplitParams s;    // num_kv_heads counts pairs, the partials hold 2G rows of 2D values;
+                    // fuse_merge 0: launch_diff_merge joins them
+  // A partial's row is o, its values over its sum of weights; m, the reference of the
+  // weights (in s.part_lse; NaN: the split gave up); and l, their sum, here.  m and l stay
+  // apart: in m + log2(l), with scores of 10^5 the roundings of m are parts of a unit, and
+  // splits with as large scores were weighted wrong.  m = -inf: no token, l = 0.
+  float* part_sum;
   DiffEpilogue e;
 };
+
+// The workspace: the decode layout, then the partials' sums.
+inline size_t diff_workspace_bytes(const Layout& l, int split_items, int rows) {
+  return l.total + align_sz(4 * (size_t)split_items * rows, 256);
+}
 
 struct DiffPrefillParams {
   const void* q;

@@ -102,6 +102,58 @@ __device__ __forceinline__ void diff_write_head(const DiffEpilogue& e, float lam
   }
 }
 
+// What a split's row counts for beside others, relative to the reference M of them all.
+// (m = -inf: no token, and l is 0, or NaN where scores were.)
+__device__ __forceinline__ float diff_split_weight(float m, float l, float M) {
+  return m == -INFINITY ? l : ex2(m - M) * l;
+}
+
+// Dims d0 .. d0+3 of a row over all splits of the target, in their order, NB at once.
+template <int VD, int NB>
+__device__ __forceinline__ float4 diff_merge_chunk(const MergeTarget& t, const float* part_sum, int row, int d0) {
+  const int ns = t.grp.z;
+  const size_t first = (size_t)t.grp.w * t.G + row;
+  float m = -INFINITY, z = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < ns; s0 += NB) {
+    float r[NB], l[NB];
+    float4 x[NB];
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      r[u] = -INFINITY;
+      l[u] = 0.f;
+      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s0 + u < ns) {
+        const size_t at = first + (size_t)(s0 + u) * t.G;
+        r[u] = __ldcg(t.lse + at);
+        l[u] = __ldcg(part_sum + at);
+        x[u] = __ldcg(reinterpret_cast<const float4*>(t.o + at * VD + d0));
+      }
+    }
+    float M = m;
+#pragma unroll
+    for (int u = 0; u < NB; ++u) M = fmaxf(M, r[u]);
+    const float sc = m == -INFINITY ? 1.f : ex2(m - M);  // nothing but zeros (or NaN) so far: as it is
+    z *= sc;
+    a.x *= sc;
+    a.y *= sc;
+    a.z *= sc;
+    a.w *= sc;
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      const float w = diff_split_weight(r[u], l[u], M);
+      z += w;
+      a.x = fmaf(w, x[u].x, a.x);
+      a.y = fmaf(w, x[u].y, a.y);
+      a.z = fmaf(w, x[u].z, a.z);
+      a.w = fmaf(w, x[u].w, a.w);
+    }
+    m = M;
+  }
+  if (z == 0.f) return make_float4(0.f, 0.f, 0.f, 0.f);
+  return make_float4(a.x / z, a.y / z, a.z / z, a.w / z);
+}
+
 // The heads first, first + stride, ... of a pair whose partials are complete,
 // a warp each.
 template <typename T, int D, int G>
@@ -115,8 +167,8 @@ __device__ __forceinline__ void diff_merge_heads(const DiffDecodeParams& p, cons
 #pragma unroll
       for (int i = 0; i < N; ++i)
         r[m][i] = t.grp.z <= kMergeBatchSmall
-                      ? merge_chunk<VD, kMergeBatchSmall>(t, m * G + h, 128 * i + 4 * lane)
-                      : merge_chunk<VD, kMergeBatch>(t, m * G + h, 128 * i + 4 * lane);
+                      ? diff_merge_chunk<VD, kMergeBatchSmall>(t, p.part_sum, m * G + h, 128 * i + 4 * lane)
+                      : diff_merge_chunk<VD, kDiffMergeSplits>(t, p.part_sum, m * G + h, 128 * i + 4 * lane);
     const size_t head = (size_t)t.grp.y * G + h;
     diff_write_head<T, VD>(p.e, __ldg(p.e.lambda + head), r[0], r[1], lane,
                            static_cast<T*>(p.s.out) +
@@ -492,9 +544,10 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
           stage[row * VD + 16 * mt + g] = o[mt][n][i] * inv;
           stage[row * VD + 16 * mt + g + 8] = o[mt][n][2 + i] * inv;
         }
-        if (is_split && g == 0)
-          p.part_lse[(size_t)slot * R + row] =
-              l_part[n][i] > 0.f ? m_run[n][i] + (lg2(l_part[n][i]) - kDiffBias<T>) : -INFINITY;
+        if (is_split && g == 0) {
+          p.part_lse[(size_t)slot * R + row] = m_run[n][i];
+          dp.part_sum[(size_t)slot * R + row] = l_part[n][i];
+        }
       }
     __syncwarp();
     if (!is_split) {
@@ -553,12 +606,12 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
     }
   __syncthreads();
 
-  // four dims of a row over the warps, normalised; the row's log-sum-exp
-  auto merged = [&](int row, int d, float& lse) {
-    float M = -INFINITY;
+  // four dims of a row over the warps, normalised; the row's reference and sum
+  auto merged = [&](int row, int d, float& M, float& Z) {
+    M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < NW; ++w) M = fmaxf(M, st[w * SLOT + row]);
-    float Z = 0.f;
+    Z = 0.f;
     float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
     if (M != -INFINITY) {
 #pragma unroll
@@ -573,26 +626,28 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
       }
     }
     const float inv = Z > 0.f || Z != Z ? 1.f / Z : 0.f;
-    lse = Z > 0.f ? M + (lg2(Z) - kDiffBias<T>) : -INFINITY;
     return make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv);
   };
-  float lse;
+  float ref, total;
   if (!is_split) {
     for (int h = warp; h < G; h += NW) {
       float4 r[2][VD / 128];
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int i = 0; i < VD / 128; ++i) r[m][i] = merged(m * G + h, 128 * i + 4 * lane, lse);
+        for (int i = 0; i < VD / 128; ++i) r[m][i] = merged(m * G + h, 128 * i + 4 * lane, ref, total);
       diff_write_head<T, VD>(dp.e, __ldg(lambda + h), r[0], r[1], lane, out + (size_t)h * VD);
     }
     return;
   }
   for (int idx = threadIdx.x; idx < R * VD / 4; idx += NW * 32) {
     const int row = idx / (VD / 4), d = idx % (VD / 4) * 4;
-    const float4 r = merged(row, d, lse);
+    const float4 r = merged(row, d, ref, total);
     *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * R + row) * VD + d) = r;
-    if (d == 0) p.part_lse[(size_t)slot * R + row] = lse;
+    if (d == 0) {
+      p.part_lse[(size_t)slot * R + row] = ref;
+      dp.part_sum[(size_t)slot * R + row] = total;
+    }
   }
   if (!p.fuse_merge) return;
   const MergeTarget mt = merge_target(p, sg.y, grp, R);

@@ -2,7 +2,7 @@
 // its own, for plans with many splits.
 //
 // A head's output is the difference of two rows, each joined from ns partials
-// (o_s, lse_s): with M = max_s lse_s, w_s = 2^(lse_s - M),
+// (o_s, m_s, l_s): with M = max_s m_s, w_s = 2^(m_s - M) l_s,
 //   row = sum_s w_s o_s / sum_s w_s.
 // Two rows of 2D fp32 values a split and head have to be read: with one SM doing it
 // for all heads of a pair (the last task of the pair in the split kernel), 76
@@ -64,13 +64,16 @@ __global__ void __launch_bounds__(2 * D / 4 * kLanes) diff_merge_kernel(const __
   load(sl);  // on their way while the weights are made
   __syncthreads();
   if (warp < 2) {  // a map each: the splits' weights
-    const float* lse = p.part_lse + (size_t)off * R + warp * group_size + h;
+    const size_t first = (size_t)off * R + warp * group_size + h;
+    // the lane's own sums, where the joined values will be
+    float* sum = reinterpret_cast<float*>(part) + warp * kMaxSplits;
     float top = -INFINITY;
     bool lost = false;
 #pragma unroll 4
     for (int s = lane; s < ns; s += 32) {
-      const float v = __ldcg(lse + (size_t)s * R);
+      const float v = __ldcg(p.part_lse + first + (size_t)s * R);
       weight[warp][s] = v;
+      sum[s] = __ldcg(dp.part_sum + first + (size_t)s * R);
       lost = lost || isnan(v);
       top = fmaxf(top, v);
     }
@@ -78,13 +81,13 @@ __global__ void __launch_bounds__(2 * D / 4 * kLanes) diff_merge_kernel(const __
     for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, m));
     float z = 0.f;
     for (int s = lane; s < ns; s += 32) {
-      const float w = top == -INFINITY ? 0.f : ex2(weight[warp][s] - top);  // 0 for an empty split
+      const float w = diff_split_weight(weight[warp][s], sum[s], top);
       weight[warp][s] = w;
       z += w;
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) z += __shfl_xor_sync(kFull, z, m);
-    if (lane == 0) norm[warp] = z > 0.f ? 1.f / z : 0.f;
+    if (lane == 0) norm[warp] = z == 0.f ? 0.f : 1.f / z;
     if (lost) missing = 1;
   }
   __syncthreads();
@@ -127,6 +130,7 @@ __global__ void __launch_bounds__(2 * D / 4 * kLanes) diff_merge_kernel(const __
   diff_write_head<T, VD>(dp.e, __ldg(dp.e.lambda + head), r[0], r[1], lane,
                          static_cast<T*>(p.out) + ((size_t)grp.x * p.num_kv_heads * group_size + head) * VD);
   static_assert(THREADS >= 64, "a warp for each map");
+  static_assert(2 * kMaxSplits * sizeof(float) <= sizeof(part), "the sums fit where the values go");
 }
 
 template <typename T, int D>

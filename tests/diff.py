@@ -172,6 +172,27 @@ def check_sink(c, got):
     assert worst <= 1.0, f"error {worst:.3g} of the bound"
 
 
+def exact_case(scale, dtype, lens, dim=64, group=2):
+    """Whole scores of at most 32, so that they are exact, and of a few sizes, so that large
+    scales leave several equal tokens on top."""
+    c = Case(lens, pairs=1, group=group, dim=dim, dtype=dtype, seed=5, scale=scale, eps=0.0, factor=1.0, weight=False)
+    for name in ("q", "k_pages"):
+        x = torch.clamp((getattr(c, name).float() * 0.7).round(), -2, 2)
+        x[..., 8:] = 0
+        getattr(c, name).copy_(x.to(DT[dtype]))
+    return c
+
+
+def exact_want(c):
+    """The oracle's tuple with the size that exact scores leave: score x scale and its difference
+    to the maximum are each off by half a step of at most 32 x scale x log2(e) log2 units; from
+    scale 10 on scores that differ do so by 14 units and more, whose weights, 2^-14 and below, are
+    off by that much of 2^-14 of the row."""
+    out, o, base, _ = c.want()
+    units = 32 * min(c.scale, 1.0) * 1.45 * 2 * 2.0**-24 if c.scale < 10 else 2.0**-24
+    return out, o, base, np.full(out.shape[:2], units / (2 * c.dim * 2.0**-23))
+
+
 class Device:
     """A Case on the GPU."""
 

@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.diff import DT, PAGE, Case, check_sink, f64, sink
+from tests.diff import DT, PAGE, Case, check_sink, exact_case, exact_want, f64, sink
 
 
 def rounded(x, dtype, factor, parts):
@@ -57,6 +57,24 @@ def accepted(check):
     except AssertionError:
         return False
     return True
+
+
+@pytest.mark.parametrize("scale", [1e-3, 0.5, 1e4, 1e6])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_exact_scores_reject_wrong_outputs(scale, dtype):
+    c = exact_case(scale, dtype, [90, 3, 17])
+    want = exact_want(c)
+    got = model(c, 1.0, 2)
+    c.check(got, want, True)
+    wrong = [torch.zeros_like(got), -got, got.flip(1), got.flip(0), got.roll(1, -1), 1.01 * got]
+    for i, x in enumerate(wrong):
+        assert not accepted(lambda: c.check(x, want, True)), i
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_exact_scores_reject_a_missing_second_part(dtype):
+    c = exact_case(0.5, dtype, [90, 3, 17])
+    assert not accepted(lambda: c.check(model(c, 1.0, 1), exact_want(c), True))
 
 
 @pytest.mark.parametrize("n", [1040, 2500])

@@ -14,7 +14,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
-from tests.diff import DT, HALF_STEP, Case, Device, check_sink, sink  # noqa: E402
+from tests.diff import DT, HALF_STEP, Case, Device, check_sink, exact_case, exact_want, sink  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -67,3 +67,18 @@ def test_prefill_of_small_weights_beside_a_sink(gap, dim, group, dtype):
     got = d.prefill()
     assert d.done() == 0
     check_sink(c, got)
+
+
+# --------------------------------------------------------------------------
+# exact scores: bounds that a wrong weight does not pass (tests/test_diff_bounds.py)
+
+@pytest.mark.parametrize("scale", [1e-3, 0.5, 1e4, 1e6])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim,group", [(64, 2), (128, 8)])
+def test_decode_of_exact_scores(scale, dtype, dim, group):
+    c = exact_case(scale, dtype, [90, 3, 17], dim, group)
+    for splits in (1, 2, 12):
+        d = Device(c).make_plan(forced_splits=splits)
+        got = d.decode()
+        assert d.done() == 0
+        c.check(got, exact_want(c), True, f"splits {splits}")
