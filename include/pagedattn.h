@@ -879,7 +879,8 @@ pa_status_t pa_diff_plan_upload(const pa_diff_plan_t* plan, void* workspace, siz
  * in a fixed order, the same bits on every call: by the last task of the
  * (sequence, pair), or, where some sequence has more than 8, by a second kernel.
  * A sequence of length 0, or without a valid page, gets zeros.  Rows past a
- * sequence's end may hold anything, queries and its own rows have to be finite.
+ * sequence's end may hold anything, queries and its own rows have to be finite
+ * (a head with a query that holds a NaN gets NaN, the others are as they would be).
  * Device-side problems are reported as pa_decode_attention's. */
 pa_status_t pa_diff_attention(const pa_shape_t* shape, const pa_diff_plan_t* plan,
                               const pa_diff_t* diff, const void* q, const void* k_pages,

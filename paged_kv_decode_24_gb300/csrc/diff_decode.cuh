@@ -58,11 +58,13 @@ struct DiffLayout {
 template <typename T>
 constexpr float kDiffBias = std::is_same<T, __half>::value ? 15.f : 0.f;
 
+// A token that is left out (s = -inf) has weight 0 under any maximum, that of no token
+// (-inf) too, under which a score that is not a number stays one.
 template <typename T>
 __device__ __forceinline__ float diff_weight(float s, float m) {
   float x = s - m;
   if constexpr (kDiffBias<T> != 0.f) x += kDiffBias<T>;
-  return ex2(x);
+  return s == -INFINITY ? 0.f : ex2(x);
 }
 
 // Lane's share of head dims: chunk i holds dims 128 i + 4 lane .. + 3.  The
@@ -411,13 +413,10 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
           mB = fmaxf(mB, __shfl_xor_sync(kFull, mB, m));
         }
         const float nA = fmaxf(m_run[n][0], mA), nB = fmaxf(m_run[n][1], mB);
-        const bool deadA = nA == -INFINITY, deadB = nB == -INFINITY;
-        al[n][0] = deadA ? 1.f : ex2(m_run[n][0] - nA);
-        al[n][1] = deadB ? 1.f : ex2(m_run[n][1] - nB);
-        const float p0 = deadA ? 0.f : diff_weight<T>(s[0], nA);
-        const float p2 = deadA ? 0.f : diff_weight<T>(s[2], nA);
-        const float p1 = deadB ? 0.f : diff_weight<T>(s[1], nB);
-        const float p3 = deadB ? 0.f : diff_weight<T>(s[3], nB);
+        al[n][0] = nA == -INFINITY ? 1.f : ex2(m_run[n][0] - nA);
+        al[n][1] = nB == -INFINITY ? 1.f : ex2(m_run[n][1] - nB);
+        const float p0 = diff_weight<T>(s[0], nA), p2 = diff_weight<T>(s[2], nA);
+        const float p1 = diff_weight<T>(s[1], nB), p3 = diff_weight<T>(s[3], nB);
         l_part[n][0] = l_part[n][0] * al[n][0] + (p0 + p2);
         l_part[n][1] = l_part[n][1] * al[n][1] + (p1 + p3);
         m_run[n][0] = nA;
@@ -613,17 +612,16 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
     for (int w = 0; w < NW; ++w) M = fmaxf(M, st[w * SLOT + row]);
     Z = 0.f;
     float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M != -INFINITY) {
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const float sc = ex2(st[w * SLOT + row] - M);  // 0 for an empty warp (m = -inf)
-        const float4 x = *reinterpret_cast<const float4*>(st + w * SLOT + 2 * R + row * VD + d);
-        Z = fmaf(st[w * SLOT + R + row], sc, Z);
-        r.x = fmaf(x.x, sc, r.x);
-        r.y = fmaf(x.y, sc, r.y);
-        r.z = fmaf(x.z, sc, r.z);
-        r.w = fmaf(x.w, sc, r.w);
-      }
+    for (int w = 0; w < NW; ++w) {
+      // 0 for an empty warp (m = -inf), unless all are: zeros, or NaN, then
+      const float sc = M == -INFINITY ? 1.f : ex2(st[w * SLOT + row] - M);
+      const float4 x = *reinterpret_cast<const float4*>(st + w * SLOT + 2 * R + row * VD + d);
+      Z = fmaf(st[w * SLOT + R + row], sc, Z);
+      r.x = fmaf(x.x, sc, r.x);
+      r.y = fmaf(x.y, sc, r.y);
+      r.z = fmaf(x.z, sc, r.z);
+      r.w = fmaf(x.w, sc, r.w);
     }
     const float inv = Z > 0.f || Z != Z ? 1.f / Z : 0.f;
     return make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv);

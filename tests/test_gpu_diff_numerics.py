@@ -4,6 +4,7 @@ and beside the cases that have exact scores."""
 
 from __future__ import annotations
 
+import numpy as np
 import pytest
 
 from paged_kv_decode_24_gb300 import binding
@@ -14,7 +15,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
-from tests.diff import DT, HALF_STEP, Case, Device, check_sink, exact_case, exact_want, sink  # noqa: E402
+from tests.diff import DT, HALF_STEP, Case, Device, check_sink, exact_case, exact_want, f64, sink  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -67,6 +68,68 @@ def test_prefill_of_small_weights_beside_a_sink(gap, dim, group, dtype):
     got = d.prefill()
     assert d.done() == 0
     check_sink(c, got)
+
+
+# --------------------------------------------------------------------------
+# queries that are not numbers
+
+def poisoned(c, marks):
+    """The case's outputs with NaN in queries of map m of head h of row r, marks = (r, h, m)."""
+    want = c.want()
+    for r, h, m in marks:
+        c.q[r, 2 * h + m, 5] = float("nan")
+    return want
+
+
+def check_poisoned(c, got, want, marks):
+    g = f64(got)
+    lost = np.zeros(g.shape[:2], bool)
+    for r, h, _ in marks:
+        lost[r, h] = True
+    assert np.isnan(g[lost]).all()
+    out, o, base, size = want
+    keep = np.where(lost[..., None], out, g)     # the others are as they would be
+    c.check(torch.from_numpy(keep), (out, o, base, size), True)
+
+
+@pytest.mark.parametrize("group,dim", [(1, 64), (4, 128), (8, 64)])
+@pytest.mark.parametrize("splits", [1, 3, 12])
+def test_decode_shows_queries_that_are_not_numbers(group, dim, splits):
+    c = Case([300, 40, 1, 77], pairs=2, group=group, dim=dim, seed=3, poison=True)
+    marks = [(0, 0, 0), (1, c.heads - 1, 1), (2, c.heads // 2, 0)]
+    want = poisoned(c, marks)
+    d = Device(c).make_plan(forced_splits=splits)
+    got = d.decode()
+    assert d.done() == 0
+    check_poisoned(c, got, want, marks)
+
+
+@pytest.mark.parametrize("group,dim", [(1, 64), (4, 128), (8, 64)])
+@pytest.mark.parametrize("splits", [1, 2])
+def test_decode_of_many_short_sequences_shows_queries_that_are_not_numbers(group, dim, splits):
+    """Tasks of one warp each."""
+    c = Case([20 + i % 60 for i in range(900)], pairs=3, group=group, dim=dim, seed=4)
+    marks = [(0, 0, 1), (500, c.heads - 1, 0)]
+    for r, h, m in marks:
+        c.q[r, 2 * h + m, 5] = float("nan")
+    d = Device(c).make_plan(forced_splits=splits)
+    assert d.plan.c.num_shared_ctas < d.plan.c.num_ctas
+    got = d.decode()
+    assert d.done() == 0
+    lost = torch.isnan(got).all(-1)
+    assert torch.equal(lost, torch.isnan(got).any(-1)) and int(lost.sum()) == 2
+    assert all(bool(lost[r, h]) for r, h, _ in marks)
+
+
+@pytest.mark.parametrize("group,dim", [(1, 64), (4, 128)])
+def test_prefill_shows_queries_that_are_not_numbers(group, dim):
+    c = Case([300, 40], [70, 40], pairs=2, group=group, dim=dim, seed=3, poison=True)
+    marks = [(0, 0, 0), (75, c.heads - 1, 1), (109, 1, 0)]
+    want = poisoned(c, marks)
+    d = Device(c).make_prefill_plan()
+    got = d.prefill()
+    assert d.done() == 0
+    check_poisoned(c, got, want, marks)
 
 
 # --------------------------------------------------------------------------
