@@ -35,13 +35,15 @@ __global__ void __launch_bounds__(2 * D / 4 * kLanes) diff_merge_kernel(const __
   const int gi = blockIdx.x / group_size, h = blockIdx.x % group_size;
   // the plan is written by the upload alone: it may be read before the wait
   const int4 hdr = *reinterpret_cast<const int4*>(p.ws_header);
+  const int2 hdr_ctas = *reinterpret_cast<const int2*>(p.ws_header + 8);
   const int4 grp = gi < p.num_groups ? p.groups[gi] : make_int4(0, 0, 0, 0);  // {seq, pair, splits, first slot}
   if (threadIdx.x == 0) missing = 0;
   pdl_launch_dependents();
   pdl_wait_primary();  // the partials are there
   const int ns = grp.z, off = grp.w, R = 2 * group_size;
+  // (The split kernel's own checks of the plan: where it refuses one, nothing is joined.)
   if (hdr.x != (int)kDiffMagic || hdr.y != p.num_items || hdr.z != p.num_groups || hdr.w != p.num_split_items ||
-      gi >= p.num_groups || ns < 1 || ns > kMaxSplits || off < 0 || off + ns > p.num_split_items || grp.x < 0 ||
+      hdr_ctas.x != p.num_ctas || hdr_ctas.y != p.num_shared || gi >= p.num_groups || ns < 1 || ns > kMaxSplits || off < 0 || off + ns > p.num_split_items || grp.x < 0 ||
       grp.x >= p.batch || grp.y < 0 || grp.y >= p.num_kv_heads) {
     if (threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
     return;

@@ -15,7 +15,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
-from tests.diff import DT, HALF_STEP, Case, Device, check_sink, exact_case, exact_want, f64, sink  # noqa: E402
+from tests.diff import DT, HALF_STEP, PAGE, Case, Device, check_sink, exact_case, exact_want, f64, sink  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -130,6 +130,27 @@ def test_prefill_shows_queries_that_are_not_numbers(group, dim):
     got = d.prefill()
     assert d.done() == 0
     check_poisoned(c, got, want, marks)
+
+
+# --------------------------------------------------------------------------
+# another plan's partials
+
+def test_decode_joins_no_partials_of_another_plan():
+    """Two plans with as many tasks, groups and partials, dealt to other CTAs: a call with the
+    one, over a workspace that holds the other and its partials, writes nothing."""
+    short, long = Case([160] * 20, pairs=2, group=2, dim=64, seed=1), Case([1920] * 20, pairs=2, group=2, dim=64, seed=1)
+    shape = binding.make_shape(20, 8, 4, 64, PAGE, long.max_pages, long.num_pages, "fp16")
+    d = Device(long).make_plan(sms=8, forced_splits=10)
+    other = binding.DiffPlan(shape, short.lens, 8, forced_splits=10)
+    for name in ("num_work_items", "num_groups", "num_split_items", "workspace_bytes"):
+        assert getattr(other.c, name) == getattr(d.plan.c, name)
+    assert other.c.num_ctas != d.plan.c.num_ctas and other.c.max_splits > 8
+    d.decode()                                    # its partials stay in the workspace
+    assert d.done() == 0
+    d.plan = other
+    got = d.decode()
+    assert d.done() == binding.PA_DEV_PLAN_MISMATCH
+    assert bool(torch.isnan(got).all())
 
 
 # --------------------------------------------------------------------------
