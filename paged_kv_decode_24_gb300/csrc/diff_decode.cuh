@@ -260,9 +260,11 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
   const bool is_split = (hw & kItemSplit) != 0;
   const bool is_last = (hw & kItemLast) != 0;
   const int pg0 = it.z, pg1 = it.w;
+  const bool slot_ok = is_split && split_slot_ok(p, sg, grp, b, pair);
   if (b < 0 || b >= p.batch || pair >= p.num_kv_heads || pg0 < 0 || pg1 < pg0 || pg1 > p.max_pages ||
-      (is_split && !split_slot_ok(p, sg, grp, b, pair))) {
+      slot_ok != is_split) {
     if (lane == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
+    if (slot_ok && (!coop || warp == 0)) mark_split_missing(p.part_lse, slot, R, lane);
     return;  // all warps of a shared task see the same task
   }
   const int Lmax = p.max_pages * kPageSize;

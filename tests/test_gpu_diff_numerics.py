@@ -153,6 +153,22 @@ def test_decode_joins_no_partials_of_another_plan():
     assert bool(torch.isnan(got).all())
 
 
+def test_decode_joins_nothing_where_a_split_does_not_fit():
+    """The workspace holds a plan of longer sequences, otherwise alike: their last splits lie past
+    the call's block table.  What an earlier call left of those splits is not joined."""
+    long, short = Case([1920] * 3, pairs=2, group=2, dim=64, seed=1), Case([1600] * 3, pairs=2, group=2, dim=64, seed=1)
+    d, e = Device(long).make_plan(forced_splits=10), Device(short).make_plan(forced_splits=10)
+    for name in ("num_work_items", "num_groups", "num_split_items", "num_ctas", "num_shared_ctas", "workspace_bytes"):
+        assert getattr(e.plan.c, name) == getattr(d.plan.c, name)
+    assert long.max_pages > 120 > short.max_pages
+    d.decode()
+    assert d.done() == 0
+    e.ws = d.ws
+    got = e.decode()
+    assert e.done() == binding.PA_DEV_PLAN_MISMATCH
+    assert bool(torch.isnan(got).all())
+
+
 # --------------------------------------------------------------------------
 # exact scores: bounds that a wrong weight does not pass (tests/test_diff_bounds.py)
 
