@@ -124,7 +124,8 @@ struct DPLayout {
   static constexpr int TMEM_SLOT = Q_READY + 8;
   static constexpr int FLAG = TMEM_SLOT + 8;            // this CTA gave up
   static constexpr int MISSING = FLAG + 4;              // a page of the span does not exist
-  static constexpr int BYTES = MISSING + 4 + 1024;
+  static constexpr int MOVED = MISSING + 4;             // score products issued so far
+  static constexpr int BYTES = MOVED + 4 + 1024;
   // once every product of the CTA is done, output rows where q was ([row warp][32
   // rows][D / 2 dims]), and where keys were
   static constexpr int SQ = K;                          // [quarter of the columns][row] sums of squares
@@ -218,6 +219,7 @@ __global__ void __launch_bounds__(kDiffPrefillThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* flag = reinterpret_cast<int*>(base + L::FLAG);
   volatile int* missing = reinterpret_cast<int*>(base + L::MISSING);
+  volatile int* moved = reinterpret_cast<int*>(base + L::MOVED);
 
   // The plan is written by the upload alone, which the programmatic launch
   // does not overlap: it may be read before the wait for the kernel ahead.
@@ -227,6 +229,7 @@ __global__ void __launch_bounds__(kDiffPrefillThreads, 1)
   if (threadIdx.x == 0) {
     *flag = 0;
     *missing = 0;
+    *moved = 0;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_k)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_v)) : "memory");
     for (int b = L::K_FULL; b < L::S1_READ; b += 8) mbar_init(sb + b, 1);
@@ -301,6 +304,17 @@ __global__ void __launch_bounds__(kDiffPrefillThreads, 1)
   }
   const int n = (span + KT - 1) / KT;                   // stages (0: nothing to do)
   const int parts = (span + kTokens - 1) / kTokens;     // buffers of pass 2
+  // The first value slot to be read again and the first weights come after all of pass 1,
+  // which takes as long as the context is: such a wait's limit counts from the last score
+  // product that was issued, so that every limit is one of a stage, in both passes.
+  auto while_moving = [&](auto&& wait) {
+    for (int seen = *moved; !wait();) {
+      const int now = *moved;
+      if (now == seen) return false;
+      seen = now;
+    }
+    return true;
+  };
   const int npages = (span + kPageSize - 1) / kPageSize;
 
   if (warp >= kRowWarps + 2) {
@@ -389,7 +403,7 @@ __global__ void __launch_bounds__(kDiffPrefillThreads, 1)
           const bool all = take_entries(phys, there);
           if (issued + 1 < n) load_entries(issued + 1);
           if (issued >= L::NV) {
-            good = mbar_wait_bounded_sleep(sb + L::V_FREE + 8 * slot, phase, p.wait_ns);
+            good = while_moving([&]() { return mbar_wait_bounded_sleep(sb + L::V_FREE + 8 * slot, phase, p.wait_ns); });
             if (!good) break;
           }
           const uint32_t bar = sb + L::V_FULL + 8 * slot;
@@ -516,6 +530,7 @@ __global__ void __launch_bounds__(kDiffPrefillThreads, 1)
             scores(1, idesc1, at * 2 * KT + KT, 0);
           }
           tc5::commit(sb + L::S1_DONE + 8 * at);
+          *moved = i + 1;
           read_keys();
         }
         int at = 0, part = 0;
@@ -541,6 +556,7 @@ __global__ void __launch_bounds__(kDiffPrefillThreads, 1)
           }
           scores(0, idesc2, at * 128, part);
           tc5::commit(sb + L::S2_DONE + 8 * at);
+          *moved = n + i + 1;
           if (++part == L::PARTS || i == parts - 1) {
             part = 0;
             read_keys();
@@ -557,7 +573,7 @@ __global__ void __launch_bounds__(kDiffPrefillThreads, 1)
           if (part == 0)
             good = wait(L::V_FULL + 8 * vs, vphase) &&
                    (i + L::PARTS < parts || span % KT == 0 || wait(L::V_CLEAR, 0u));  // rows to clear: once they are
-          good = good && wait(L::P_READY + 8 * at, phase);
+          good = good && while_moving([&]() { return wait(L::P_READY + 8 * at, phase); });
           if (!good) break;
           tc5::fence_after();
           const uint64_t vb = tc5::desc_at(v_desc, vs * L::VSTAGE + part * (kTokens / kPageSize) * L::VPAGE);

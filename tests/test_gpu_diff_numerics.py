@@ -170,6 +170,31 @@ def test_decode_joins_nothing_where_a_split_does_not_fit():
 
 
 # --------------------------------------------------------------------------
+# waits
+
+@pytest.mark.parametrize("dim,group", [(64, 1), (128, 4)])
+def test_prefill_limits_one_wait_and_not_a_pass(dim, group):
+    """A context whose first pass alone takes milliseconds, with a limit far below that and far
+    above any single copy or product: no wait runs out while stages keep moving."""
+    n = 1 << 18
+    c = Case([n], [2], pairs=1, group=group, dim=dim, seed=2)
+    d = Device(c).make_prefill_plan()
+    want = d.prefill()
+    assert d.done() == 0
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    d.prefill()
+    end.record()
+    assert d.done() == 0
+    limit = 300_000
+    assert start.elapsed_time(end) * 1e6 > 4 * limit
+    d.make_prefill_plan(wait_limit_ns=limit)
+    got = d.prefill()
+    assert d.done() == 0
+    assert torch.equal(got, want)
+
+
+# --------------------------------------------------------------------------
 # exact scores: bounds that a wrong weight does not pass (tests/test_diff_bounds.py)
 
 @pytest.mark.parametrize("scale", [1e-3, 0.5, 1e4, 1e6])
