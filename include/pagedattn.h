@@ -774,7 +774,7 @@ typedef struct {
  * (slices of one projection's output will do), dense within a token;
  * q_out: dense [B][Hq][D].  q and q_out may both be null (keys and values
  * alone), or the same dense buffer; any other overlap of q_out's range with
- * an input's is refused.
+ * that of something else that the call reads or writes is refused.
  * The new key and value go to position seq_lens[b] - 1 of sequence b, as
  * pa_kv_append, pa_kv_append_q8 and pa_kv_append_fp8 write them; 8-bit caches
  * take their codes and scales from the rotated fp32 values.  k_scales and

@@ -304,9 +304,9 @@ bool ranges_meet(const void* p, int64_t stride, int64_t width, const void* q, in
   return a < b_end && b < a_end;
 }
 
-// What both calls check and launch; `rows` tokens, plan already in p.ws.
+// What both calls check and launch; `rows` tokens, the plan (plan_bytes) already in p.ws.
 pa_status_t rope_impl(const pa_shape_t* s, const pa_rope_t* rope, RopeParams& p, int64_t rows,
-                      int32_t* dev_status, void* stream) {
+                      size_t plan_bytes, int32_t* dev_status, void* stream) {
   if (!rope) return PA_ERR_INVALID_ARG;
   if (rope->rotary_dim < 16 || rope->rotary_dim > s->head_dim || rope->rotary_dim % 16 != 0)
     return PA_ERR_UNSUPPORTED;
@@ -331,6 +331,17 @@ pa_status_t rope_impl(const pa_shape_t* s, const pa_rope_t* rope, RopeParams& p,
     if ((!in_place && ranges_meet(p.q, p.q_stride, wq, p.q_out, wq, rows)) ||
         ranges_meet(p.k, p.k_stride, wk, p.q_out, wq, rows) ||
         ranges_meet(p.v, p.v_stride, wk, p.q_out, wq, rows))
+      return PA_ERR_INVALID_ARG;
+    auto meets = [&](const void* a, uintptr_t bytes) {
+      return a && (uintptr_t)a < (uintptr_t)p.q_out + 2 * (uintptr_t)(rows * wq) && (uintptr_t)p.q_out < (uintptr_t)a + bytes;
+    };
+    const uintptr_t slots = (uintptr_t)s->num_pages * s->num_kv_heads * kPageSize;
+    const uintptr_t pool = slots * s->head_dim * (eight ? 1 : 2);
+    if (meets(rope->table, 4 * (uintptr_t)rope->num_positions * rope->rotary_dim) || meets(p.positions, 4 * rows) ||
+        meets(p.block_table, 4 * (uintptr_t)s->batch * s->max_pages_per_seq) ||
+        meets(p.seq_lens, 4 * (uintptr_t)s->batch) || meets(p.ws, plan_bytes) || meets(dev_status, 4) ||
+        meets(p.k_pages, pool) || meets(p.v_pages, pool) || meets(p.k_scales, 4 * slots) ||
+        meets(p.v_scales, 4 * slots))
       return PA_ERR_INVALID_ARG;
   }
   p.table = rope->table;
@@ -368,7 +379,7 @@ extern "C" pa_status_t pa_rope_append(const pa_shape_t* shape, const pa_rope_t* 
   p.q_stride = q_stride, p.k_stride = k_stride, p.v_stride = v_stride;
   p.k_pages = k_pages, p.v_pages = v_pages, p.k_scales = k_scales, p.v_scales = v_scales;
   p.positions = positions, p.block_table = block_table, p.seq_lens = seq_lens;
-  return rope_impl(shape, rope, p, shape->batch, dev_status, stream);
+  return rope_impl(shape, rope, p, shape->batch, 0, dev_status, stream);
 }
 
 extern "C" pa_status_t pa_rope_append_tokens(
@@ -389,5 +400,5 @@ extern "C" pa_status_t pa_rope_append_tokens(
   p.ws = static_cast<const int32_t*>(workspace);
   p.cu = reinterpret_cast<const int32_t*>(static_cast<const char*>(workspace) +
                                           prefill_layout(plan->num_tiles, shape->batch).cu_off);
-  return rope_impl(shape, rope, p, shape->batch == 0 ? 0 : plan->total_q, dev_status, stream);
+  return rope_impl(shape, rope, p, shape->batch == 0 ? 0 : plan->total_q, plan->workspace_bytes, dev_status, stream);
 }
