@@ -13,6 +13,7 @@ constexpr uint32_t kDiffMagic = 0x46444150u;  // "PADF", header word 0 of a one-
 // A pair of KV heads as the planner sees it: one KV head with 2G rows (both
 // queries of its G heads) and values of 2D dims.
 constexpr int kDiffWarps = 4;          // warps sharing one task's pages
+static_assert(kDiffWarps == kWarpsPerCta, "the planner deals short tasks to as many warps of a CTA");
 // Up to this many splits the last task of a pair joins them in the split kernel, which
 // saves a launch (6 splits of 16 pairs: 8.6 against 8.9 us); beyond it a kernel of
 // its own does (16 splits: 35.6 against 36.3 us, 76 splits: 30.1 against 38.9 us).
