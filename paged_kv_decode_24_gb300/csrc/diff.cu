@@ -3,10 +3,10 @@
 #include <stdlib.h>
 #include <string.h>
 
-#include <atomic>
 #include <new>
 
 #include "diff.h"
+#include "latent_launch.cuh"
 #include "latent_params.h"
 
 namespace pa {
@@ -18,19 +18,6 @@ cudaError_t launch_diff_decode(const DiffDecodeParams& p, int head_dim, int grou
 }
 
 namespace {
-
-// SMs of the current device, read once per device (0: unknown).
-int sm_count() {
-  static std::atomic<int> sms[64];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess) {
-    n = sms[dev & 63].load(std::memory_order_relaxed);
-    if (n <= 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
-      sms[dev & 63].store(n, std::memory_order_relaxed);
-  }
-  (void)cudaGetLastError();
-  return n > 0 ? n : 0;
-}
 
 bool aligned(const void* p, uintptr_t a) { return p && ((uintptr_t)p % a) == 0; }
 

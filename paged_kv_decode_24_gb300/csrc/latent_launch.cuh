@@ -1,4 +1,5 @@
-// Host-side launch of the latent attention kernels.
+// Host-side launch of the latent attention, rotary append and differential
+// attention kernels.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -6,6 +7,19 @@
 #include <atomic>
 
 namespace pa {
+
+// SMs of the current device, read once per device (0: unknown).
+inline int sm_count() {
+  static std::atomic<int> sms[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess) {
+    n = sms[dev & 63].load(std::memory_order_relaxed);
+    if (n <= 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+      sms[dev & 63].store(n, std::memory_order_relaxed);
+  }
+  (void)cudaGetLastError();
+  return n > 0 ? n : 0;
+}
 
 // Launch kern(args...) on `grid` CTAs of `threads` threads with `smem` bytes
 // of dynamic shared memory, allowing programmatic dependent launch after the

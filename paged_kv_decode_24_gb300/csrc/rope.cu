@@ -268,7 +268,8 @@ cudaError_t launch_rope(RopeParams& p, int head_dim, int dtype, int kv_kind, cud
   const int groups = (total + rows - 1) / rows;
   // A warp takes as many of its token's row groups as leave every SM 32 warps.
   const int64_t warps = (int64_t)p.rows * groups;
-  int64_t turns = warps / (152 * 32);
+  const int sms = sm_count();
+  int64_t turns = warps / ((sms > 0 ? sms : 1) * 32);
   turns = turns < 1 ? 1 : turns > groups ? groups : turns;
   p.turns = (int)turns;
   p.parts = (groups + p.turns - 1) / p.turns;
