@@ -194,6 +194,52 @@ def test_prefill_limits_one_wait_and_not_a_pass(dim, group):
     assert torch.equal(got, want)
 
 
+def cold():
+    """Nothing of what a call reads is left in L2."""
+    torch.empty(512 << 20, dtype=torch.uint8, device="cuda").fill_(1)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("splits", [0, 3])
+def test_decode_gives_up_at_a_limit_below_any_copy(dim, splits):
+    """As many pages as keep memory busy, so that copies are waited for."""
+    c = Case([3000] * 40, pairs=2, group=4, dim=dim, dtype="bf16", seed=7)
+    d = Device(c).make_plan(forced_splits=splits)
+    want = d.decode()
+    assert d.done() == 0
+    plan, ws = d.plan, d.ws
+    d.make_plan(forced_splits=splits, wait_limit_ns=1)
+    cold()
+    got = d.decode()
+    assert d.done() == binding.PA_DEV_TIMEOUT
+    written = ~torch.isnan(got).all(-1)
+    assert not bool(written.all()) and torch.equal(got[written], want[written])
+    d.status.zero_()
+    d.plan, d.ws = plan, ws
+    assert torch.equal(d.decode(), want) and d.done() == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prefill_gives_up_at_a_limit_below_any_copy(dim):
+    c = Case([1500, 40, 700], [400, 40, 1], pairs=2, group=2, dim=dim, dtype="bf16", seed=7)
+    d = Device(c).make_prefill_plan()
+    want = d.prefill()
+    assert d.done() == 0
+    plan = d.plan
+    d.make_prefill_plan(wait_limit_ns=1)
+    cold()
+    got = d.prefill()
+    assert d.done() == binding.PA_DEV_TIMEOUT
+    missing = torch.isnan(got)
+    assert bool(missing.any()) and torch.equal(missing.any(-1), missing.all(-1))
+    assert torch.equal(got[~missing], want[~missing])
+    d.status.zero_()
+    d.plan = plan
+    binding.prefill_upload(plan, d.ws)
+    assert torch.equal(d.prefill(), want) and d.done() == 0
+
+
 # --------------------------------------------------------------------------
 # exact scores: bounds that a wrong weight does not pass (tests/test_diff_bounds.py)
 
