@@ -14,14 +14,17 @@ constexpr uint32_t kDiffMagic = 0x46444150u;  // "PADF", header word 0 of a one-
 // queries of its G heads) and values of 2D dims.
 constexpr int kDiffWarps = 4;          // warps sharing one task's pages
 static_assert(kDiffWarps == kWarpsPerCta, "the planner deals short tasks to as many warps of a CTA");
-// Up to this many splits the last task of a pair joins them in the split kernel, which
-// saves a launch (6 splits of 16 pairs: 8.6 against 8.9 us); beyond it a kernel of
-// its own does (16 splits: 35.6 against 36.3 us, 76 splits: 30.1 against 38.9 us).
+// Up to this many splits the last task of a pair joins them in the split kernel, beyond
+// it a kernel of its own does.  The former is the shorter of many groups (40 sequences
+// of 3 splits, 4 pairs: 17.3 against 22.1 us; 10 of 4: 14.6 against 17.2) and few splits
+// (one sequence, 16 pairs, 2 splits: 11.3 against 11.8; 4: 12.2 both), the latter of single
+// sequences with more (8: 13.4 against 12.2; 4 pairs, 76: 38.6 against 27.6).
 constexpr int kDiffMergeSplits = 8;
 // Automatic plans cut no split shorter than this many pages: 384 KB where the
 // (sequence, pair)s alone give each SM a task (batch of 48 short sequences, 16 pairs:
-// 21.2 us, cut at half of that 23.7), two pages a warp where they do not (4096
-// tokens, 4 pairs: 11.3 us; 14.1 with four pages, 12.4 with one).
+// 17.8 us, cut at half of that 21.2), two pages a warp where they do not (4096
+// tokens, 4 pairs: 10.3 us; 13.1 with four pages, 11.1 with one; 1000 tokens: 10.5, 11.7
+// and 9.0).
 constexpr int kDiffShortChunkPages = 8;
 PA_HD constexpr int diff_min_chunk(int head_dim) { return head_dim == 64 ? 48 : 24; }
 // Page tiles of a warp in flight (K or V of one page and pair: 64 D bytes), and
@@ -29,8 +32,8 @@ PA_HD constexpr int diff_min_chunk(int head_dim) { return head_dim == 64 ? 48 : 
 constexpr int kDiffStages = 3;
 PA_HD constexpr int diff_ctas_per_sm(int head_dim) { return head_dim == 64 ? 4 : 2; }
 // Pages of each warp of the first CTAs that L2 is asked for while the kernel ahead
-// still runs (one: long context 28.6 us, batch of 48 short ones 19.4; none: 30.1 and
-// 21.2; two: 29.5 and 20.3).
+// still runs (one: long context 27.6 us, batch of 48 short ones 18.2; none: 29.1 and
+// 20.6; two: 27.0 and 18.3).
 constexpr int kDiffPrefetchPages = 1;
 
 // What turns the two maps of a head into its output.

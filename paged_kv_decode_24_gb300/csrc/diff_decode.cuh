@@ -24,9 +24,11 @@
 //    product for both maps.  With G = 8 each map has a column tile.
 //
 // Measured: 160 sequences of 128 to 2048 tokens, 32 query heads over 8 KV heads of 128
-// (718 MB), 103 us, the measured copy bandwidth, with 722 MB of DRAM traffic; 48
-// of 5 to 563, 32 over 32 of 64 (111 MB), 19.2 us, 85 %; one of 32,768 (134 MB),
-// 28.3 us: 22.8 in this kernel (87 %), the rest in the join of 76 splits.
+// (718 MB), 103 to 104 us, the measured copy bandwidth, with DRAM traffic within 1 % of
+// the bytes; 48 of 5 to 563, 32 over 32 of 64 (111 MB), 18.9 us, 87 %; one of 32,768 (134 MB),
+// 28.5 us: about 23 in this kernel (87 %), the rest in the join of 76 splits.
+// Registers: 221 with head_dim 128 and G up to 4, 255 with G = 8; 128 and less with
+// head_dim 64 (G = 8 spills 68 bytes).
 #pragma once
 
 #include <type_traits>

@@ -9,7 +9,8 @@
 // splits of four heads of 128 are 620 KB through one SM.  Here a CTA joins one head,
 // its threads a sixteenth of the splits each: sixteen lanes of splits by VD / 4 groups
 // of four dims.  Bound by a launch, and by three dependent reads (plan, sums, values):
-// 5.8 us of the 28.3 of a context of 32,768 tokens (76 splits of 4 pairs of 128).
+// 5 to 6 us of the 28.5 of a context of 32,768 tokens (76 splits of 4 pairs of 128).  64
+// registers a thread, all of an SM's: none of its CTAs starts beside the split kernel's.
 #include <math.h>
 
 #include <atomic>

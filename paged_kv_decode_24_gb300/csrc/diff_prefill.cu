@@ -42,11 +42,15 @@
 // hold anything) become zeros before P V reads them.  Every wait is bounded; a
 // CTA that gave up writes nothing.
 //
-// Measured: a prompt of 8192 tokens with 32 query heads of 128 (16 heads), 762 us, 1080
-// TFLOP/s of the formula's operations (12 D a visible pair; the second parts of the
-// weights are 4 D more: 1440 TFLOP/s with them, of the 1705 that a library product
-// reaches under the power cap).  4100 tokens, 32 query heads of 64: 152 us, 679 TFLOP/s.  Weights rounded
-// once took 620 and 143 us.
+// Measured: a prompt of 8192 tokens with 32 query heads of 128 (16 heads), 762 to 780 us,
+// 1070 TFLOP/s of the formula's operations (12 D a visible pair), 1430 with those of the
+// weights' second parts (4 D more), of the 1705 that a library product reaches under the
+// power cap; the tensor cores and the thread that feeds them bound it, in pass 2 with
+// 64-token score tiles that read q from shared memory at two thirds of their rate.  4100
+// tokens, 32 query heads of 64: 151 us, 684 TFLOP/s (912): neither the tensor cores (42 % of
+// the clocks) nor the exponentials (40 %, each taken twice), but the waits and hand-overs
+// between them.  Weights rounded once took 620 and 143 us; the steps' figures below were
+// taken with those.
 #include <math.h>
 
 #include "diff.h"
