@@ -891,7 +891,8 @@ pa_status_t pa_diff_attention(const pa_shape_t* shape, const pa_diff_plan_t* pla
 /* The same of several new tokens of each sequence, causal: T rows packed as in
  * pa_prefill_attention, whose plan it takes (in the workspace; rows_per_tile
  * has to be 128).  q: [T][Hq][D], out: [T][H][2D].  Scores, statistics and
- * accumulation are fp32; weights keep about twice the element type's bits.
+ * accumulation are fp32; weights keep about twice the element type's bits (fp16:
+ * those below 2^-17 of their row's whole weight are kept to 2^-39 of it).
  * Tokens of a page whose index is out of range are left out (PA_DEV_BAD_PAGE);
  * a row left without any token gets zeros.  Weights of later tokens of the
  * sequence are 0, but their products are formed: queries and the rows of a

@@ -44,8 +44,9 @@ __global__ void __launch_bounds__(2 * D / 4 * kLanes) diff_merge_kernel(const __
   const int ns = grp.z, off = grp.w, R = 2 * group_size;
   // (The split kernel's own checks of the plan: where it refuses one, nothing is joined.)
   if (hdr.x != (int)kDiffMagic || hdr.y != p.num_items || hdr.z != p.num_groups || hdr.w != p.num_split_items ||
-      hdr_ctas.x != p.num_ctas || hdr_ctas.y != p.num_shared || gi >= p.num_groups || ns < 1 || ns > kMaxSplits || off < 0 || off + ns > p.num_split_items || grp.x < 0 ||
-      grp.x >= p.batch || grp.y < 0 || grp.y >= p.num_kv_heads) {
+      hdr_ctas.x != p.num_ctas || hdr_ctas.y != p.num_shared || gi >= p.num_groups || ns < 1 ||
+      ns > kMaxSplits || off < 0 || off + ns > p.num_split_items || grp.x < 0 || grp.x >= p.batch || grp.y < 0 ||
+      grp.y >= p.num_kv_heads) {
     if (threadIdx.x == 0) set_status(p.status, PA_DEV_PLAN_MISMATCH);
     return;
   }
